@@ -83,6 +83,12 @@ enum {
                                          whose largest code leaves fp16's range (scale >
                                          65504 / 127 for int8, > 65504 / 448 for fp8): the
                                          outputs that attend it are not finite            */
+    PA_FLAG_TREE_PARENT = 256,        /* pa_draft.h: a row's parent is neither -1 nor below the
+                                         row: its sequence is left out                     */
+    PA_FLAG_TOKEN_OUT_OF_RANGE = 512, /* pa_verify_tree: a drafted token outside [0, V): it is
+                                         never accepted                                    */
+    PA_FLAG_PROBABILITY = 1024,       /* pa_verify_tree: a row of probabilities to draw from
+                                         has no finite, positive sum: token -1             */
     PA_FLAG_WORKSPACE_SHORT = 128     /* pa_multi_token_attention, 8-bit cache, prefill-
                                          shaped call: the workspace's dequantised pool could
                                          not hold every attended block; the blocks beyond

@@ -31,12 +31,19 @@ PA_FLAG_QUERY_OUT_OF_RANGE = 16
 PA_FLAG_TIMEOUT = 32
 PA_FLAG_FP16_RANGE = 64
 PA_FLAG_WORKSPACE_SHORT = 128
+PA_FLAG_TREE_PARENT = 256
+PA_FLAG_TOKEN_OUT_OF_RANGE = 512
+PA_FLAG_PROBABILITY = 1024
+PA_TREE_MAX_NODES = 256
+PA_PROB_F32, PA_PROB_BF16 = 0, 1
+PA_ROTARY_PLAIN, PA_ROTARY_LINEAR, PA_ROTARY_BASE, PA_ROTARY_RAMP, PA_ROTARY_WAVELENGTH = range(5)
 
 EXPORTED = ["pa_version", "pa_status_string", "pa_last_error_string", "pa_reshape_and_cache",
             "pa_quantize_kv", "pa_quantize_kv_fp8", "pa_copy_blocks", "pa_decode_workspace_size", "pa_decode",
             "pa_decode_noalloc", "pa_decode_shared_prefix_workspace_size", "pa_decode_shared_prefix",
             "pa_multi_token_workspace_size", "pa_multi_token_workspace_size_for_tokens",
-            "pa_multi_token_attention"]
+            "pa_multi_token_attention", "pa_rotary_frequencies", "pa_rotary_table", "pa_rotary_and_cache",
+            "pa_tree_workspace_size", "pa_tree_attention", "pa_verify_tree"]
 PA_NOALLOC_SCRATCH_BYTES = 16 << 20
 
 
@@ -95,6 +102,22 @@ def load_library(path: Path | str | None = None) -> ctypes.CDLL:
                                              i32, i32, i32, i32, i32, i32, f32, i32, i32, vp, sz,
                                              vp, vp]
     lib.pa_multi_token_attention.restype = i32
+    f64 = ctypes.c_double
+    lib.pa_rotary_frequencies.argtypes = [i32, f64, i32, f64, f64, f64, f64, vp, vp]
+    lib.pa_rotary_frequencies.restype = i32
+    lib.pa_rotary_table.argtypes = [vp, i32, vp]
+    lib.pa_rotary_table.restype = i32
+    lib.pa_rotary_and_cache.argtypes = [vp, vp, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, i32, vp, vp, vp,
+                                        i32, i32, f32, i32, i32, i32, i32, i32, i32, vp, vp]
+    lib.pa_rotary_and_cache.restype = i32
+    lib.pa_tree_workspace_size.argtypes = [i32] * 9
+    lib.pa_tree_workspace_size.restype = sz
+    lib.pa_tree_attention.argtypes = [vp, vp, vp, i64, vp, i64, vp, vp, vp, vp, i32, vp, i32, vp, vp, vp,
+                                      i32, i32, i32, i32, i32, i32, i32, f32, i32, i32, vp, sz, vp, vp]
+    lib.pa_tree_attention.restype = i32
+    lib.pa_verify_tree.argtypes = [vp, vp, vp, vp, vp, vp, i64, vp, i64, i32, vp, vp, vp, vp, i32, i32, i32,
+                                   i32, vp, i32, vp, i32, i32, vp, vp]
+    lib.pa_verify_tree.restype = i32
     if path is None:
         _LIB = lib
     return lib
@@ -437,6 +460,230 @@ def decode_workspace(query, k_cache, max_context_len: int) -> torch.Tensor | Non
     if n == 0:
         return None
     return torch.empty(n, dtype=torch.uint8, device=query.device)
+
+
+# ------------------------------------------------- speculative decoding (include/pa_draft.h)
+def _heads(t, name: str) -> int:
+    """Check a [T][heads][D] bf16 CUDA tensor with dense heads; its token stride in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on a CUDA device")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name}: expected 3 dimensions, got {t.dim()}")
+    T, heads, D = t.shape
+    by_token, by_head, by_element = t.stride()
+    if (D > 1 and by_element != 1) or (heads > 1 and by_head != D):
+        raise ValueError(f"{name}: the heads of a token must be dense")
+    return by_token if T > 1 else heads * D
+
+
+def _one_device(*tensors) -> torch.device:
+    """The device all tensors live on."""
+    index = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            raise ValueError("all tensors must live on one CUDA device")
+    return tensors[0].device
+
+
+def _call(function, device, stream, *args) -> None:
+    """Call a library function with `device` current and the stream as its last argument."""
+    if torch.cuda.current_device() == device.index:
+        _check(function(*args, _stream(stream, device)))
+    else:
+        with torch.cuda.device(device):
+            _check(function(*args, _stream(stream, device)))
+
+
+def pa_rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: int = PA_ROTARY_PLAIN, factor: float = 1.0,
+                          original_context: float = 0.0, p0: float = 0.0, p1: float = 0.0):
+    """(inv_freq [rot_dim / 2] float64 on the host, attention_factor) of a scaling rule."""
+    inv = torch.empty(max(int(rot_dim), 0) // 2, dtype=torch.float64)
+    attention = ctypes.c_double(1.0)
+    _check(load_library().pa_rotary_frequencies(int(rot_dim), float(base), int(scaling), float(factor),
+                                                float(original_context), float(p0), float(p1), inv.data_ptr(),
+                                                ctypes.byref(attention)))
+    return inv, attention.value
+
+
+def pa_rotary_table(inv_freq, device=None) -> torch.Tensor:
+    """The 64-bit table of host frequencies (radians per position), as int64 bit patterns on
+    `device`."""
+    inv = torch.as_tensor(inv_freq, dtype=torch.float64, device="cpu").contiguous()
+    if inv.dim() != 1:
+        raise ValueError("inv_freq: expected 1 dimension")
+    table = torch.empty(inv.shape[0], dtype=torch.int64)
+    _check(load_library().pa_rotary_table(inv.data_ptr(), inv.shape[0], table.data_ptr()))
+    return table if device is None else table.to(device)
+
+
+def pa_rotary_and_cache(query_out, query, key, positions, table, interleaved: bool = False,
+                        attention_factor: float = 1.0, key_out=None, value=None, k_cache=None, v_cache=None,
+                        slot_mapping=None, k_scale=None, v_scale=None, err_flag=None, stream=None) -> None:
+    """Rotate query [T][Hq][D] and key [T][Hkv][D] to positions [T] (int64), the first
+    2 * len(table) elements of each head; write query_out, key_out if given, and append the
+    rotated keys and the values if a cache is given.  query, key and value may be slices of
+    one tensor (dense heads, any token stride that is a multiple of 8)."""
+    q_stride, k_stride = _heads(query, "query"), _heads(key, "key")
+    T, Hq, D = query.shape
+    Hkv = key.shape[1]
+    _cuda(query_out, "query_out", torch.bfloat16, 3)
+    _cuda(positions, "positions", torch.int64, 1)
+    _cuda(table, "table", torch.int64, 1)
+    if query_out.shape != query.shape or key.shape[0] != T or key.shape[2] != D or positions.shape[0] != T:
+        raise ValueError("pa_rotary_and_cache: shape mismatch")
+    if key_out is not None:
+        _cuda(key_out, "key_out", torch.bfloat16, 3)
+        if key_out.shape != key.shape:
+            raise ValueError("pa_rotary_and_cache: shape mismatch")
+    v_stride, kv_dtype, bs, N = 0, PA_KV_BF16, 16, 1
+    if k_cache is not None or v_cache is not None:
+        if k_cache is None or v_cache is None or value is None or slot_mapping is None:
+            raise ValueError("appending needs k_cache, v_cache, value and slot_mapping")
+        v_stride, kv_dtype = _heads(value, "value"), kv_dtype_of(k_cache)
+        _cuda(k_cache, "k_cache", k_cache.dtype, 4)
+        _cuda(v_cache, "v_cache", k_cache.dtype, 4)
+        _cuda(slot_mapping, "slot_mapping", torch.int64, 1)
+        N, heads, bs, D2 = k_cache.shape
+        if value.shape != key.shape or v_cache.shape != k_cache.shape or heads != Hkv or D2 != D \
+                or slot_mapping.shape[0] != T:
+            raise ValueError("pa_rotary_and_cache: shape mismatch")
+        if kv_dtype != PA_KV_BF16:
+            if k_scale is None or v_scale is None:
+                raise ValueError("an int8 or fp8 cache needs k_scale and v_scale")
+            _cuda(k_scale, "k_scale", torch.float32, 3)
+            _cuda(v_scale, "v_scale", torch.float32, 3)
+            if tuple(k_scale.shape) != (N, Hkv, bs) or v_scale.shape != k_scale.shape:
+                raise ValueError("pa_rotary_and_cache: scale shapes")
+        else:
+            k_scale = v_scale = None
+    else:
+        value = slot_mapping = k_scale = v_scale = None
+    device = _one_device(query, query_out, key, key_out, positions, table, value, k_cache, v_cache, slot_mapping,
+                         k_scale, v_scale, err_flag)
+    _call(load_library().pa_rotary_and_cache, device, stream, _ptr(query_out), _ptr(key_out), _ptr(query), q_stride,
+          _ptr(key), k_stride, _ptr(value), v_stride, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+          kv_dtype, _ptr(slot_mapping), _ptr(positions), _ptr(table), 2 * table.shape[0], int(interleaved),
+          float(attention_factor), T, Hq, Hkv, D, bs, N, _flag(err_flag))
+
+
+def pa_tree_workspace_size(S: int, T: int, Hq: int, Hkv: int, D: int, bs: int, kv_dtype: int,
+                           max_context_len: int, max_query_len: int) -> int:
+    return int(load_library().pa_tree_workspace_size(S, T, Hq, Hkv, D, bs, kv_dtype, max_context_len,
+                                                     max_query_len))
+
+
+def pa_tree_attention(out, query, key, value, k_cache, v_cache, block_tables, context_lens, query_start, parents,
+                      scale: float, max_context_len: int, max_query_len: int, workspace=None, k_scale=None,
+                      v_scale=None, err_flag=None, stream=None) -> None:
+    """Rows of drafted tokens attend their sequence's cached context and, among the rows
+    (key/value [T][Hkv][D] beside the cache), themselves and their ancestors.  workspace
+    defaults to a fresh allocation."""
+    _cuda(out, "out", torch.bfloat16, 3)
+    _cuda(query, "query", torch.bfloat16, 3)
+    k_stride, v_stride = _heads(key, "key"), _heads(value, "value")
+    kv_dtype = kv_dtype_of(k_cache)
+    _cuda(k_cache, "k_cache", k_cache.dtype, 4)
+    _cuda(v_cache, "v_cache", k_cache.dtype, 4)
+    _cuda(block_tables, "block_tables", torch.int32, 2)
+    _cuda(context_lens, "context_lens", torch.int32, 1)
+    _cuda(query_start, "query_start", torch.int32, 1)
+    _cuda(parents, "parents", torch.int32, 1)
+    T, Hq, D = query.shape
+    N, Hkv, bs, D2 = k_cache.shape
+    S, M = block_tables.shape
+    if kv_dtype != PA_KV_BF16:
+        if k_scale is None or v_scale is None:
+            raise ValueError("an int8 or fp8 cache needs k_scale and v_scale")
+        _cuda(k_scale, "k_scale", torch.float32, 3)
+        _cuda(v_scale, "v_scale", torch.float32, 3)
+        if tuple(k_scale.shape) != (N, Hkv, bs) or v_scale.shape != k_scale.shape:
+            raise ValueError("pa_tree_attention: scale shapes")
+    else:
+        k_scale = v_scale = None
+    if out.shape != query.shape or tuple(key.shape) != (T, Hkv, D) or value.shape != key.shape \
+            or v_cache.shape != k_cache.shape or D2 != D or context_lens.shape[0] != S \
+            or query_start.shape[0] != S + 1 or parents.shape[0] != T:
+        raise ValueError("pa_tree_attention: shape mismatch")
+    if workspace is None:
+        n = pa_tree_workspace_size(S, T, Hq, Hkv, D, bs, kv_dtype, max_context_len, max_query_len)
+        workspace = torch.empty(n, dtype=torch.uint8, device=query.device) if n else None
+    ws_bytes = 0
+    if workspace is not None:
+        _cuda(workspace, "workspace", workspace.dtype)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    device = _one_device(query, out, key, value, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                         query_start, parents, workspace, err_flag)
+    _call(load_library().pa_tree_attention, device, stream, _ptr(out), _ptr(query), _ptr(key), k_stride, _ptr(value),
+          v_stride, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), kv_dtype, _ptr(block_tables), M,
+          _ptr(context_lens), _ptr(query_start), _ptr(parents), S, T, Hq, Hkv, D, bs, N, float(scale),
+          int(max_context_len), int(max_query_len), _ptr(workspace), ws_bytes, _flag(err_flag))
+
+
+def _probabilities(t, name: str, T: int, V: int, dtype: torch.dtype) -> int:
+    """Check [T][V] probabilities with dense rows; the row stride in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on a CUDA device")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if tuple(t.shape) != (T, V):
+        raise ValueError(f"{name}: expected shape {(T, V)}, got {tuple(t.shape)}")
+    if V > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the probabilities of a row must be dense")
+    return t.stride(0) if T > 1 else V
+
+
+def pa_verify_tree(tokens_out, path, n_out, draft_tokens, target_probs, query_start, parents, uniforms,
+                   final_uniforms, draft_probs=None, slot_mapping=None, block_tables=None, context_lens=None,
+                   block_size: int = 16, num_blocks: int = 0, err_flag=None, stream=None) -> None:
+    """Accept or reject drafted tokens against target_probs [T][V] (fp32 or bf16) with given
+    uniform numbers, draw each sequence's next token, and write the accepted branch: tokens_out
+    and path [S][max_query_len], n_out [S], and (with block_tables, context_lens, block_size
+    and num_blocks) slot_mapping [T]."""
+    _cuda(tokens_out, "tokens_out", torch.int32, 2)
+    _cuda(path, "path", torch.int32, 2)
+    _cuda(n_out, "n_out", torch.int32, 1)
+    _cuda(draft_tokens, "draft_tokens", torch.int32, 1)
+    _cuda(query_start, "query_start", torch.int32, 1)
+    _cuda(parents, "parents", torch.int32, 1)
+    _cuda(uniforms, "uniforms", torch.float32, 1)
+    _cuda(final_uniforms, "final_uniforms", torch.float32, 1)
+    T, S = draft_tokens.shape[0], n_out.shape[0]
+    if target_probs.dim() != 2:
+        raise ValueError("target_probs: expected 2 dimensions")
+    if target_probs.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("target_probs: expected float32 or bfloat16")
+    V = target_probs.shape[1]
+    p_stride = _probabilities(target_probs, "target_probs", T, V, target_probs.dtype)
+    q_stride = 0 if draft_probs is None else _probabilities(draft_probs, "draft_probs", T, V, target_probs.dtype)
+    W = tokens_out.shape[1]
+    if tokens_out.shape[0] != S or path.shape != tokens_out.shape or query_start.shape[0] != S + 1 \
+            or parents.shape[0] != T or uniforms.shape[0] != T or final_uniforms.shape[0] != S:
+        raise ValueError("pa_verify_tree: shape mismatch")
+    M = 0
+    if slot_mapping is not None:
+        if block_tables is None or context_lens is None:
+            raise ValueError("slot_mapping needs block_tables and context_lens")
+        _cuda(slot_mapping, "slot_mapping", torch.int64, 1)
+        _cuda(block_tables, "block_tables", torch.int32, 2)
+        _cuda(context_lens, "context_lens", torch.int32, 1)
+        if slot_mapping.shape[0] != T or block_tables.shape[0] != S or context_lens.shape[0] != S:
+            raise ValueError("pa_verify_tree: shape mismatch")
+        M = block_tables.shape[1]
+    else:
+        block_tables = context_lens = None
+    device = _one_device(target_probs, draft_probs, tokens_out, path, n_out, slot_mapping, draft_tokens, query_start,
+                         parents, uniforms, final_uniforms, block_tables, context_lens, err_flag)
+    _call(load_library().pa_verify_tree, device, stream, _ptr(tokens_out), _ptr(path), _ptr(n_out), _ptr(slot_mapping),
+          _ptr(draft_tokens), _ptr(target_probs), p_stride, _ptr(draft_probs), q_stride,
+          PA_PROB_F32 if target_probs.dtype == torch.float32 else PA_PROB_BF16, _ptr(query_start), _ptr(parents),
+          _ptr(uniforms), _ptr(final_uniforms), S, T, V, W, _ptr(block_tables), M, _ptr(context_lens),
+          int(block_size), int(num_blocks), _flag(err_flag))
 
 
 # ------------------------------------------------------------------ block manager

@@ -28,9 +28,7 @@ pa_status check_launch(const char *what) {
     return PA_OK;
 }
 
-static bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-static size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+void clear_error() { g_last_error[0] = 0; }
 
 // Split of long contexts: each CTA handles one partition of one (sequence, kv head,
 // query-head chunk) unit.  A CTA pays a pipeline ramp-up (its first tiles' latency,
@@ -48,7 +46,7 @@ constexpr int kRampTokens = 64;
 constexpr double kSingleRampTokens = 512.0;  // the single-buffered kernel's (see plan_decode)
 constexpr int kCtasPerSm = 2;
 
-static int device_sms() {
+int device_sms() {
     static int cached[64] = {0};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
@@ -138,6 +136,39 @@ DecodePlan plan_decode(int S, int Hq, int Hkv, int D, int bs, int kv_dtype, int 
     return p;
 }
 
+pa_status check_cache_shape(const char *fn, int Hkv, int D, int bs, int N) {
+    if (Hkv <= 0 || N <= 0)
+        return fail(PA_ERR_INVALID_ARG, "%s: Hkv (%d) and N (%d) must be positive", fn, Hkv, N);
+    if (D != 64 && D != 128)
+        return fail(PA_ERR_UNSUPPORTED, "%s: head_dim %d not supported (64 or 128)", fn, D);
+    if (bs != 16 && bs != 32)
+        return fail(PA_ERR_UNSUPPORTED, "%s: block size %d not supported (16 or 32)", fn, bs);
+    if ((int64_t)N * bs > (int64_t)1 << 40)
+        return fail(PA_ERR_INVALID_ARG, "%s: pool too large", fn);
+    return PA_OK;
+}
+
+pa_status check_decode_shape(const char *fn, int S, int Hq, int Hkv, int D, int bs,
+                                    int kv_dtype, int max_context_len) {
+    if (S < 0 || Hq <= 0 || Hkv <= 0)
+        return fail(PA_ERR_INVALID_ARG, "%s: S = %d, Hq = %d, Hkv = %d", fn, S, Hq, Hkv);
+    if (Hq % Hkv != 0)
+        return fail(PA_ERR_INVALID_ARG, "%s: Hq (%d) must be a multiple of Hkv (%d)", fn, Hq, Hkv);
+    if (D != 64 && D != 128)
+        return fail(PA_ERR_UNSUPPORTED, "%s: head_dim %d not supported (64 or 128)", fn, D);
+    if (bs != 16 && bs != 32)
+        return fail(PA_ERR_UNSUPPORTED, "%s: block size %d not supported (16 or 32)", fn, bs);
+    if (kv_dtype != PA_KV_BF16 && kv_dtype != PA_KV_INT8 && kv_dtype != PA_KV_FP8)
+        return fail(PA_ERR_UNSUPPORTED, "%s: kv dtype %d not supported", fn, kv_dtype);
+    if (max_context_len < 0)
+        return fail(PA_ERR_INVALID_ARG, "%s: max_context_len = %d", fn, max_context_len);
+    if (S > 65535)
+        return fail(PA_ERR_UNSUPPORTED, "%s: at most 65535 sequences per call (got %d)", fn, S);
+    if ((int64_t)Hkv * ((Hq / Hkv + 7) / 8) > 65535)
+        return fail(PA_ERR_UNSUPPORTED, "%s: too many heads", fn);
+    return PA_OK;
+}
+
 }  // namespace pa
 
 using namespace pa;
@@ -159,18 +190,6 @@ const char *pa_status_string(pa_status status) {
 }
 
 const char *pa_last_error_string(void) { return g_last_error; }
-
-static pa_status check_cache_shape(const char *fn, int Hkv, int D, int bs, int N) {
-    if (Hkv <= 0 || N <= 0)
-        return fail(PA_ERR_INVALID_ARG, "%s: Hkv (%d) and N (%d) must be positive", fn, Hkv, N);
-    if (D != 64 && D != 128)
-        return fail(PA_ERR_UNSUPPORTED, "%s: head_dim %d not supported (64 or 128)", fn, D);
-    if (bs != 16 && bs != 32)
-        return fail(PA_ERR_UNSUPPORTED, "%s: block size %d not supported (16 or 32)", fn, bs);
-    if ((int64_t)N * bs > (int64_t)1 << 40)
-        return fail(PA_ERR_INVALID_ARG, "%s: pool too large", fn);
-    return PA_OK;
-}
 
 pa_status pa_reshape_and_cache(const pa_bf16 *key, const pa_bf16 *value, pa_bf16 *k_cache,
                                pa_bf16 *v_cache, const int64_t *slot_mapping, int T, int Hkv,
@@ -273,27 +292,6 @@ pa_status pa_copy_blocks(void *k_cache, void *v_cache, float *k_scale, float *v_
     launch_copy_blocks(k_cache, v_cache, k_scale, v_scale, block_mapping, n, block_bytes,
                        scale_elems_per_block, (cudaStream_t)stream);
     return check_launch(fn);
-}
-
-static pa_status check_decode_shape(const char *fn, int S, int Hq, int Hkv, int D, int bs,
-                                    int kv_dtype, int max_context_len) {
-    if (S < 0 || Hq <= 0 || Hkv <= 0)
-        return fail(PA_ERR_INVALID_ARG, "%s: S = %d, Hq = %d, Hkv = %d", fn, S, Hq, Hkv);
-    if (Hq % Hkv != 0)
-        return fail(PA_ERR_INVALID_ARG, "%s: Hq (%d) must be a multiple of Hkv (%d)", fn, Hq, Hkv);
-    if (D != 64 && D != 128)
-        return fail(PA_ERR_UNSUPPORTED, "%s: head_dim %d not supported (64 or 128)", fn, D);
-    if (bs != 16 && bs != 32)
-        return fail(PA_ERR_UNSUPPORTED, "%s: block size %d not supported (16 or 32)", fn, bs);
-    if (kv_dtype != PA_KV_BF16 && kv_dtype != PA_KV_INT8 && kv_dtype != PA_KV_FP8)
-        return fail(PA_ERR_UNSUPPORTED, "%s: kv dtype %d not supported", fn, kv_dtype);
-    if (max_context_len < 0)
-        return fail(PA_ERR_INVALID_ARG, "%s: max_context_len = %d", fn, max_context_len);
-    if (S > 65535)
-        return fail(PA_ERR_UNSUPPORTED, "%s: at most 65535 sequences per call (got %d)", fn, S);
-    if ((int64_t)Hkv * ((Hq / Hkv + 7) / 8) > 65535)
-        return fail(PA_ERR_UNSUPPORTED, "%s: too many heads", fn);
-    return PA_OK;
 }
 
 size_t pa_decode_workspace_size(int S, int Hq, int Hkv, int D, int bs, int kv_dtype,

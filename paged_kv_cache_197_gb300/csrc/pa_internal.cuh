@@ -14,6 +14,14 @@ namespace pa {
 pa_status fail(pa_status status, const char *fmt, ...);
 // Turns the result of the launches just made into a status.
 pa_status check_launch(const char *what);
+void clear_error();  // at the start of a call
+// The checks of a cache's shape, and of decode-like arguments, that every entry point shares.
+pa_status check_cache_shape(const char *fn, int Hkv, int D, int bs, int N);
+pa_status check_decode_shape(const char *fn, int S, int Hq, int Hkv, int D, int bs, int kv_dtype,
+                             int max_context_len);
+inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+int device_sms();  // SMs of the current device (152 where there is none)
 
 // ------------------------------------------------------------- decode planning
 // Split of each sequence's context into partitions processed by separate CTAs
@@ -112,6 +120,9 @@ struct MultiArgs {
 
 int multi_cols_per_cta();
 cudaError_t launch_multi_token(const MultiArgs &a, int D, int bs, int kv_dtype, cudaStream_t stream);
+// The mma.sync kernel over the whole context for every column (no causal limit, contexts
+// apart from the new tokens): partials only, ceil(context / part_tokens) per column.
+cudaError_t launch_multi_context(const MultiArgs &a, int D, int bs, int kv_dtype, cudaStream_t stream);
 // The log-sum-exp merge of multi-token partials (a programmatic dependent launch).
 cudaError_t launch_multi_merge(const MultiArgs &a, int D, int bs, cudaStream_t stream);
 // Whether a multi-token call runs on the decode kernel in rows mode (a CTA per one or

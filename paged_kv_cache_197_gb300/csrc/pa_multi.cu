@@ -53,13 +53,14 @@ __device__ __forceinline__ void raise_flag(int *err_flag, int bit) {
 // The sequence's context, new-token count and first query row, checked: a context
 // outside [0, min(M * bs, max_context_len)] is clamped (CONTEXT flag); query offsets
 // outside [0, T], a negative count, more new tokens than context or than
-// max_query_len leave the sequence out (QUERY flag, its rows are not written).
+// max_query_len leave the sequence out (QUERY flag, its rows are not written).  ALL: the
+// new tokens are not part of the context, which may be shorter.
 struct SeqView {
     int ctx, L, row0, base;
     bool ok;
 };
 
-template <int BS>
+template <int BS, bool ALL = false>
 __device__ __forceinline__ SeqView seq_view(const MultiArgs &a, int s, bool report) {
     SeqView v;
     int ctx = a.context_lens[s];
@@ -72,7 +73,7 @@ __device__ __forceinline__ SeqView seq_view(const MultiArgs &a, int s, bool repo
     v.ctx = ctx;
     v.row0 = r0;
     v.L = r1 - r0;
-    v.ok = r0 >= 0 && r1 <= a.T && v.L >= 0 && v.L <= ctx && v.L <= a.max_query_len;
+    v.ok = r0 >= 0 && r1 <= a.T && v.L >= 0 && (ALL || v.L <= ctx) && v.L <= a.max_query_len;
     if (!v.ok && report) raise_flag(a.err_flag, PA_FLAG_QUERY_OUT_OF_RANGE);
     v.base = ctx - v.L;
     return v;
@@ -289,7 +290,9 @@ __device__ __forceinline__ void attend_tokens_q(float (&o)[D / 8][4], float (&m)
     }
 }
 
-template <typename KV, int D, int BS>
+// ALL (a tree of drafted tokens, whose own rows are joined later): every column sees the
+// whole context and leaves a partial.
+template <typename KV, int D, int BS, bool ALL>
 __global__ void __launch_bounds__(kThreads, 2) paged_multi_kernel(const __grid_constant__ MultiArgs a) {
     constexpr bool QUANT = sizeof(KV) == 1;  // int8 / fp8 cache: exact fp16 codes, fp32 scales, fp16 products
     constexpr int ROW = D * 2;          // bytes of one token row (bf16)
@@ -311,13 +314,15 @@ __global__ void __launch_bounds__(kThreads, 2) paged_multi_kernel(const __grid_c
     const int s = blockIdx.z;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, t = lane & 3;
 
-    const SeqView v = seq_view<BS>(a, s, part == 0 && blockIdx.y == 0 && tid == 0);
+    const SeqView v = seq_view<BS, ALL>(a, s, part == 0 && blockIdx.y == 0 && tid == 0);
     if (!v.ok) return;
+    // the last token column c sees
+    auto col_lim = [&](int c) { return ALL ? v.ctx - 1 : v.base + col_token(a, c); };
     const int ncols = v.L * a.G;
     const int col0 = cb * kColsPerCta;
     if (col0 >= ncols) return;
     // the CTA's last column sees the most tokens
-    const int cta_lim = v.base + col_token(a, min(ncols, col0 + kColsPerCta) - 1);  // inclusive
+    const int cta_lim = col_lim(min(ncols, col0 + kColsPerCta) - 1);  // inclusive
     const int tok_begin = part * a.part_tokens;
     const int tok_end = min(tok_begin + a.part_tokens, cta_lim + 1);
     if (tok_begin >= tok_end) return;
@@ -393,10 +398,10 @@ __global__ void __launch_bounds__(kThreads, 2) paged_multi_kernel(const __grid_c
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int c = wcol0 + gq + 8 * h;
-        lim[h] = (active && c < ncols) ? min(v.base + col_token(a, c), tok_end - 1) : -1;
+        lim[h] = (active && c < ncols) ? min(col_lim(c), tok_end - 1) : -1;
     }
-    const int warp_hi = (active && wcol0 < ncols) ? min(v.base + col_token(a, min(ncols, wcol0 + kColsPerWarp) - 1), tok_end - 1) : -1;
-    const int warp_lo = (active && wcol0 < ncols) ? min(v.base + col_token(a, wcol0), tok_end - 1) : -1;
+    const int warp_hi = (active && wcol0 < ncols) ? min(col_lim(min(ncols, wcol0 + kColsPerWarp) - 1), tok_end - 1) : -1;
+    const int warp_lo = (active && wcol0 < ncols) ? min(col_lim(wcol0), tok_end - 1) : -1;
     __syncthreads();  // s_blk
 
     // staging (bf16): thread tid always copies 16-byte piece pc of rows pr, pr + RPP, ...
@@ -593,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_multi_kernel(const __grid_c
         for (int cc = warp; cc < ncg * kColsPerWarp; cc += kWarps) {
             const int c = col0 + cc;
             if (c >= ncols) break;
-            const int lim_c = v.base + col_token(a, c);
+            const int lim_c = col_lim(c);
             if (tok_begin > lim_c) continue;  // this partition holds nothing the column sees
             const int g = cc / kColsPerWarp, r = cc % kColsPerWarp;
             float mv = -INFINITY;
@@ -612,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_multi_kernel(const __grid_c
                 for (int e = 0; e < PER; ++e) acc[e] += f * src[e];
             }
             const int64_t pair = (int64_t)(v.row0 + col_token(a, c)) * a.Hq + kvh * a.G + col_head(a, c);
-            if (lim_c < a.part_tokens) {
+            if (!ALL && lim_c < a.part_tokens) {
                 const float inv = lv > 0.f ? 1.f / lv : 0.f;
                 uint16_t *dst = a.out + pair * D + lane * PER;
                 if constexpr (PER == 4)
@@ -637,10 +642,10 @@ __global__ void __launch_bounds__(kThreads, 2) paged_multi_kernel(const __grid_c
     for (int h = 0; h < 2; ++h) {
         const int c = wcol0 + gq + 8 * h;
         if (c >= ncols) continue;
-        const int lim_c = v.base + col_token(a, c);
+        const int lim_c = col_lim(c);
         if (tok_begin > lim_c) continue;
         const int64_t pair = (int64_t)(v.row0 + col_token(a, c)) * a.Hq + kvh * a.G + col_head(a, c);
-        if (lim_c < a.part_tokens) {
+        if (!ALL && lim_c < a.part_tokens) {
             const float inv = l[h] > 0.f ? 1.f / l[h] : 0.f;
             uint16_t *dst = a.out + pair * D + 2 * t;
 #pragma unroll
@@ -719,22 +724,22 @@ __global__ void __launch_bounds__(128) merge_multi_kernel(const __grid_constant_
     for (int e = 0; e < PER; e += 2) *reinterpret_cast<uint32_t *>(dst + e) = bf16x2(acc[e] * inv, acc[e + 1] * inv);
 }
 
-template <typename KV, int D, int BS>
+template <typename KV, int D, int BS, bool ALL>
 cudaError_t launch_multi_typed(const MultiArgs &a, cudaStream_t stream) {
     constexpr int SMEM = sizeof(KV) == 1 ? multi_smem_bytes_q<D>() : multi_smem_bytes<D>();
     static std::atomic<bool> configured[64];  // per device: the shared-memory attribute is set
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!configured[dev].load(std::memory_order_acquire)) {
-        cudaError_t e = cudaFuncSetAttribute(paged_multi_kernel<KV, D, BS>,
+        cudaError_t e = cudaFuncSetAttribute(paged_multi_kernel<KV, D, BS, ALL>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
         if (e != cudaSuccess) return e;
         configured[dev].store(true, std::memory_order_release);
     }
     dim3 grid(a.max_parts, a.Hkv * a.CB, a.S);
-    paged_multi_kernel<KV, D, BS><<<grid, kThreads, SMEM, stream>>>(a);
+    paged_multi_kernel<KV, D, BS, ALL><<<grid, kThreads, SMEM, stream>>>(a);
     cudaError_t err = cudaGetLastError();
-    if (err != cudaSuccess || a.max_parts == 1) return err;
+    if (err != cudaSuccess || a.max_parts == 1 || ALL) return err;
     return launch_multi_merge(a, D, BS, stream);
 }
 
@@ -761,11 +766,18 @@ cudaError_t launch_multi_merge(const MultiArgs &a, int D, int bs, cudaStream_t s
     return bs == 16 ? launch_merge_typed<64, 16>(a, stream) : launch_merge_typed<64, 32>(a, stream);
 }
 
-template <typename KV>
+template <typename KV, bool ALL = false>
 cudaError_t launch_multi_kv(const MultiArgs &a, int D, int bs, cudaStream_t stream) {
     if (D == 128)
-        return bs == 16 ? launch_multi_typed<KV, 128, 16>(a, stream) : launch_multi_typed<KV, 128, 32>(a, stream);
-    return bs == 16 ? launch_multi_typed<KV, 64, 16>(a, stream) : launch_multi_typed<KV, 64, 32>(a, stream);
+        return bs == 16 ? launch_multi_typed<KV, 128, 16, ALL>(a, stream) : launch_multi_typed<KV, 128, 32, ALL>(a, stream);
+    return bs == 16 ? launch_multi_typed<KV, 64, 16, ALL>(a, stream) : launch_multi_typed<KV, 64, 32, ALL>(a, stream);
+}
+
+cudaError_t launch_multi_context(const MultiArgs &a, int D, int bs, int kv_dtype, cudaStream_t stream) {
+    if (!a.ws_acc || !a.ws_ml) return cudaErrorInvalidValue;
+    if (kv_dtype == PA_KV_INT8) return launch_multi_kv<int8_t, true>(a, D, bs, stream);
+    if (kv_dtype == PA_KV_FP8) return launch_multi_kv<e4m3_tag, true>(a, D, bs, stream);
+    return launch_multi_kv<uint16_t, true>(a, D, bs, stream);
 }
 
 bool multi_per_token_eligible(int D, int kv_dtype, int G, int max_query_len) {

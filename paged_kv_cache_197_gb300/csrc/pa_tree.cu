@@ -1,0 +1,266 @@
+// Attention of a tree of drafted tokens over the paged cache (pa_draft.h).
+//
+// Row i of a sequence attends all C cached tokens and, among its sequence's own rows, its
+// ancestors and itself.  With the keys split into those two sets, and (m, l, o) the
+// maximum, sum and weighted values of a set's softmax in the exp2 domain,
+//   out = (2^(m1 - m) o1 + 2^(m2 - m) o2) / (2^(m1 - m) l1 + 2^(m2 - m) l2),  m = max(m1, m2):
+// the context needs no mask at all and streams like a prompt every row shares, and the
+// tree's own rows, a few hundred at most, are joined afterwards.
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include <algorithm>
+
+#include "pa_draft.h"
+#include "pa_internal.cuh"
+#include "pa_mma.cuh"
+
+namespace pa {
+namespace {
+
+using tiled::bf16x2;
+using tiled::ex2;
+
+struct TreeArgs {
+    uint16_t *out;
+    const uint16_t *q, *k, *v;  // [T][Hq][D]; rows' own keys and values
+    int64_t k_stride, v_stride;
+    const int32_t *parents, *query_start, *context_lens;
+    const float *ws_acc, *ws_ml;  // [T][Hq][max_parts][D], [T][Hq][max_parts][2]
+    int *err_flag;
+    int S, T, Hq, Hkv, G, M, bs;
+    int part_tokens, max_parts;
+    int max_context_len, max_query_len;
+    float scale_log2;
+};
+
+// One warp per (row, query head): the tree's own part by walking up from the row, then the
+// context's partials.
+template <int D>
+__global__ void __launch_bounds__(128) tree_join_kernel(const __grid_constant__ TreeArgs a) {
+    constexpr int PER = D / 32;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31, s = blockIdx.y;
+    const int job = blockIdx.x * 4 + (threadIdx.x >> 5);
+    const int i = job / a.Hq, h = job % a.Hq;
+    const int r0 = a.query_start[s], r1 = a.query_start[s + 1], L = r1 - r0;
+    const bool lead = blockIdx.x == 0 && threadIdx.x == 0;
+    if (!(r0 >= 0 && r1 <= a.T && L >= 0 && L <= a.max_query_len)) {
+        if (lead && a.err_flag) atomicOr(a.err_flag, PA_FLAG_QUERY_OUT_OF_RANGE);
+        return;
+    }
+    bool bad = false;
+    for (int j = lane; j < L; j += 32) {
+        const int p = a.parents[r0 + j];
+        bad |= p < -1 || p >= j;
+    }
+    if (__any_sync(0xffffffffu, bad)) {
+        if (lead && a.err_flag) atomicOr(a.err_flag, PA_FLAG_TREE_PARENT);
+        return;
+    }
+    if (i >= L) return;
+    const int ctx = min(max(a.context_lens[s], 0), min(a.M * a.bs, a.max_context_len));
+    auto load = [&](const uint16_t *p, float (&x)[PER]) {
+#pragma unroll
+        for (int e = 0; e < PER; e += 2) {
+            const uint32_t w = *reinterpret_cast<const uint32_t *>(p + e);
+            x[e] = __uint_as_float(w << 16);
+            x[e + 1] = __uint_as_float(w & 0xffff0000u);
+        }
+    };
+    float q[PER], acc[PER], m = -INFINITY, l = 0.f;
+    load(a.q + ((int64_t)(r0 + i) * a.Hq + h) * D + lane * PER, q);
+#pragma unroll
+    for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+    const int kvh = h / a.G;
+    for (int at = i; at >= 0; at = a.parents[r0 + at]) {  // strictly decreasing: at most L steps
+        float k[PER], v[PER];
+        load(a.k + (int64_t)(r0 + at) * a.k_stride + kvh * D + lane * PER, k);
+        load(a.v + (int64_t)(r0 + at) * a.v_stride + kvh * D + lane * PER, v);
+        float x = 0.f;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) x = fmaf(q[e], k[e], x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        x *= a.scale_log2;
+        const float mn = fmaxf(m, x), base = mn == -INFINITY ? 0.f : mn;
+        const float f = ex2(m - base), w = ex2(x - base);
+        m = mn;
+        l = l * f + w;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, v[e], acc[e] * f);
+    }
+    const int nparts = (ctx + a.part_tokens - 1) / a.part_tokens;
+    const int64_t row = ((int64_t)(r0 + i) * a.Hq + h) * a.max_parts;
+    for (int p = 0; p < nparts; ++p) {
+        const float2 ml = *reinterpret_cast<const float2 *>(a.ws_ml + (row + p) * 2);
+        const float mn = fmaxf(m, ml.x), base = mn == -INFINITY ? 0.f : mn;
+        const float f = ex2(m - base), w = ex2(ml.x - base);
+        const float *src = a.ws_acc + (row + p) * D + lane * PER;
+        m = mn;
+        l = l * f + w * ml.y;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, src[e], acc[e] * f);
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    uint16_t *dst = a.out + ((int64_t)(r0 + i) * a.Hq + h) * D + lane * PER;
+#pragma unroll
+    for (int e = 0; e < PER; e += 2) *reinterpret_cast<uint32_t *>(dst + e) = bf16x2(acc[e] * inv, acc[e + 1] * inv);
+}
+
+// Partitions of the contexts and the workspace: as for the multi-token calls, n balanced
+// partitions of the longest context scored by (last-wave fill) x len / (len + 512), with at
+// least two waves of two CTAs per SM.
+struct TreePlan {
+    int CB, part_tokens, max_parts;
+    size_t ml_off, bytes;
+};
+
+TreePlan plan_tree(int S, int T, int Hq, int Hkv, int D, int max_context_len, int max_query_len) {
+    TreePlan p{};
+    const int G = Hq / Hkv, ctx = std::max(max_context_len, 1);
+    p.CB = std::max(1, (int)(((int64_t)max_query_len * G + multi_cols_per_cta() - 1) / multi_cols_per_cta()));
+    const double units = (double)S * Hkv * p.CB, slots = (double)device_sms() * 2;
+    p.part_tokens = 256;
+    double best = -1.0;
+    for (int n = 1; n <= (ctx + 255) / 256; ++n) {
+        const int cand = std::min(4096, std::max(256, (int)align_up((size_t)((ctx + n - 1) / n), 64)));
+        const int parts = (ctx + cand - 1) / cand;
+        if (parts != n) continue;
+        const double waves = units * parts / slots;
+        if (waves < 2.0 && cand != 256) continue;
+        const double len = (double)std::min(cand, ctx), score = waves / std::ceil(waves) * len / (len + 512.0);
+        if (score > best + 1e-9) {
+            best = score;
+            p.part_tokens = cand;
+        }
+    }
+    p.max_parts = (ctx + p.part_tokens - 1) / p.part_tokens;
+    const size_t rows = (size_t)T * Hq * p.max_parts;
+    p.ml_off = align_up(rows * D * sizeof(float), 256);
+    p.bytes = align_up(p.ml_off + rows * 2 * sizeof(float), 256);
+    return p;
+}
+
+pa_status check_tree_args(const char *fn, int S, int T, int Hq, int Hkv, int D, int bs, int kv_dtype,
+                          int max_context_len, int max_query_len) {
+    const pa_status st = check_decode_shape(fn, S, Hq, Hkv, D, bs, kv_dtype, max_context_len);
+    if (st != PA_OK) return st;
+    if (T < 0) return fail(PA_ERR_INVALID_ARG, "%s: T = %d", fn, T);
+    if (max_query_len < 1 || max_query_len > T || max_query_len > PA_TREE_MAX_NODES)
+        return fail(PA_ERR_INVALID_ARG, "%s: max_query_len = %d (1 .. min(T, %d))", fn, max_query_len, PA_TREE_MAX_NODES);
+    const int64_t cb = ((int64_t)max_query_len * (Hq / Hkv) + multi_cols_per_cta() - 1) / multi_cols_per_cta();
+    if ((int64_t)Hkv * cb > 65535) return fail(PA_ERR_UNSUPPORTED, "%s: too many rows and heads", fn);
+    return PA_OK;
+}
+
+}  // namespace
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" {
+
+size_t pa_tree_workspace_size(int S, int T, int Hq, int Hkv, int D, int bs, int kv_dtype, int max_context_len,
+                              int max_query_len) {
+    if (check_tree_args("pa_tree_workspace_size", S, T, Hq, Hkv, D, bs, kv_dtype, max_context_len, max_query_len) != PA_OK)
+        return 0;
+    return plan_tree(S, T, Hq, Hkv, D, max_context_len, max_query_len).bytes;
+}
+
+pa_status pa_tree_attention(pa_bf16 *out, const pa_bf16 *query, const pa_bf16 *key, int64_t key_stride,
+                            const pa_bf16 *value, int64_t value_stride, const void *k_cache, const void *v_cache,
+                            const float *k_scale, const float *v_scale, int kv_dtype, const int32_t *block_tables,
+                            int M, const int32_t *context_lens, const int32_t *query_start, const int32_t *parents,
+                            int S, int T, int Hq, int Hkv, int D, int bs, int N, float scale, int max_context_len,
+                            int max_query_len, void *workspace, size_t workspace_bytes, int *err_flag,
+                            void *stream) {
+    const char *fn = "pa_tree_attention";
+    clear_error();
+    if (S == 0 || T == 0) return PA_OK;
+    const pa_status st = check_tree_args(fn, S, T, Hq, Hkv, D, bs, kv_dtype, max_context_len, max_query_len);
+    if (st != PA_OK) return st;
+    if (N <= 0 || M <= 0) return fail(PA_ERR_INVALID_ARG, "%s: N = %d, M = %d must be positive", fn, N, M);
+    if ((int64_t)max_context_len > (int64_t)M * bs)
+        return fail(PA_ERR_OUT_OF_RANGE, "%s: max_context_len %d exceeds M * bs = %lld", fn, max_context_len,
+                    (long long)M * bs);
+    if (!out || !query || !key || !value || !k_cache || !v_cache || !block_tables || !context_lens || !query_start ||
+        !parents)
+        return fail(PA_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if (kv_dtype != PA_KV_BF16 && (!k_scale || !v_scale))
+        return fail(PA_ERR_INVALID_ARG, "%s: an int8 or fp8 cache needs k_scale and v_scale", fn);
+    if (!aligned16(out) || !aligned16(query) || !aligned16(key) || !aligned16(value) || !aligned16(k_cache) ||
+        !aligned16(v_cache) || (kv_dtype != PA_KV_BF16 && (!aligned16(k_scale) || !aligned16(v_scale))))
+        return fail(PA_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", fn);
+    const int64_t kw = (int64_t)Hkv * D;
+    constexpr int64_t kMost = (int64_t)1 << 36;
+    if (key_stride < kw || value_stride < kw || key_stride % 8 != 0 || value_stride % 8 != 0 || key_stride > kMost ||
+        value_stride > kMost)
+        return fail(PA_ERR_INVALID_ARG, "%s: row strides must be multiples of 8, at least heads * head_dim", fn);
+    if (!(scale == scale) || scale == __builtin_inff() || scale == -__builtin_inff())
+        return fail(PA_ERR_INVALID_ARG, "%s: scale must be finite", fn);
+    const TreePlan plan = plan_tree(S, T, Hq, Hkv, D, max_context_len, max_query_len);
+    if (!workspace || workspace_bytes < plan.bytes)
+        return fail(PA_ERR_INVALID_ARG, "%s: workspace of %zu bytes needed, %zu given", fn, plan.bytes,
+                    workspace ? workspace_bytes : (size_t)0);
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return fail(PA_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", fn);
+    MultiArgs c{};
+    c.out = out;
+    c.q = query;
+    c.k_cache = k_cache;
+    c.v_cache = v_cache;
+    c.k_scale = k_scale;
+    c.v_scale = v_scale;
+    c.block_tables = block_tables;
+    c.context_lens = context_lens;
+    c.query_start = query_start;
+    c.ws_acc = (float *)workspace;
+    c.ws_ml = (float *)((char *)workspace + plan.ml_off);
+    c.err_flag = err_flag;
+    c.M = M;
+    c.S = S;
+    c.T = T;
+    c.Hq = Hq;
+    c.Hkv = Hkv;
+    c.G = Hq / Hkv;
+    c.g_shift = (c.G & (c.G - 1)) == 0 ? __builtin_ctz((unsigned)c.G) : -1;
+    c.N = N;
+    c.CB = plan.CB;
+    c.part_tokens = plan.part_tokens;
+    c.max_parts = plan.max_parts;
+    c.max_context_len = max_context_len;
+    c.max_query_len = max_query_len;
+    c.scale_log2 = scale * 1.4426950408889634f;
+    launch_multi_context(c, D, bs, kv_dtype, (cudaStream_t)stream);
+    TreeArgs t{};
+    t.out = out;
+    t.q = query;
+    t.k = key;
+    t.v = value;
+    t.k_stride = key_stride;
+    t.v_stride = value_stride;
+    t.parents = parents;
+    t.query_start = query_start;
+    t.context_lens = context_lens;
+    t.ws_acc = c.ws_acc;
+    t.ws_ml = c.ws_ml;
+    t.err_flag = err_flag;
+    t.S = S;
+    t.T = T;
+    t.Hq = Hq;
+    t.Hkv = Hkv;
+    t.G = c.G;
+    t.M = M;
+    t.bs = bs;
+    t.part_tokens = plan.part_tokens;
+    t.max_parts = plan.max_parts;
+    t.max_context_len = max_context_len;
+    t.max_query_len = max_query_len;
+    t.scale_log2 = c.scale_log2;
+    const dim3 grid((unsigned)(((int64_t)max_query_len * Hq + 3) / 4), S);
+    launch_dependent(D == 128 ? tree_join_kernel<128> : tree_join_kernel<64>, grid, dim3(128), 0, (cudaStream_t)stream, t);
+    return check_launch(fn);
+}
+
+}  // extern "C"
