@@ -11,9 +11,8 @@
 
 #include <algorithm>
 
-#include "pa_draft.h"
-#include "pa_internal.cuh"
 #include "pa_mma.cuh"
+#include "pa_tree.cuh"
 
 namespace pa {
 namespace {
@@ -26,40 +25,68 @@ struct TreeArgs {
     const uint16_t *q, *k, *v;  // [T][Hq][D]; rows' own keys and values
     int64_t k_stride, v_stride;
     const int32_t *parents, *query_start, *context_lens;
-    const float *ws_acc, *ws_ml;  // [T][Hq][max_parts][D], [T][Hq][max_parts][2]
     int *err_flag;
-    int S, T, Hq, Hkv, G, M, bs;
-    int part_tokens, max_parts;
+    int S, T, Hq, Hkv, G;
+    int chunks;                 // ceil(G / 8): query heads a warp takes at once
     int max_context_len, max_query_len;
     float scale_log2;
+    // the context's partials: per partition of part_tokens tokens ...
+    const float *ws_acc, *ws_ml;  // [T][Hq][max_parts][D], [T][Hq][max_parts][2]
+    int part_tokens, max_parts;
+    // ... or, with tiles.prefix, as the tcgen05 kernel leaves them
+    TreeContext tiles;
 };
 
-// One warp per (row, query head): the tree's own part by walking up from the row, then the
-// context's partials.
-template <int D>
-__global__ void __launch_bounds__(128) tree_join_kernel(const __grid_constant__ TreeArgs a) {
-    constexpr int PER = D / 32;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int lane = threadIdx.x & 31, s = blockIdx.y;
-    const int job = blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int i = job / a.Hq, h = job % a.Hq;
-    const int r0 = a.query_start[s], r1 = a.query_start[s + 1], L = r1 - r0;
-    const bool lead = blockIdx.x == 0 && threadIdx.x == 0;
-    if (!(r0 >= 0 && r1 <= a.T && L >= 0 && L <= a.max_query_len)) {
-        if (lead && a.err_flag) atomicOr(a.err_flag, PA_FLAG_QUERY_OUT_OF_RANGE);
-        return;
+constexpr int kHeads = 8;
+constexpr int kJoinWarps = 4;
+
+// The sum over the warp of each of eight values, in every lane: three exchanges that halve
+// the values a lane carries, two that sum, and a broadcast (17 shuffles instead of 40).
+__device__ __forceinline__ void sum8(float (&x)[kHeads], int lane) {
+#pragma unroll
+    for (int o = 16, n = 4; n >= 1; o >>= 1, n >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const float give = up ? x[i] : x[i + n], keep = up ? x[i + n] : x[i];
+            x[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+        }
     }
+    float s = x[0];
+    s += __shfl_xor_sync(0xffffffffu, s, 2);
+    s += __shfl_xor_sync(0xffffffffu, s, 1);
+    // the lanes with (bit 16, bit 8, bit 4) = (h / 4, h / 2, h) hold value h
+#pragma unroll
+    for (int h = 0; h < kHeads; ++h)
+        x[h] = __shfl_sync(0xffffffffu, s, ((h >> 2) & 1) * 16 + ((h >> 1) & 1) * 8 + (h & 1) * 4);
+}
+
+// One warp per (row, kv head, up to eight of its query heads): the row's ancestors from the
+// row up, in fp32, then the context's partials.  Launched as a programmatic dependent: the
+// tree's own part, which the context's kernel does not touch, runs before the wait.
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const __grid_constant__ TreeArgs a) {
+    constexpr int PER = D / 32;
+    __shared__ int s_parent[PA_TREE_MAX_NODES];
+    const int tid = threadIdx.x, lane = tid & 31, s = blockIdx.y;
+    const int job = blockIdx.x * kJoinWarps + (tid >> 5), jobs = a.Hkv * a.chunks;
+    const int i = job / jobs, kvh = job % jobs / a.chunks, h0 = job % a.chunks * kHeads;
+    const int r0 = a.query_start[s], r1 = a.query_start[s + 1], L = r1 - r0;
+    const bool lead = blockIdx.x == 0 && tid == 0;
+    if (!(r0 >= 0 && r1 <= a.T && L >= 0 && L <= a.max_query_len)) return;  // flagged by the context's kernel
     bool bad = false;
-    for (int j = lane; j < L; j += 32) {
+    for (int j = tid; j < L; j += kJoinWarps * 32) {
         const int p = a.parents[r0 + j];
+        s_parent[j] = p;
         bad |= p < -1 || p >= j;
     }
-    if (__any_sync(0xffffffffu, bad)) {
+    if (__syncthreads_or(bad)) {
         if (lead && a.err_flag) atomicOr(a.err_flag, PA_FLAG_TREE_PARENT);
         return;
     }
     if (i >= L) return;
-    const int ctx = min(max(a.context_lens[s], 0), min(a.M * a.bs, a.max_context_len));
+    const int heads = min(kHeads, a.G - h0);
+    const int64_t pair = (int64_t)(r0 + i) * a.Hq + kvh * a.G + h0;  // row of the first head
     auto load = [&](const uint16_t *p, float (&x)[PER]) {
 #pragma unroll
         for (int e = 0; e < PER; e += 2) {
@@ -68,44 +95,88 @@ __global__ void __launch_bounds__(128) tree_join_kernel(const __grid_constant__ 
             x[e + 1] = __uint_as_float(w & 0xffff0000u);
         }
     };
-    float q[PER], acc[PER], m = -INFINITY, l = 0.f;
-    load(a.q + ((int64_t)(r0 + i) * a.Hq + h) * D + lane * PER, q);
+    float q[kHeads][PER], acc[kHeads][PER], m[kHeads], l[kHeads];
 #pragma unroll
-    for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-    const int kvh = h / a.G;
-    for (int at = i; at >= 0; at = a.parents[r0 + at]) {  // strictly decreasing: at most L steps
-        float k[PER], v[PER];
-        load(a.k + (int64_t)(r0 + at) * a.k_stride + kvh * D + lane * PER, k);
-        load(a.v + (int64_t)(r0 + at) * a.v_stride + kvh * D + lane * PER, v);
-        float x = 0.f;
+    for (int h = 0; h < kHeads; ++h) {
+        load(a.q + (pair + (h < heads ? h : 0)) * D + lane * PER, q[h]);
+        m[h] = -INFINITY;
+        l[h] = 0.f;
 #pragma unroll
-        for (int e = 0; e < PER; ++e) x = fmaf(q[e], k[e], x);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        x *= a.scale_log2;
-        const float mn = fmaxf(m, x), base = mn == -INFINITY ? 0.f : mn;
-        const float f = ex2(m - base), w = ex2(x - base);
-        m = mn;
-        l = l * f + w;
-#pragma unroll
-        for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, v[e], acc[e] * f);
+        for (int e = 0; e < PER; ++e) acc[h][e] = 0.f;
     }
-    const int nparts = (ctx + a.part_tokens - 1) / a.part_tokens;
-    const int64_t row = ((int64_t)(r0 + i) * a.Hq + h) * a.max_parts;
-    for (int p = 0; p < nparts; ++p) {
-        const float2 ml = *reinterpret_cast<const float2 *>(a.ws_ml + (row + p) * 2);
-        const float mn = fmaxf(m, ml.x), base = mn == -INFINITY ? 0.f : mn;
-        const float f = ex2(m - base), w = ex2(ml.x - base);
-        const float *src = a.ws_acc + (row + p) * D + lane * PER;
-        m = mn;
-        l = l * f + w * ml.y;
+    const uint16_t *kp = a.k + (int64_t)r0 * a.k_stride + kvh * D + lane * PER;
+    const uint16_t *vp = a.v + (int64_t)r0 * a.v_stride + kvh * D + lane * PER;
+    for (int at = i; at >= 0; at = s_parent[at]) {  // strictly decreasing: at most L steps
+        float k[PER], v[PER], x[kHeads];
+        load(kp + at * a.k_stride, k);
+        load(vp + at * a.v_stride, v);
 #pragma unroll
-        for (int e = 0; e < PER; ++e) acc[e] = fmaf(w, src[e], acc[e] * f);
+        for (int h = 0; h < kHeads; ++h) {
+            x[h] = 0.f;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) x[h] = fmaf(q[h][e], k[e], x[h]);
+        }
+        sum8(x, lane);
+#pragma unroll
+        for (int h = 0; h < kHeads; ++h) {
+            const float y = x[h] * a.scale_log2, mn = fmaxf(m[h], y), base = mn == -INFINITY ? 0.f : mn;
+            const float f = ex2(m[h] - base), w = ex2(y - base);
+            m[h] = mn;
+            l[h] = l[h] * f + w;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) acc[h][e] = fmaf(w, v[e], acc[h][e] * f);
+        }
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    uint16_t *dst = a.out + ((int64_t)(r0 + i) * a.Hq + h) * D + lane * PER;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int ctx = min(max(a.context_lens[s], 0), a.max_context_len);
+    // the partials of head h: rows (row, row + step, ..) of acc and ml
+    auto join = [&](const float *acc_in, const float *ml_in, int64_t row, int64_t step, int n, int h) {
+        for (int p = 0; p < n; ++p, row += step) {
+            const float2 ml = *reinterpret_cast<const float2 *>(ml_in + row * 2);
+            const float mn = fmaxf(m[h], ml.x), base = mn == -INFINITY ? 0.f : mn;
+            const float f = ex2(m[h] - base), w = ex2(ml.x - base);
+            const float *src = acc_in + row * D + lane * PER;
+            m[h] = mn;
+            l[h] = l[h] * f + w * ml.y;
 #pragma unroll
-    for (int e = 0; e < PER; e += 2) *reinterpret_cast<uint32_t *>(dst + e) = bf16x2(acc[e] * inv, acc[e + 1] * inv);
+            for (int e = 0; e < PER; ++e) acc[h][e] = fmaf(w, src[e], acc[h][e] * f);
+        }
+    };
+    if (a.tiles.prefix == nullptr) {
+        const int n = (ctx + a.part_tokens - 1) / a.part_tokens;
+#pragma unroll
+        for (int h = 0; h < kHeads; ++h)
+            if (h < heads) join(a.ws_acc, a.ws_ml, (pair + h) * a.max_parts, 1, n, h);
+    } else {
+        const TreeContext &c = a.tiles;
+        const int64_t n = (ctx + kTreeTile - 1) / kTreeTile, total = c.prefix[a.S];
+        if (n > 0) {
+            const int64_t first = c.prefix[s] + kvh * n;
+            const int64_t groups = min((int64_t)c.groups, total);
+            const int64_t g0 = tree_group_of(first, total, groups), g1 = tree_group_of(first + n - 1, total, groups);
+#pragma unroll
+            for (int h = 0; h < kHeads; ++h) {
+                if (h >= heads) continue;
+                if (g0 == g1) {
+                    join(c.whole_acc, c.whole_ml, pair + h, 0, 1, h);
+                } else {
+                    const int col = i * a.G + h0 + h, member = col / c.cols, in = col % c.cols;
+                    const int64_t cta = g0 * c.members + member;
+                    join(c.cut_acc, c.cut_ml, (cta * 2 + 1) * c.cols + in, 0, 1, h);
+                    join(c.cut_acc, c.cut_ml, (cta + c.members) * 2 * c.cols + in, (int64_t)c.members * 2 * c.cols, (int)(g1 - g0), h);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < kHeads; ++h) {
+        if (h >= heads) continue;
+        const float inv = l[h] > 0.f ? 1.f / l[h] : 0.f;
+        uint16_t *dst = a.out + (pair + h) * D + lane * PER;
+#pragma unroll
+        for (int e = 0; e < PER; e += 2)
+            *reinterpret_cast<uint32_t *>(dst + e) = bf16x2(acc[h][e] * inv, acc[h][e + 1] * inv);
+    }
 }
 
 // Partitions of the contexts and the workspace: as for the multi-token calls, n balanced
@@ -113,14 +184,30 @@ __global__ void __launch_bounds__(128) tree_join_kernel(const __grid_constant__ 
 // least two waves of two CTAs per SM.
 struct TreePlan {
     int CB, part_tokens, max_parts;
-    size_t ml_off, bytes;
+    // tcgen05: members and groups of CTAs, columns per CTA, and where the cut partials and
+    // the sequences' first tiles lie
+    int members, groups, cols;
+    size_t ml_off, cut_off, cut_ml_off, prefix_off, bytes;
 };
 
-TreePlan plan_tree(int S, int T, int Hq, int Hkv, int D, int max_context_len, int max_query_len) {
+TreePlan plan_tree(int S, int T, int Hq, int Hkv, int D, int kv_dtype, int max_context_len, int max_query_len) {
     TreePlan p{};
-    const int G = Hq / Hkv, ctx = std::max(max_context_len, 1);
+    const int G = Hq / Hkv, ctx = std::max(max_context_len, 1), sms = device_sms();
+    if (tree_tc_eligible(D, kv_dtype)) {
+        const int64_t columns = (int64_t)max_query_len * G;
+        p.cols = columns <= 128 ? 128 : 256;
+        p.members = (int)((columns + p.cols - 1) / p.cols);
+        p.groups = std::max(1, sms / p.members);
+        const size_t whole = (size_t)T * Hq, cut = (size_t)p.groups * p.members * 2 * p.cols;
+        p.ml_off = align_up(whole * D * sizeof(float), 256);
+        p.cut_off = align_up(p.ml_off + whole * 2 * sizeof(float), 256);
+        p.cut_ml_off = align_up(p.cut_off + cut * D * sizeof(float), 256);
+        p.prefix_off = align_up(p.cut_ml_off + cut * 2 * sizeof(float), 256);
+        p.bytes = align_up(p.prefix_off + (size_t)(S + 1) * sizeof(int64_t), 256);
+        return p;
+    }
     p.CB = std::max(1, (int)(((int64_t)max_query_len * G + multi_cols_per_cta() - 1) / multi_cols_per_cta()));
-    const double units = (double)S * Hkv * p.CB, slots = (double)device_sms() * 2;
+    const double units = (double)S * Hkv * p.CB, slots = (double)sms * 2;
     p.part_tokens = 256;
     double best = -1.0;
     for (int n = 1; n <= (ctx + 255) / 256; ++n) {
@@ -165,7 +252,7 @@ size_t pa_tree_workspace_size(int S, int T, int Hq, int Hkv, int D, int bs, int 
                               int max_query_len) {
     if (check_tree_args("pa_tree_workspace_size", S, T, Hq, Hkv, D, bs, kv_dtype, max_context_len, max_query_len) != PA_OK)
         return 0;
-    return plan_tree(S, T, Hq, Hkv, D, max_context_len, max_query_len).bytes;
+    return plan_tree(S, T, Hq, Hkv, D, kv_dtype, max_context_len, max_query_len).bytes;
 }
 
 pa_status pa_tree_attention(pa_bf16 *out, const pa_bf16 *query, const pa_bf16 *key, int64_t key_stride,
@@ -199,40 +286,14 @@ pa_status pa_tree_attention(pa_bf16 *out, const pa_bf16 *query, const pa_bf16 *k
         return fail(PA_ERR_INVALID_ARG, "%s: row strides must be multiples of 8, at least heads * head_dim", fn);
     if (!(scale == scale) || scale == __builtin_inff() || scale == -__builtin_inff())
         return fail(PA_ERR_INVALID_ARG, "%s: scale must be finite", fn);
-    const TreePlan plan = plan_tree(S, T, Hq, Hkv, D, max_context_len, max_query_len);
+    const TreePlan plan = plan_tree(S, T, Hq, Hkv, D, kv_dtype, max_context_len, max_query_len);
     if (!workspace || workspace_bytes < plan.bytes)
         return fail(PA_ERR_INVALID_ARG, "%s: workspace of %zu bytes needed, %zu given", fn, plan.bytes,
                     workspace ? workspace_bytes : (size_t)0);
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
         return fail(PA_ERR_INVALID_ARG, "%s: workspace must be 256-byte aligned", fn);
-    MultiArgs c{};
-    c.out = out;
-    c.q = query;
-    c.k_cache = k_cache;
-    c.v_cache = v_cache;
-    c.k_scale = k_scale;
-    c.v_scale = v_scale;
-    c.block_tables = block_tables;
-    c.context_lens = context_lens;
-    c.query_start = query_start;
-    c.ws_acc = (float *)workspace;
-    c.ws_ml = (float *)((char *)workspace + plan.ml_off);
-    c.err_flag = err_flag;
-    c.M = M;
-    c.S = S;
-    c.T = T;
-    c.Hq = Hq;
-    c.Hkv = Hkv;
-    c.G = Hq / Hkv;
-    c.g_shift = (c.G & (c.G - 1)) == 0 ? __builtin_ctz((unsigned)c.G) : -1;
-    c.N = N;
-    c.CB = plan.CB;
-    c.part_tokens = plan.part_tokens;
-    c.max_parts = plan.max_parts;
-    c.max_context_len = max_context_len;
-    c.max_query_len = max_query_len;
-    c.scale_log2 = scale * 1.4426950408889634f;
-    launch_multi_context(c, D, bs, kv_dtype, (cudaStream_t)stream);
+    char *ws = static_cast<char *>(workspace);
+    const int G = Hq / Hkv, g_shift = (G & (G - 1)) == 0 ? __builtin_ctz((unsigned)G) : -1;
     TreeArgs t{};
     t.out = out;
     t.q = query;
@@ -243,23 +304,91 @@ pa_status pa_tree_attention(pa_bf16 *out, const pa_bf16 *query, const pa_bf16 *k
     t.parents = parents;
     t.query_start = query_start;
     t.context_lens = context_lens;
-    t.ws_acc = c.ws_acc;
-    t.ws_ml = c.ws_ml;
     t.err_flag = err_flag;
     t.S = S;
     t.T = T;
     t.Hq = Hq;
     t.Hkv = Hkv;
-    t.G = c.G;
-    t.M = M;
-    t.bs = bs;
-    t.part_tokens = plan.part_tokens;
-    t.max_parts = plan.max_parts;
+    t.G = G;
+    t.chunks = (G + kHeads - 1) / kHeads;
     t.max_context_len = max_context_len;
     t.max_query_len = max_query_len;
-    t.scale_log2 = c.scale_log2;
-    const dim3 grid((unsigned)(((int64_t)max_query_len * Hq + 3) / 4), S);
-    launch_dependent(D == 128 ? tree_join_kernel<128> : tree_join_kernel<64>, grid, dim3(128), 0, (cudaStream_t)stream, t);
+    t.scale_log2 = scale * 1.4426950408889634f;
+    cudaError_t err;
+    if (plan.cols > 0) {
+        TreeContext c{};
+        c.q = query;
+        c.k_cache = k_cache;
+        c.v_cache = v_cache;
+        c.k_scale = k_scale;
+        c.v_scale = v_scale;
+        c.block_tables = block_tables;
+        c.context_lens = context_lens;
+        c.query_start = query_start;
+        c.whole_acc = (float *)ws;
+        c.whole_ml = (float *)(ws + plan.ml_off);
+        c.cut_acc = (float *)(ws + plan.cut_off);
+        c.cut_ml = (float *)(ws + plan.cut_ml_off);
+        c.prefix = (int64_t *)(ws + plan.prefix_off);
+        c.err_flag = err_flag;
+        c.M = M;
+        c.S = S;
+        c.T = T;
+        c.Hq = Hq;
+        c.Hkv = Hkv;
+        c.G = G;
+        c.N = N;
+        c.g_shift = g_shift;
+        c.members = plan.members;
+        c.groups = plan.groups;
+        c.cols = plan.cols;
+        c.max_context_len = max_context_len;
+        c.max_query_len = max_query_len;
+        c.scale_log2 = t.scale_log2;
+        err = launch_tree_tc(c, bs, kv_dtype, (cudaStream_t)stream);
+        t.tiles = c;
+    } else {
+        MultiArgs c{};
+        c.out = out;
+        c.q = query;
+        c.k_cache = k_cache;
+        c.v_cache = v_cache;
+        c.k_scale = k_scale;
+        c.v_scale = v_scale;
+        c.block_tables = block_tables;
+        c.context_lens = context_lens;
+        c.query_start = query_start;
+        c.ws_acc = (float *)ws;
+        c.ws_ml = (float *)(ws + plan.ml_off);
+        c.err_flag = err_flag;
+        c.M = M;
+        c.S = S;
+        c.T = T;
+        c.Hq = Hq;
+        c.Hkv = Hkv;
+        c.G = G;
+        c.g_shift = g_shift;
+        c.N = N;
+        c.CB = plan.CB;
+        c.part_tokens = plan.part_tokens;
+        c.max_parts = plan.max_parts;
+        c.max_context_len = max_context_len;
+        c.max_query_len = max_query_len;
+        c.scale_log2 = t.scale_log2;
+        err = launch_multi_context(c, D, bs, kv_dtype, (cudaStream_t)stream);
+        t.ws_acc = c.ws_acc;
+        t.ws_ml = c.ws_ml;
+        t.part_tokens = plan.part_tokens;
+        t.max_parts = plan.max_parts;
+    }
+    if (err != cudaSuccess) {
+        cudaGetLastError();
+        return fail(PA_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(err));
+    }
+    const int64_t jobs = (int64_t)max_query_len * Hkv * t.chunks;
+    const dim3 grid((unsigned)((jobs + kJoinWarps - 1) / kJoinWarps), S);
+    launch_dependent(D == 128 ? tree_join_kernel<128> : tree_join_kernel<64>, grid, dim3(kJoinWarps * 32), 0,
+                     (cudaStream_t)stream, t);
     return check_launch(fn);
 }
 
