@@ -106,10 +106,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const __grid
     }
     const uint16_t *kp = a.k + (int64_t)r0 * a.k_stride + kvh * D + lane * PER;
     const uint16_t *vp = a.v + (int64_t)r0 * a.v_stride + kvh * D + lane * PER;
-    for (int at = i; at >= 0; at = s_parent[at]) {  // strictly decreasing: at most L steps
-        float k[PER], v[PER], x[kHeads];
-        load(kp + at * a.k_stride, k);
-        load(vp + at * a.v_stride, v);
+    // strictly decreasing: at most L steps; the next ancestor's rows are loaded ahead
+    float k[PER], v[PER];
+    load(kp + i * a.k_stride, k);
+    load(vp + i * a.v_stride, v);
+    for (int at = i; at >= 0;) {
+        const int up = s_parent[at];
+        float kn[PER], vn[PER], x[kHeads];
+        if (up >= 0) {
+            load(kp + up * a.k_stride, kn);
+            load(vp + up * a.v_stride, vn);
+        }
 #pragma unroll
         for (int h = 0; h < kHeads; ++h) {
             x[h] = 0.f;
@@ -126,46 +133,75 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const __grid
 #pragma unroll
             for (int e = 0; e < PER; ++e) acc[h][e] = fmaf(w, v[e], acc[h][e] * f);
         }
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+            k[e] = kn[e];
+            v[e] = vn[e];
+        }
+        at = up;
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int ctx = min(max(a.context_lens[s], 0), a.max_context_len);
-    // the partials of head h: rows (row, row + step, ..) of acc and ml
-    auto join = [&](const float *acc_in, const float *ml_in, int64_t row, int64_t step, int n, int h) {
-        for (int p = 0; p < n; ++p, row += step) {
-            const float2 ml = *reinterpret_cast<const float2 *>(ml_in + row * 2);
-            const float mn = fmaxf(m[h], ml.x), base = mn == -INFINITY ? 0.f : mn;
-            const float f = ex2(m[h] - base), w = ex2(ml.x - base);
-            const float *src = acc_in + row * D + lane * PER;
-            m[h] = mn;
-            l[h] = l[h] * f + w * ml.y;
-#pragma unroll
-            for (int e = 0; e < PER; ++e) acc[h][e] = fmaf(w, src[e], acc[h][e] * f);
-        }
-    };
+    // where the partials lie: lane h < 8 keeps head h's first row and the step to its next
+    const float *acc_in = a.ws_acc, *ml_in = a.ws_ml;
+    int64_t row = (pair + lane) * a.max_parts, step = 1, later = 0;  // later: row of the second partial
+    int n;
     if (a.tiles.prefix == nullptr) {
-        const int n = (ctx + a.part_tokens - 1) / a.part_tokens;
-#pragma unroll
-        for (int h = 0; h < kHeads; ++h)
-            if (h < heads) join(a.ws_acc, a.ws_ml, (pair + h) * a.max_parts, 1, n, h);
+        n = (ctx + a.part_tokens - 1) / a.part_tokens;
+        later = row + 1;
     } else {
         const TreeContext &c = a.tiles;
-        const int64_t n = (ctx + kTreeTile - 1) / kTreeTile, total = c.prefix[a.S];
-        if (n > 0) {
-            const int64_t first = c.prefix[s] + kvh * n;
-            const int64_t groups = min((int64_t)c.groups, total);
-            const int64_t g0 = tree_group_of(first, total, groups), g1 = tree_group_of(first + n - 1, total, groups);
-#pragma unroll
-            for (int h = 0; h < kHeads; ++h) {
-                if (h >= heads) continue;
-                if (g0 == g1) {
-                    join(c.whole_acc, c.whole_ml, pair + h, 0, 1, h);
-                } else {
-                    const int col = i * a.G + h0 + h, member = col / c.cols, in = col % c.cols;
-                    const int64_t cta = g0 * c.members + member;
-                    join(c.cut_acc, c.cut_ml, (cta * 2 + 1) * c.cols + in, 0, 1, h);
-                    join(c.cut_acc, c.cut_ml, (cta + c.members) * 2 * c.cols + in, (int64_t)c.members * 2 * c.cols, (int)(g1 - g0), h);
-                }
+        const int64_t tiles = (ctx + kTreeTile - 1) / kTreeTile, total = c.prefix[a.S];
+        n = 0;
+        if (tiles > 0) {
+            const int64_t first = c.prefix[s] + kvh * tiles, groups = min((int64_t)c.groups, total);
+            const int64_t g0 = tree_group_of(first, total, groups), g1 = tree_group_of(first + tiles - 1, total, groups);
+            n = (int)(g1 - g0) + 1;
+            if (n == 1) {
+                acc_in = c.whole_acc;
+                ml_in = c.whole_ml;
+                row = pair + lane;
+            } else {
+                acc_in = c.cut_acc;
+                ml_in = c.cut_ml;
+                const int col = i * a.G + h0 + lane, member = col / c.cols, in = col % c.cols;
+                const int64_t cta = g0 * c.members + member;
+                row = (cta * 2 + 1) * c.cols + in;
+                later = (cta + c.members) * 2 * c.cols + in;
+                step = (int64_t)c.members * 2 * c.cols;
             }
+        }
+    }
+    for (int p = 0; p < n; ++p) {
+        float x[kHeads][PER];
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (lane < heads) ml = *reinterpret_cast<const float2 *>(ml_in + row * 2);
+#pragma unroll
+        for (int h = 0; h < kHeads; ++h) {
+            const int64_t r = __shfl_sync(0xffffffffu, row, h < heads ? h : 0);
+            const float *src = acc_in + r * D + lane * PER;
+            if constexpr (PER == 4) {
+                const float4 w = *reinterpret_cast<const float4 *>(src);
+                x[h][0] = w.x;
+                x[h][1] = w.y;
+                x[h][2] = w.z;
+                x[h][3] = w.w;
+            } else {
+                const float2 w = *reinterpret_cast<const float2 *>(src);
+                x[h][0] = w.x;
+                x[h][1] = w.y;
+            }
+        }
+        row = p == 0 ? later : row + step;
+#pragma unroll
+        for (int h = 0; h < kHeads; ++h) {
+            const float pm = __shfl_sync(0xffffffffu, ml.x, h), pl = __shfl_sync(0xffffffffu, ml.y, h);
+            const float mn = fmaxf(m[h], pm), base = mn == -INFINITY ? 0.f : mn;
+            const float f = ex2(m[h] - base), w = ex2(pm - base);
+            m[h] = mn;
+            l[h] = l[h] * f + w * pl;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) acc[h][e] = fmaf(w, x[h][e], acc[h][e] * f);
         }
     }
 #pragma unroll
