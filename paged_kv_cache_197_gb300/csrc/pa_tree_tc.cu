@@ -6,14 +6,15 @@
 //
 // One CTA per SM (224 KB of shared memory, all 512 tensor-memory columns) works through its
 // share of all tiles of the batch (pa_tree.cuh): 128 tokens of K and V at a time, staged by
-// TMA into a ring of five 32 KB stages that runs on across units.  Ten warps with fixed
-// roles, coupled by mbarriers:
+// TMA into a ring of five 32 KB stages that runs on across units.  Warps with fixed roles,
+// coupled by mbarriers:
 //   * warps 0-3 and 4-7 are two lanes of 128 columns, a thread per column.  With more than
 //     128 columns the lanes take the two halves of 256 columns and share every staged
 //     tile; with at most 128 they take the same columns and alternate tiles, and are
 //     joined at the end of a unit.  Either way one lane's exponentials run while the
 //     tensor cores work for the other;
-//   * warp 8 copies K and V tiles; warp 9 issues the products.
+//   * warp 8 copies K and V tiles; one thread each of warps 9 and 10 issues a lane's products.
+//     (Warp 11 fills the warpgroup, whose spare registers go to the columns.)
 // Tensor memory: S of the lanes at columns 0 and 128 (overwritten by P as bf16 pairs, the A
 // operand of P V), O at 256 and 384.
 // Bounds: up to 128 columns, or 256 shared ones, the 64 KB of a K and V tile take 2800 SM
@@ -24,7 +25,6 @@
 
 #include <atomic>
 
-#include "pa_stages.h"
 #include "pa_tc.cuh"
 #include "pa_tree.cuh"
 
@@ -36,21 +36,32 @@ using namespace tc;
 constexpr int kTile = kTreeTile;
 constexpr int kD = 128;
 constexpr int kLaneCols = 128;
-constexpr int kTileBytes = kTile * kD * 2;   // 32 KB: two 64-dim halves of 128 rows of 128 B
-constexpr int kHalf = kTile * 128;
+constexpr int kTileBytes = kTile * kD * 2;   // 32 KB
+// A staged tile: groups of 8 rows, each as two 64-dim halves of 8 x 128 B (one swizzle atom
+// each).  A cache block is then one copy of bs x 256 contiguous bytes, and the atoms of a
+// half lie a constant 2 KB apart, as the matrix descriptors need.
+constexpr int kHalf = 1024, kGroup = 2048;
 constexpr int kStages = 5;
+// Ring position p lands in stage p % kStages and completes barrier p % kFull.  With
+// alternating lanes a lane sees only its own positions, up to three apart, and copies land
+// in any order, so a stage's own barrier could still be at the other lane's copy of
+// position p - 5 when position p is asked for, and that phase has the parity of p's
+// predecessor's predecessor.  With two barriers a stage the predecessor is p - 10, and a
+// copy past p - 5 is only issued once p - 10 was consumed.
+constexpr int kFull = 2 * kStages;
 constexpr int kOffQ = 0, kOffRing = 2 * kTileBytes, kOffShared = kOffRing + kStages * kTileBytes;
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;  // three warpgroups: two lanes of columns; copies and products
+constexpr int kRegsColumns = 192, kRegsOther = 120;  // 2 x 128 x 192 + 128 x 120 = 384 x 168 at launch
 constexpr uint32_t kTmemS = 0, kTmemO = 256;  // + 128 per lane
 constexpr float kRescaleLog2 = 8.0f;
 
 struct Shared {
     float2 ml[2][kLaneCols];                    // lanes joined: each one's (max, sum) per column
-    uint64_t full[kStages], free[kStages];      // ring stages: landed / consumed
+    uint64_t full[kFull], free[kStages];        // ring positions landed / stages consumed
     uint64_t sfull[2], pfull[2], odone[2];      // per lane: S written, P written, P V done
     uint64_t qfull[2];                          // per lane: the unit's queries are staged
     uint64_t mlready, oread;                    // lanes joined: both (max, sum) and O in / read
-    uint64_t drain;
+    uint64_t drain[2];
     int64_t total, first_tile;                  // of all tiles; of the first sequence
     int first_seq;
     int wsum[kThreads / 32];
@@ -86,9 +97,17 @@ __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, int *ab
     }
 }
 
-// Byte offset of the 16-byte chunk ch of row r in a 128-row tile with the 128-byte swizzle.
+// Byte offset of the 16-byte chunk ch of row r in a tile (128-byte swizzle).
 __device__ __forceinline__ uint32_t tile_chunk(int r, int ch) {
-    return (ch >> 3) * kHalf + (r >> 3) * 1024 + (r & 7) * 128 + (((ch & 7) ^ (r & 7)) << 4);
+    return (r >> 3) * kGroup + (ch >> 3) * kHalf + (r & 7) * 128 + (((ch & 7) ^ (r & 7)) << 4);
+}
+
+// One block of a pool, [bs / 8][2][8][64] in the order of a staged tile.
+__device__ __forceinline__ void tma_block(uint32_t dst, const CUtensorMap *map, int group, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(group), "r"(bar)
+        : "memory");
 }
 
 // The next range of tiles of one (sequence, kv head) in a CTA's share.
@@ -135,9 +154,9 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
     }
     const int group = blockIdx.x / a.members, member = blockIdx.x % a.members;
     if (tid == 0) {
+        for (int i = 0; i < kFull; ++i) mbar_init(tc_smem(&sh.full[i]));
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(tc_smem(&sh.full[i]));
-            mbar_init(tc_smem(&sh.free[i]));
+            mbar_init_n(tc_smem(&sh.free[i]), SPLIT ? 1 : 2);  // lanes that read a stage
         }
         for (int w = 0; w < 2; ++w) {
             mbar_init(tc_smem(&sh.sfull[w]));
@@ -147,7 +166,8 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
         }
         mbar_init_n(tc_smem(&sh.mlready), 2 * kLaneCols);
         mbar_init_n(tc_smem(&sh.oread), 2 * kLaneCols);
-        mbar_init(tc_smem(&sh.drain));
+        mbar_init(tc_smem(&sh.drain[0]));
+        mbar_init(tc_smem(&sh.drain[1]));
         sh.abort = 0;
         sh.first_seq = 0;
         sh.first_tile = 0;
@@ -170,8 +190,9 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
         if (report && !ok) raise_flag(a.err_flag, PA_FLAG_QUERY_OUT_OF_RANGE);
         return ok && L > 0 ? (min(max(ctx, 0), lim) + kTile - 1) / kTile : 0;
     };
-    int64_t sum = 0;
-    for (int s = tid; s < a.S; s += kThreads) sum += tiles_of(s, blockIdx.x == 0);
+    const int n_first = tid < a.S ? tiles_of(tid, blockIdx.x == 0) : 0;
+    int64_t sum = n_first;
+    for (int s = tid + kThreads; s < a.S; s += kThreads) sum += tiles_of(s, blockIdx.x == 0);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (tid == 0) sh.total = 0;
@@ -184,7 +205,7 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
     const int64_t end = group < groups ? (group + 1) * total / groups : total;
     int64_t carry = 0;
     for (int base = 0; base < a.S; base += kThreads) {
-        const int s = base + tid, n = s < a.S ? tiles_of(s, false) : 0;
+        const int s = base + tid, n = base == 0 ? n_first : s < a.S ? tiles_of(s, false) : 0;
         int v = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -220,132 +241,143 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
     auto mine = [&](const Walk &u) { return u.ncols > member * a.cols; };
     // Ring positions of tile t's K and V within a unit of n tiles, in the order they are used:
     // K0 V0 K1 V1 .. (shared tiles), K0 K1 V0 K2 V1 .. (alternating lanes).
-    auto k_at = [&](int t, int n) { return SPLIT ? (t == 0 ? 0 : 2 * t - 1) : 2 * t; };
-    auto v_at = [&](int t, int n) { return SPLIT ? (t < n - 1 ? 2 * t + 2 : 2 * n - 1) : 2 * t + 1; };
+    auto k_at = [](int t, int n) { return SPLIT ? (t == 0 ? 0 : 2 * t - 1) : 2 * t; };
+    auto v_at = [](int t, int n) { return SPLIT ? (t < n - 1 ? 2 * t + 2 : 2 * n - 1) : 2 * t + 1; };
 
+    if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
     if (warp == 8) {
-        // ---- copies
-        const int oob_row = a.N * a.Hkv * BS;  // a row past the pool: the copy fills zeros
-        constexpr int kBoxes = kTile / BS * 2;  // two 64-dim boxes per block
+        // ---- copies: lane i takes block i of a tile
+        constexpr int kBlocks = kTile / BS, kGroups = BS / 8;  // 8-row groups of a block and kv head
+        const int oob = a.N * a.Hkv * kGroups;  // past the pool: the copy fills zeros
+        const uint32_t box = tc_smem(smem + kOffRing) + lane * BS * 256;
+        int st = 0;
+        uint32_t phase = 0;   // of the stage's next wait for `free`
         int issued = 0;
         bool ok = true;
+        auto fill = [&](const CUtensorMap *map, int y) {
+            if (issued >= kStages) ok = wait_for(&sh.free[st], phase ^ 1, abort);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) return;
+            const uint32_t bar = tc_smem(&sh.full[issued % kFull]);
+            if (lane == 0) mbar_expect(bar, kTileBytes);
+            __syncwarp();
+            if (lane < kBlocks) tma_block(box + st * kTileBytes, map, y, bar);
+            ++issued;
+            if (++st == kStages) {
+                st = 0;
+                phase ^= 1;
+            }
+        };
         while (ok && w.next(a)) {
             if (!mine(w)) continue;
             const int nblk = (w.ctx + BS - 1) / BS;
-            auto fill = [&](bool is_k, int t) {
-                const int st = issued % kStages, use = issued / kStages;
-                int y = oob_row;
-                const int idx = (w.t0 + t) * (kTile / BS) + lane / 2;
-                if (lane < kBoxes && idx < nblk) {
-                    const int b = __ldg(a.block_tables + (int64_t)w.s * a.M + idx);
-                    if (b >= 0 && b < a.N)
-                        y = (b * a.Hkv + w.kvh) * BS;
-                    else if (is_k && member == 0)
-                        raise_flag(a.err_flag, PA_FLAG_BLOCK_OUT_OF_RANGE);
-                }
-                if (use > 0) ok = wait_for(&sh.free[st], (use - 1) & 1, abort);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) return;
-                const uint32_t bar = tc_smem(&sh.full[st]);
-                if (lane == 0) mbar_expect(bar, kTileBytes);
-                __syncwarp();
-                if (lane < kBoxes)
-                    tma_load(tc_smem(smem + kOffRing + st * kTileBytes) + (lane & 1) * kHalf + (lane / 2) * BS * 128,
-                             is_k ? &kmap : &vmap, (lane & 1) * 64, y, bar);
-                __syncwarp();
-                ++issued;
+            const int32_t *table = a.block_tables + (int64_t)w.s * a.M;
+            // the raw table entry of this lane's block of tile t; -2 for blocks past the context
+            auto entry = [&](int t) {
+                const int idx = (w.t0 + t) * kBlocks + lane;
+                return t < w.n && lane < kBlocks && idx < nblk ? __ldg(table + idx) : -2;
             };
-            fill(true, 0);
+            auto row_of = [&](int t, int b) {
+                if (b >= 0 && b < a.N) return (b * a.Hkv + w.kvh) * kGroups;
+                const int idx = (w.t0 + t) * kBlocks + lane;
+                if (t < w.n && lane < kBlocks && idx < nblk && member == 0) raise_flag(a.err_flag, PA_FLAG_BLOCK_OUT_OF_RANGE);
+                return oob;
+            };
+            // entries are loaded two tiles ahead of their copies
+            int y = row_of(0, entry(0)), e1 = entry(1), e2 = entry(2);
+            fill(&kmap, y);
             for (int t = 0; ok && t < w.n; ++t) {
-                if (SPLIT && t + 1 < w.n) fill(true, t + 1);
-                if (ok) fill(false, t);
-                if (!SPLIT && ok && t + 1 < w.n) fill(true, t + 1);
+                const int yn = row_of(t + 1, e1);
+                e1 = e2;
+                e2 = entry(t + 3);
+                if (SPLIT && t + 1 < w.n) fill(&kmap, yn);
+                if (ok) fill(&vmap, y);
+                if (!SPLIT && ok && t + 1 < w.n) fill(&kmap, yn);
+                y = yn;
             }
         }
         if (!ok) {
             // stopping early: copies already issued may still be landing in shared memory
-            for (int st = 0; st < kStages; ++st) {
-                const StageFill f = last_fill(issued, kStages, st);
-                if (f.any) mbar_wait(tc_smem(&sh.full[st]), f.parity);
-            }
+            for (int i = max(0, issued - kStages); i < issued; ++i)
+                mbar_wait(tc_smem(&sh.full[i % kFull]), (i / kFull) & 1);
         }
-    } else if (warp == 9) {
-        // ---- products: the whole warp waits, lane 0 issues
-        int ring = 0, pv[2] = {0, 0}, qs[2] = {0, 0};
-        bool ok = true;
-        auto stage_addr = [&](int at) { return tc_smem(smem + kOffRing + ((ring + at) % kStages) * kTileBytes); };
-        auto landed = [&](int at) { return wait_for(&sh.full[(ring + at) % kStages], ((ring + at) / kStages) & 1, abort); };
-        while (ok && w.next(a)) {
-            if (!mine(w)) continue;
-            const bool two = second(w);
-            // S of lane l, tile t; `last`: no other lane uses this K after it
-            auto scores = [&](int l, int t, bool first, bool last) {
-                const int at = k_at(t, w.n);
-                if (first) ok = wait_for(&sh.qfull[l], qs[l]++ & 1, abort);
-                // S overwrites P: the lane's last P V is done (this also orders O for its rows)
-                if (ok && pv[l] > 0) ok = wait_for(&sh.odone[l], (pv[l] - 1) & 1, abort);
-                if (ok) ok = landed(at);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) return;
-                tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t qb = tc_smem(smem + kOffQ + l * kTileBytes), kb = stage_addr(at);
+    } else if (warp < 11) {
+        // ---- products of lane l: one thread waits and issues (a thread per lane, so that one
+        // lane's waits do not hold up the other's products)
+        if (lane == 0) {
+            const int l = warp - 9;
+            int ring = 0;
+            uint32_t pv = 0, qs = 0;
+            bool ok = true;
+            const uint32_t t_s = tmem + kTmemS + l * 128, t_o = tmem + kTmemO + l * 128;
+            const uint64_t qd = sw128_desc(tc_smem(smem + kOffQ + l * kTileBytes), 16, kGroup);
+            const uint64_t kd = sw128_desc(tc_smem(smem + kOffRing), 16, kGroup);
+            const uint64_t vd = sw128_desc(tc_smem(smem + kOffRing), kHalf, kGroup);
+            const uint32_t sfull = tc_smem(&sh.sfull[l]), odone = tc_smem(&sh.odone[l]);
+            while (ok && w.next(a)) {
+                if (!mine(w)) continue;
+                if (l == 1 && !second(w)) {
+                    // the other lane reads these tiles alone
+                    if constexpr (!SPLIT)
+                        for (int at = ring; ok && at < ring + 2 * w.n; ++at) {
+                            ok = wait_for(&sh.full[at % kFull], (at / kFull) & 1, abort);
+                            if (ok) mbar_arrive(tc_smem(&sh.free[at % kStages]));
+                        }
+                    ring += 2 * w.n;
+                    continue;
+                }
+                auto scores = [&](int t, bool first) {
+                    const int at = ring + k_at(t, w.n), st = at % kStages;
+                    // (the queries first: their lane has seen every earlier unit's end)
+                    if (first) ok = wait_for(&sh.qfull[l], qs++ & 1, abort);
+                    if (ok) ok = wait_for(&sh.full[at % kFull], (at / kFull) & 1, abort);
+                    // S overwrites P: the lane's last P V is done (this also orders O for its rows)
+                    if (ok && pv > 0) ok = wait_for(&sh.odone[l], (pv - 1) & 1, abort);
+                    if (!ok) return;
+                    tc_fence_after();
+                    const uint64_t k0 = kd + (uint64_t)(st * (kTileBytes >> 4));
 #pragma unroll
                     for (int kk = 0; kk < kD / 16; ++kk) {
-                        const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-                        umma(tmem + kTmemS + l * 128, sw128_desc(qb + off, 16, 1024), sw128_desc(kb + off, 16, 1024),
-                             bf16_idesc(128, kTile, 0), kk > 0);
+                        const uint64_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+                        umma(t_s, qd + off, k0 + off, bf16_idesc(128, kTile, 0), kk > 0);
                     }
-                    umma_commit(tc_smem(&sh.sfull[l]));
-                    if (last) umma_commit(tc_smem(&sh.free[(ring + at) % kStages]));
-                }
-                __syncwarp();
-            };
-            auto weighted = [&](int l, int t, bool first, bool last) {
-                const int at = v_at(t, w.n);
-                ok = wait_for(&sh.pfull[l], pv[l] & 1, abort);
-                if (ok) ok = landed(at);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) return;
-                tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t vb = stage_addr(at);
+                    umma_commit(sfull);
+                    umma_commit(tc_smem(&sh.free[st]));
+                };
+                auto weighted = [&](int t, bool first) {
+                    const int at = ring + v_at(t, w.n), st = at % kStages;
+                    ok = wait_for(&sh.full[at % kFull], (at / kFull) & 1, abort);
+                    if (ok) ok = wait_for(&sh.pfull[l], pv & 1, abort);
+                    if (!ok) return;
+                    tc_fence_after();
+                    const uint64_t v0 = vd + (uint64_t)(st * (kTileBytes >> 4));
 #pragma unroll
                     for (int kk = 0; kk < kTile / 16; ++kk)
-                        umma_ts(tmem + kTmemO + l * 128, tmem + kTmemS + l * 128 + kk * 8,
-                                sw128_desc(vb + kk * 2048, kHalf, 1024), bf16_idesc(128, kD, 1), !first || kk > 0);
-                    umma_commit(tc_smem(&sh.odone[l]));
-                    if (last) umma_commit(tc_smem(&sh.free[(ring + at) % kStages]));
+                        umma_ts(t_o, t_s + kk * 8, v0 + (kk * 2 * kGroup >> 4), bf16_idesc(128, kD, 1), !first || kk > 0);
+                    umma_commit(odone);
+                    umma_commit(tc_smem(&sh.free[st]));
+                    ++pv;
+                };
+                constexpr int kStep = SPLIT ? 2 : 1;
+                const int t_first = SPLIT ? l : 0;
+                scores(t_first, true);
+                for (int t = t_first; ok && t < w.n; t += kStep) {
+                    weighted(t, t == t_first);
+                    if (ok && t + kStep < w.n) scores(t + kStep, false);
                 }
-                __syncwarp();
-                ++pv[l];
-            };
-            if constexpr (SPLIT) {
-                scores(0, 0, true, true);
-                if (ok && two) scores(1, 1, true, true);
-                for (int t = 0; ok && t < w.n; ++t) {
-                    weighted(t & 1, t, t < 2, true);
-                    if (ok && t + 2 < w.n) scores(t & 1, t + 2, false, true);
-                }
-            } else {
-                scores(0, 0, true, !two);
-                if (ok && two) scores(1, 0, true, true);
-                for (int t = 0; ok && t < w.n; ++t) {
-                    weighted(0, t, t == 0, !two);
-                    if (ok && t + 1 < w.n) scores(0, t + 1, false, !two);
-                    if (ok && two) weighted(1, t, t == 0, true);
-                    if (ok && two && t + 1 < w.n) scores(1, t + 1, false, true);
-                }
+                ring += 2 * w.n;
             }
-            ring += 2 * w.n;
+            if (!ok) {
+                // stopping early: every product already issued finishes before tensor memory is released
+                umma_commit(tc_smem(&sh.drain[l]));
+                mbar_wait(tc_smem(&sh.drain[l]), 0);
+            }
         }
-        if (!ok) {
-            // stopping early: every product already issued finishes before tensor memory is released
-            if (lane == 0) umma_commit(tc_smem(&sh.drain));
-            __syncwarp();
-            mbar_wait(tc_smem(&sh.drain), 0);
-        }
+        __syncwarp();
+    }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsColumns));
         // ---- a lane's columns: thread = column = tensor-memory lane
         const int l = warp >> 2, row = tid & 127;
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
@@ -367,14 +399,19 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
             const int64_t pair = (int64_t)(w.r0 + tok) * a.Hq + w.kvh * a.G + head;
             float m = -INFINITY, sum_l = 0.f;
             if (active) {
-                // the unit's queries (this lane's products with the last unit's are done)
-                const uint4 *src = reinterpret_cast<const uint4 *>(a.q + pair * kD);
+                // the unit's queries (this lane's products with the last unit's are done): a
+                // row at a time by half a warp
+                uint4 x[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                    if (col) x = __ldg(src + i);
-                    *reinterpret_cast<uint4 *>(qbuf + tile_chunk(row, i)) = x;
+                    const int r = 2 * i + (lane >> 4);
+                    const int64_t from = __shfl_sync(0xffffffffu, col ? pair : -1, r);
+                    x[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (from >= 0) x[i] = __ldg(reinterpret_cast<const uint4 *>(a.q + from * kD) + (lane & 15));
                 }
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    *reinterpret_cast<uint4 *>(qbuf + tile_chunk((warp & 3) * 32 + 2 * i + (lane >> 4), lane & 15)) = x[i];
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 mbar_arrive(tc_smem(&sh.qfull[l]));
             }
@@ -445,9 +482,9 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                 }
                 // rows past the context inside its last block may hold anything, and a zero
                 // weight times a NaN is a NaN: zero them in the V stage
-                if (k0 + kTile > w.ctx && w.ctx % BS != 0 && (SPLIT || l == 0)) {
+                if (k0 + kTile > w.ctx && w.ctx % BS != 0) {
                     const int at = ring + v_at(t, w.n), st = at % kStages;
-                    ok = wait_for(&sh.full[st], (at / kStages) & 1, abort);
+                    ok = wait_for(&sh.full[at % kFull], (at / kFull) & 1, abort);
                     if (!(ok = __all_sync(0xffffffffu, ok))) break;
                     const int lo = w.ctx - k0, hi = min(kTile, (w.ctx + BS - 1) / BS * BS - k0);
                     unsigned char *vst = smem + kOffRing + st * kTileBytes;
@@ -461,11 +498,29 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
             }
             ring += 2 * w.n;
             if (!ok) break;
-            // ---- the columns' partials
+            // ---- the columns' partials, 32 dims at a time through the query buffer (the unit's
+            // products with it are done): rows by threads in, 128-byte pieces of rows out
             const bool all = w.t0 == 0 && w.n == w.tiles;
             const int64_t at = all ? pair : ((int64_t)blockIdx.x * 2 + (w.t0 == 0 ? 1 : 0)) * a.cols + (c - member * a.cols);
-            float *acc = (all ? a.whole_acc : a.cut_acc) + at * kD;
+            float *acc = all ? a.whole_acc : a.cut_acc;
             float2 *ml = reinterpret_cast<float2 *>(all ? a.whole_ml : a.cut_ml) + at;
+            constexpr int kPitch = 144;  // of a staged row of 128 bytes: no bank conflicts
+            unsigned char *stage = qbuf + (warp & 3) * 32 * kPitch;
+            auto put = [&](const float (&ov)[32], int q) {
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    *reinterpret_cast<float4 *>(stage + lane * kPitch + i * 16) =
+                        make_float4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = 4 * i + (lane >> 3);
+                    const int64_t to = __shfl_sync(0xffffffffu, col ? at : -1, r);
+                    const float4 x = *reinterpret_cast<const float4 *>(stage + r * kPitch + (lane & 7) * 16);
+                    if (to >= 0) *reinterpret_cast<float4 *>(acc + to * kD + 32 * q + (lane & 7) * 4) = x;
+                }
+            };
             if (active) ok = wait_for(&sh.odone[l], (done - 1) & 1, abort);
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
             tc_fence_after();
@@ -475,11 +530,7 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                     float ov[32];
                     tmem_ld32(t_o + 32 * q, ov);
                     tmem_wait_ld();
-                    if (!col) continue;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        reinterpret_cast<float4 *>(acc)[8 * q + i] =
-                            make_float4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
+                    put(ov, q);
                 }
                 if (col) *ml = make_float2(m, sum_l);
             } else {
@@ -507,11 +558,7 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
 #pragma unroll
                         for (int i = 0; i < 32; ++i) ov[i] = fmaf(other[i], fy, ov[i]);
                     }
-                    if (!col) continue;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        reinterpret_cast<float4 *>(acc)[8 * q + i] =
-                            make_float4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
+                    put(ov, q);
                 }
                 if (col && l == 0) *ml = make_float2(top, x.y * fx + y.y * fy);
                 // O may be overwritten, and ml, once both lanes have read them
@@ -521,6 +568,7 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 ++joins;
             }
+            __syncwarp();
             tc_fence_before();
         }
     }
@@ -531,16 +579,16 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
     if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
-// A cache pool [N][Hkv][bs][128] bf16 as rows of 128 values, copied in boxes of 64 values x
-// bs rows with the 128-byte swizzle.
-bool pool_map(CUtensorMap *map, const void *pool, int rows, int bs) {
+// A cache pool [N][Hkv][bs][128] bf16 as [8-row group][64-dim half][8 rows][64], copied a
+// block at a time with the 128-byte swizzle.
+bool pool_map(CUtensorMap *map, const void *pool, int groups, int bs) {
     const EncodeTiled fn = encode_tiled();
     if (!fn) return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)kD, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)kD * 2};
-    const cuuint32_t box[2] = {64u, (cuuint32_t)bs};
-    const cuuint32_t estr[2] = {1u, 1u};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(pool), dims, strides, box, estr,
+    const cuuint64_t dims[4] = {64, 8, 2, (cuuint64_t)groups};
+    const cuuint64_t strides[3] = {kD * 2, 128, 8 * kD * 2};
+    const cuuint32_t box[4] = {64u, 8u, 2u, (cuuint32_t)(bs / 8)};
+    const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(pool), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -548,9 +596,9 @@ bool pool_map(CUtensorMap *map, const void *pool, int rows, int bs) {
 template <int BS, bool SPLIT>
 cudaError_t launch_typed(const TreeContext &a, cudaStream_t stream) {
     CUtensorMap kmap, vmap;
-    if ((int64_t)a.N * a.Hkv * BS >= (int64_t)INT32_MAX) return cudaErrorInvalidValue;  // TMA row coordinates
-    const int rows = a.N * a.Hkv * BS;
-    if (!pool_map(&kmap, a.k_cache, rows, BS) || !pool_map(&vmap, a.v_cache, rows, BS)) return cudaErrorInvalidValue;
+    if ((int64_t)a.N * a.Hkv * BS >= (int64_t)INT32_MAX) return cudaErrorInvalidValue;  // TMA coordinates
+    const int groups = a.N * a.Hkv * (BS / 8);
+    if (!pool_map(&kmap, a.k_cache, groups, BS) || !pool_map(&vmap, a.v_cache, groups, BS)) return cudaErrorInvalidValue;
     static std::atomic<bool> configured[64];  // per device: the shared-memory attribute is set
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
