@@ -61,6 +61,7 @@ struct Shared {
     uint64_t sfull[2], pfull[2], odone[2];      // per lane: S written, P written, P V done
     uint64_t qfull[2];                          // per lane: the unit's queries are staged
     uint64_t mlready, oread;                    // lanes joined: both (max, sum) and O in / read
+    uint64_t turn[2];                           // shared tiles: the lane may issue its next products
     uint64_t drain[2];
     int64_t total, first_tile;                  // of all tiles; of the first sequence
     int first_seq;
@@ -109,6 +110,8 @@ __device__ __forceinline__ void tma_block(uint32_t dst, const CUtensorMap *map, 
         "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(group), "r"(bar)
         : "memory");
 }
+
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // The next range of tiles of one (sequence, kv head) in a CTA's share.
 struct Walk {
@@ -166,6 +169,8 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
         }
         mbar_init_n(tc_smem(&sh.mlready), 2 * kLaneCols);
         mbar_init_n(tc_smem(&sh.oread), 2 * kLaneCols);
+        mbar_init(tc_smem(&sh.turn[0]));
+        mbar_init(tc_smem(&sh.turn[1]));
         mbar_init(tc_smem(&sh.drain[0]));
         mbar_init(tc_smem(&sh.drain[1]));
         sh.abort = 0;
@@ -254,7 +259,7 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
         int st = 0;
         uint32_t phase = 0;   // of the stage's next wait for `free`
         int issued = 0;
-        bool ok = true;
+        bool ok = true, first = true;
         auto fill = [&](const CUtensorMap *map, int y) {
             if (issued >= kStages) ok = wait_for(&sh.free[st], phase ^ 1, abort);
             ok = __all_sync(0xffffffffu, ok);
@@ -284,9 +289,19 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                 if (t < w.n && lane < kBlocks && idx < nblk && member == 0) raise_flag(a.err_flag, PA_FLAG_BLOCK_OUT_OF_RANGE);
                 return oob;
             };
-            // entries are loaded two tiles ahead of their copies
+            // With the ring's copies of all SMs queued up, a load that misses L2 takes several
+            // microseconds: the unit's table entries are fetched into L2 at its start (32 to a
+            // line) and loaded two tiles ahead of their copies, and the first unit's queries
+            // go before all copies but one.
+            for (int i = lane * 32; i < w.n * kBlocks; i += 32 * 32) prefetch_l2(table + min(w.t0 * kBlocks + i, nblk - 1));
             int y = row_of(0, entry(0)), e1 = entry(1), e2 = entry(2);
             fill(&kmap, y);
+            if (first) {
+                first = false;
+                ok = wait_for(&sh.qfull[0], 0, abort);
+                if (second(w) && ok) ok = wait_for(&sh.qfull[1], 0, abort);
+                ok = __all_sync(0xffffffffu, ok);
+            }
             for (int t = 0; ok && t < w.n; ++t) {
                 const int yn = row_of(t + 1, e1);
                 e1 = e2;
@@ -308,7 +323,7 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
         if (lane == 0) {
             const int l = warp - 9;
             int ring = 0;
-            uint32_t pv = 0, qs = 0;
+            uint32_t pv = 0, qs = 0, taken = 0;
             bool ok = true;
             const uint32_t t_s = tmem + kTmemS + l * 128, t_o = tmem + kTmemO + l * 128;
             const uint64_t qd = sw128_desc(tc_smem(smem + kOffQ + l * kTileBytes), 16, kGroup);
@@ -327,44 +342,59 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                     ring += 2 * w.n;
                     continue;
                 }
-                auto scores = [&](int t, bool first) {
-                    const int at = ring + k_at(t, w.n), st = at % kStages;
-                    // (the queries first: their lane has seen every earlier unit's end)
-                    if (first) ok = wait_for(&sh.qfull[l], qs++ & 1, abort);
-                    if (ok) ok = wait_for(&sh.full[at % kFull], (at / kFull) & 1, abort);
-                    // S overwrites P: the lane's last P V is done (this also orders O for its rows)
-                    if (ok && pv > 0) ok = wait_for(&sh.odone[l], (pv - 1) & 1, abort);
-                    if (!ok) return;
+                auto landed = [&](int at) { return wait_for(&sh.full[at % kFull], (at / kFull) & 1, abort); };
+                auto scores = [&](int at) {
                     tc_fence_after();
-                    const uint64_t k0 = kd + (uint64_t)(st * (kTileBytes >> 4));
+                    const uint64_t k0 = kd + (uint64_t)(at % kStages * (kTileBytes >> 4));
 #pragma unroll
                     for (int kk = 0; kk < kD / 16; ++kk) {
                         const uint64_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
                         umma(t_s, qd + off, k0 + off, bf16_idesc(128, kTile, 0), kk > 0);
                     }
                     umma_commit(sfull);
-                    umma_commit(tc_smem(&sh.free[st]));
                 };
-                auto weighted = [&](int t, bool first) {
-                    const int at = ring + v_at(t, w.n), st = at % kStages;
-                    ok = wait_for(&sh.full[at % kFull], (at / kFull) & 1, abort);
-                    if (ok) ok = wait_for(&sh.pfull[l], pv & 1, abort);
-                    if (!ok) return;
+                auto weighted = [&](int at, bool first) {
                     tc_fence_after();
-                    const uint64_t v0 = vd + (uint64_t)(st * (kTileBytes >> 4));
+                    const uint64_t v0 = vd + (uint64_t)(at % kStages * (kTileBytes >> 4));
 #pragma unroll
                     for (int kk = 0; kk < kTile / 16; ++kk)
                         umma_ts(t_o, t_s + kk * 8, v0 + (kk * 2 * kGroup >> 4), bf16_idesc(128, kD, 1), !first || kk > 0);
                     umma_commit(odone);
-                    umma_commit(tc_smem(&sh.free[st]));
                     ++pv;
                 };
                 constexpr int kStep = SPLIT ? 2 : 1;
                 const int t_first = SPLIT ? l : 0;
-                scores(t_first, true);
+                // Lanes that share their tiles take turns at the tensor cores, P V and the next
+                // S at a time: left alone they fall into step, both computing exponentials and
+                // then both waiting for products.  What a turn needs is waited for before it.
+                const bool turns = !SPLIT && second(w);
+                int k_pos = ring + k_at(t_first, w.n);
+                // (the queries first: their lane has seen every earlier unit's end)
+                ok = wait_for(&sh.qfull[l], qs++ & 1, abort) && landed(k_pos);
+                if (ok) {
+                    scores(k_pos);
+                    umma_commit(tc_smem(&sh.free[k_pos % kStages]));
+                }
                 for (int t = t_first; ok && t < w.n; t += kStep) {
-                    weighted(t, t == t_first);
-                    if (ok && t + kStep < w.n) scores(t + kStep, false);
+                    const bool more = t + kStep < w.n;
+                    const int v_pos = ring + v_at(t, w.n);
+                    k_pos = ring + k_at(t + kStep, w.n);
+                    ok = landed(v_pos) && (SPLIT || !more || landed(k_pos)) && wait_for(&sh.pfull[l], pv & 1, abort);
+                    if (ok && turns && (l == 1 || taken > 0)) ok = wait_for(&sh.turn[l], (l == 1 ? taken : taken - 1) & 1, abort);
+                    if (!ok) break;
+                    weighted(v_pos, t == t_first);
+                    // S overwrites P: P V is done first (this also orders O for its rows)
+                    if (more) {
+                        ok = wait_for(&sh.odone[l], (pv - 1) & 1, abort) && (!SPLIT || landed(k_pos));
+                        if (!ok) break;
+                        scores(k_pos);
+                    }
+                    if (turns) {
+                        mbar_arrive(tc_smem(&sh.turn[l ^ 1]));
+                        ++taken;
+                    }
+                    umma_commit(tc_smem(&sh.free[v_pos % kStages]));
+                    if (more) umma_commit(tc_smem(&sh.free[k_pos % kStages]));
                 }
                 ring += 2 * w.n;
             }
@@ -414,6 +444,15 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                     *reinterpret_cast<uint4 *>(qbuf + tile_chunk((warp & 3) * 32 + 2 * i + (lane >> 4), lane & 15)) = x[i];
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 mbar_arrive(tc_smem(&sh.qfull[l]));
+            }
+            // the next unit's queries into L2, long before they are loaded
+            {
+                Walk u = w;
+                if (u.next(a) && mine(u) && (SPLIT || l == 0 || second(u)) && c < u.ncols) {
+                    const uint16_t *src = a.q + ((int64_t)(u.r0 + tok) * a.Hq + u.kvh * a.G + head) * kD;
+                    prefetch_l2(src);
+                    prefetch_l2(src + 64);
+                }
             }
             // a warp none of whose columns is real keeps step without computing
             const bool idle = member * a.cols + (SPLIT ? 0 : l * kLaneCols) + (warp & 3) * 32 >= w.ncols;
