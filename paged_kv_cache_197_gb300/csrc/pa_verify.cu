@@ -9,6 +9,13 @@
 // The weights p - C q and their sums are carried as unevaluated pairs of fp32 (two-term
 // sums and products with their rounding errors): about 48 bits at fp32 rates, where GB300's
 // fp64 lanes (two per SM and clock) would take several times longer than the loads.
+//
+// A cluster of CTAs serves a sequence, each CTA a slice of the vocabulary and each warp an
+// equal run of it.  All CTAs walk the tree alike, from the tests' probabilities gathered for
+// all rows at once, and meet only for the sum of a pass: every CTA writes its part into the
+// others' shared memory, one cluster barrier, and each adds the parts in the same order, so
+// all decide the same.  The draw needs no further pass: the run that holds the target's
+// place is scanned by its warp.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -20,8 +27,10 @@
 namespace pa {
 namespace {
 
-constexpr int kThreads = 1024;
+// 256 threads: four CTAs per SM at 64 registers, so 64 sequences' clusters are all resident.
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;
 
 struct VerifyArgs {
     int32_t *tokens_out, *path, *n_out;
@@ -34,6 +43,8 @@ struct VerifyArgs {
     const int32_t *block_tables, *context_lens;
     int *err_flag;
     int T, V, W, M, bs, N;  // W: columns of tokens_out and path
+    int cluster, run;       // CTAs per sequence; vocabulary entries per warp (a multiple of 8)
+    int vector;             // rows are 16-byte aligned
 };
 
 __device__ __forceinline__ void raise_flag(int *err_flag, int bit) {
@@ -41,14 +52,27 @@ __device__ __forceinline__ void raise_flag(int *err_flag, int bit) {
 }
 
 // A probability: negative and NaN entries count as 0.
+__device__ __forceinline__ float prob(const float *row, int64_t v) { return fmaxf(__ldg(row + v), 0.f); }
+__device__ __forceinline__ float prob(const uint16_t *row, int64_t v) {
+    return fmaxf(__uint_as_float((uint32_t)__ldg(row + v) << 16), 0.f);
+}
+
+// Entries of one 16-byte load.
 template <typename T>
-__device__ __forceinline__ float prob(const T *row, int64_t v) {
-    float x;
-    if constexpr (sizeof(T) == 4)
-        x = row[v];
-    else
-        x = __uint_as_float((uint32_t)row[v] << 16);
-    return x > 0.f ? x : 0.f;
+constexpr int kVec = 16 / sizeof(T);
+__device__ __forceinline__ void unpack(const uint4 &w, float (&x)[4]) {
+    x[0] = fmaxf(__uint_as_float(w.x), 0.f);
+    x[1] = fmaxf(__uint_as_float(w.y), 0.f);
+    x[2] = fmaxf(__uint_as_float(w.z), 0.f);
+    x[3] = fmaxf(__uint_as_float(w.w), 0.f);
+}
+__device__ __forceinline__ void unpack(const uint4 &w, float (&x)[8]) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = fmaxf(__uint_as_float(u[i] << 16), 0.f);
+        x[2 * i + 1] = fmaxf(__uint_as_float(u[i] & 0xffff0000u), 0.f);
+    }
 }
 
 // An unevaluated sum of two fp32, |lo| <= ulp(hi) / 2 up to a few roundings.
@@ -61,12 +85,12 @@ __device__ __forceinline__ Pair split(double x) {
     return {hi, (float)(x - (double)hi)};
 }
 
-// max(p - C q, 0) as a pair.  C q = h + e exactly (e the product's rounding error), p - h is
-// a two-term difference with its error; C.lo q is below ulp(h) / 2.
+// max(p - C q, 0) as a pair.  C.hi q = h + e exactly (e the product's rounding error), p - h
+// is a two-term difference with its error; C.lo q is below ulp(h) / 2.
 __device__ __forceinline__ Pair residual(float p, float q, Pair C) {
     const float h = __fmul_rn(C.hi, q), e = __fmaf_rn(C.hi, q, -h);
     const float d = __fsub_rn(p, h), b = __fsub_rn(p, d);
-    float lo = __fadd_rn(__fsub_rn(__fsub_rn(p, __fadd_rn(d, b)), __fsub_rn(h, b)), 0.f);
+    float lo = __fsub_rn(__fsub_rn(p, __fadd_rn(d, b)), __fsub_rn(h, b));
     lo = __fsub_rn(__fsub_rn(lo, e), __fmul_rn(C.lo, q));
     const float hi = __fadd_rn(d, lo);
     lo = __fsub_rn(lo, __fsub_rn(hi, d));
@@ -81,169 +105,329 @@ __device__ __forceinline__ void add(Pair &s, Pair x) {
     s.hi = t;
 }
 
+__device__ __forceinline__ double value(Pair x) { return (double)x.hi + (double)x.lo; }
+
+__device__ __forceinline__ double warp_sum(double x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// Inclusive sums over the lanes.
+__device__ __forceinline__ double warp_scan(double x, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const double y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    return x;
+}
+
+struct Shared {
+    double part[2][kMaxCluster];            // the CTAs' sums of a pass, by its parity
+    double run[kWarps];                     // the warps' sums of the last pass
+    double tp[PA_TREE_MAX_NODES], tq[PA_TREE_MAX_NODES];  // p and q of each row's token at its parent
+    int parent[PA_TREE_MAX_NODES], token[PA_TREE_MAX_NODES], place[PA_TREE_MAX_NODES];
+    float u[PA_TREE_MAX_NODES];
+    int gone[PA_TREE_MAX_NODES];            // the current node's rejected tokens (no drafter)
+};
+
+// A node's residual: its rows of p and q, C, and (no drafter) the tokens rejected.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant__ VerifyArgs a) {
-    __shared__ double s_sum[kWarps];
-    __shared__ int s_parent[PA_TREE_MAX_NODES], s_place[PA_TREE_MAX_NODES];
-    __shared__ int s_next;
+struct Residual {
+    const T *p, *q;  // q null: R is p without the tokens gone
+    Pair c;
+    const int *gone;
+    int n_gone;
+
+    __device__ __forceinline__ Pair operator()(int64_t v) const {
+        const float x = prob(p, v);
+        if (q) return residual(x, prob(q, v), c);
+        for (int i = 0; i < n_gone; ++i)
+            if (gone[i] == (int)v) return {0.f, 0.f};
+        return {x, 0.f};
+    }
+};
+
+// The sum of R over a warp's run [begin, end).
+template <typename T>
+__device__ __forceinline__ double run_sum(const Residual<T> &R, int64_t begin, int64_t end, bool vector, int lane) {
+    constexpr int N = kVec<T>;
+    Pair s{0.f, 0.f};
+    bool plain = true;  // no token of the run is gone
+    if (!R.q) {
+        bool in = false;
+        for (int i = lane; i < R.n_gone; i += 32) in |= R.gone[i] >= begin && R.gone[i] < end;
+        plain = !__any_sync(0xffffffffu, in);
+    }
+    int64_t v = begin;
+    if (vector && plain) {
+        constexpr int U = 4;  // loads in flight per operand
+        for (; v + 32 * N * U <= end; v += 32 * N * U) {
+            uint4 a[U], b[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                a[i] = __ldg(reinterpret_cast<const uint4 *>(R.p + v + (i * 32 + lane) * N));
+                if (R.q) b[i] = __ldg(reinterpret_cast<const uint4 *>(R.q + v + (i * 32 + lane) * N));
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                float x[N], y[N];
+                unpack(a[i], x);
+                if (R.q) unpack(b[i], y);
+#pragma unroll
+                for (int e = 0; e < N; ++e) add(s, R.q ? residual(x[e], y[e], R.c) : Pair{x[e], 0.f});
+            }
+        }
+    }
+    if (plain) {
+        constexpr int U = 8;
+        for (; v + 32 * U <= end; v += 32 * U) {
+            float x[U], y[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                x[i] = prob(R.p, v + i * 32 + lane);
+                if (R.q) y[i] = prob(R.q, v + i * 32 + lane);
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i) add(s, R.q ? residual(x[i], y[i], R.c) : Pair{x[i], 0.f});
+        }
+    }
+    for (v += lane; v < end; v += 32) add(s, R(v));
+    return warp_sum(value(s));
+}
+
+// The first v of a warp's run whose running sum, from `at`, exceeds the target; the last v
+// with weight where rounding leaves none; -1 if none has weight.
+template <typename T>
+__device__ __forceinline__ int run_find(const Residual<T> &R, int64_t begin, int64_t end, double at, double target, int lane) {
+    // lanes sum consecutive pieces, the piece that passes the target is scanned by the warp
+    const int64_t piece = (end - begin + 31) / 32;
+    const int64_t b0 = min(end, begin + lane * piece), b1 = min(end, b0 + piece);
+    Pair s{0.f, 0.f};
+#pragma unroll 8
+    for (int64_t v = b0; v < b1; ++v) add(s, R(v));
+    const double mine = value(s), upto = warp_scan(mine, lane);
+    unsigned hit = __ballot_sync(0xffffffffu, mine > 0.0 && at + upto > target);
+    const unsigned any = __ballot_sync(0xffffffffu, mine > 0.0);
+    if (!any) return -1;
+    const int from = hit ? __ffs(hit) - 1 : 31 - __clz(any);
+    at += __shfl_sync(0xffffffffu, upto - mine, from);
+    const int64_t p0 = min(end, begin + from * piece), p1 = min(end, p0 + piece);
+    int last = -1;
+    for (int64_t v0 = p0; v0 < p1; v0 += 32) {
+        const int64_t v = v0 + lane;
+        const double w = v < p1 ? value(R(v)) : 0.0, scan = warp_scan(w, lane);
+        hit = __ballot_sync(0xffffffffu, w > 0.0 && at + scan > target);
+        if (hit) return (int)(v0 + __ffs(hit) - 1);
+        const unsigned pos = __ballot_sync(0xffffffffu, w > 0.0);
+        if (pos) last = (int)(v0 + 31 - __clz(pos));
+        at += __shfl_sync(0xffffffffu, scan, 31);
+    }
+    return last;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_constant__ VerifyArgs a) {
+    __shared__ Shared sh;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int s = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int s = blockIdx.x / a.cluster, rank = blockIdx.x % a.cluster;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int r0 = a.query_start[s], r1 = a.query_start[s + 1], L = r1 - r0;
-    for (int j = tid; j < a.W; j += kThreads) a.tokens_out[(int64_t)s * a.W + j] = a.path[(int64_t)s * a.W + j] = -1;
+    int32_t *tokens_out = a.tokens_out + (int64_t)s * a.W, *path = a.path + (int64_t)s * a.W;
     const bool offsets = r0 >= 0 && r1 <= a.T && L >= 0 && L <= a.W;
+    const T *P = static_cast<const T *>(a.p), *Q = static_cast<const T *>(a.q);
     bool bad = false;
     if (offsets)
         for (int j = tid; j < L; j += kThreads) {
-            s_parent[j] = a.parents[r0 + j];
-            s_place[j] = -1;
-            bad |= s_parent[j] < -1 || s_parent[j] >= j;
+            const int p = a.parents[r0 + j], x = j ? a.tokens[r0 + j] : -1;
+            bad |= p < -1 || p >= j;
+            sh.parent[j] = p;
+            sh.token[j] = x;
+            sh.place[j] = j ? -1 : 0;
+            sh.u[j] = j ? a.u[r0 + j] : 0.f;
+            // every test needs p and q at the row's token, at its parent
+            double tp = 0.0, tq = 0.0;
+            if (p >= 0 && p < j && x >= 0 && x < a.V) {
+                tp = prob(P + (r0 + p) * a.p_stride, x);
+                tq = Q ? prob(Q + (r0 + p) * a.q_stride, x) : 1.0;
+            }
+            sh.tp[j] = tp;
+            sh.tq[j] = tq;
         }
     bad = __syncthreads_or(bad);
-    if (!offsets || bad || L == 0) {
-        if (tid == 0) {
-            a.n_out[s] = 0;
-            if (!offsets) raise_flag(a.err_flag, PA_FLAG_QUERY_OUT_OF_RANGE);
-            if (bad) raise_flag(a.err_flag, PA_FLAG_TREE_PARENT);
+    if (!offsets || bad || L == 0) {  // every CTA of the cluster alike
+        if (rank == 0) {
+            for (int j = tid; j < a.W; j += kThreads) tokens_out[j] = path[j] = -1;
+            if (offsets && a.slots)
+                for (int j = tid; j < L; j += kThreads) a.slots[r0 + j] = -1;
+            if (tid == 0) {
+                a.n_out[s] = 0;
+                if (!offsets) raise_flag(a.err_flag, PA_FLAG_QUERY_OUT_OF_RANGE);
+                if (bad) raise_flag(a.err_flag, PA_FLAG_TREE_PARENT);
+            }
         }
-        if (offsets && a.slots)
-            for (int j = tid; j < L; j += kThreads) a.slots[r0 + j] = -1;
         return;
     }
-    const T *P = static_cast<const T *>(a.p), *Q = static_cast<const T *>(a.q);
-    int cur = 0, n = 1, rejected = 0;  // rejected children of cur
-    double C = 0.0, Z = 1.0;
-    // the mass of R = max(p - C q, 0), or of p without the rejected children of cur
-    auto weight = [&](const T *pr, const T *qr, Pair c, int v) -> Pair {
-        const float p = prob(pr, v);
-        if (qr) return residual(p, prob(qr, v), c);
-        return {p, 0.f};
-    };
-    auto is_rejected = [&](int v, int before) {  // one-hot drafts: v a child of cur tried before row `before`
-        for (int j = cur + 1; j < before; ++j)
-            if (s_parent[j] == cur && a.tokens[r0 + j] == v) return true;
-        return false;
-    };
-    auto mass = [&](int before) -> double {
-        const T *pr = P + (r0 + cur) * a.p_stride, *qr = Q && rejected ? Q + (r0 + cur) * a.q_stride : nullptr;
-        const Pair c = split(C);
-        Pair sum{0.f, 0.f};
-        for (int v = tid; v < a.V; v += kThreads) {
-            if (!Q && rejected && is_rejected(v, before)) continue;
-            add(sum, weight(pr, qr, c, v));
+    const int64_t begin = min((int64_t)a.V, ((int64_t)rank * kWarps + warp) * a.run), end = min((int64_t)a.V, begin + a.run);
+    int pass = 0;
+    double total = 0.0;
+    // one pass: the sum of R over the vocabulary; sh.run and sh.part keep its pieces
+    auto mass = [&](const Residual<T> &R) {
+        const double d = run_sum(R, begin, end, a.vector != 0, lane);
+        __syncthreads();  // the last pass's pieces have been read
+        if (lane == 0) sh.run[warp] = d;
+        __syncthreads();
+        double *part = sh.part[pass & 1];
+        if (tid < a.cluster) {
+            double mine = 0.0;
+            for (int w = 0; w < kWarps; ++w) mine += sh.run[w];
+            uint32_t to = (uint32_t)__cvta_generic_to_shared(part + rank);
+            asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(to) : "r"(tid));
+            asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(to), "d"(mine) : "memory");
         }
-        double d = (double)sum.hi + (double)sum.lo;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-        __syncthreads();
-        if (lane == 0) s_sum[warp] = d;
-        __syncthreads();
-        d = 0.0;
-        for (int w = 0; w < kWarps; ++w) d += s_sum[w];
-        return d;
-    };
-    if (tid == 0) s_place[0] = 0;
-    for (int j = 1; j < L; ++j) {  // children come after their parent, and in the order they are tried
-        if (s_parent[j] != cur) continue;
-        const int x = a.tokens[r0 + j];
-        bool yes = false;
-        if (x < 0 || x >= a.V) {
-            if (tid == 0) raise_flag(a.err_flag, PA_FLAG_TOKEN_OUT_OF_RANGE);
+        if (a.cluster > 1) {
+            asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
         } else {
-            const double p = prob(P + (r0 + cur) * a.p_stride, x);
-            const double q = Q ? prob(Q + (r0 + cur) * a.q_stride, x) : 1.0;
-            const double R = Q ? fmax(p - C * q, 0.0) : (rejected && is_rejected(x, j) ? 0.0 : p);
-            yes = (double)a.u[r0 + j] * Z * q < R;
+            __syncthreads();
         }
-        if (yes) {
-            cur = j;
+        total = 0.0;
+        for (int c = 0; c < a.cluster; ++c) total += part[c];
+        ++pass;
+    };
+    // ---- the walk: every warp follows it alike; a row is tested after its parent and its
+    // older siblings
+    int cur = 0, n = 1, rejected = 0;
+    double C = 0.0, Z = 1.0;
+    bool fresh = false;  // `total` and the pieces are of the current residual
+    auto node = [&](int k) {
+        Residual<T> R;
+        R.p = P + (r0 + cur) * a.p_stride;
+        R.q = Q && k > 0 ? Q + (r0 + cur) * a.q_stride : nullptr;
+        R.c = split(C);
+        R.gone = sh.gone;
+        R.n_gone = Q ? 0 : k;
+        return R;
+    };
+    for (int j = 1;;) {
+        // the next child of cur from row j on
+        int at = L;
+        for (int base = j & ~31; base < L; base += 32) {
+            const int i = base + lane;
+            const unsigned m = __ballot_sync(0xffffffffu, i >= j && i < L && sh.parent[i] == cur);
+            if (m) {
+                at = base + __ffs(m) - 1;
+                break;
+            }
+        }
+        if (at >= L) break;
+        j = at + 1;
+        const int x = sh.token[at];
+        double R = sh.tp[at];
+        const double q = sh.tq[at];
+        bool again = false;  // no drafter: the token was rejected before
+        if (Q) {
+            R = fmax(R - C * q, 0.0);
+        } else {
+            for (int i = 0; i < rejected; ++i) again |= sh.gone[i] == x;
+            if (again) R = 0.0;
+        }
+        const bool inside = x >= 0 && x < a.V;
+        if (!inside && rank == 0 && tid == 0) raise_flag(a.err_flag, PA_FLAG_TOKEN_OUT_OF_RANGE);
+        if (inside && (double)sh.u[at] * Z * q < R) {
+            cur = at;
             C = 0.0;
             Z = 1.0;
             rejected = 0;
-            if (tid == 0) s_place[j] = n;
+            fresh = false;
+            __syncthreads();  // gone has been read
+            if (tid == 0) sh.place[at] = n;
             ++n;
+            continue;
+        }
+        C += Z;
+        if (!Q) {
+            __syncthreads();
+            if (tid == 0) sh.gone[rejected] = x;
+            __syncthreads();
+        }
+        ++rejected;
+        // Without a drafter the mass after the first rejection falls by what is rejected: no
+        // pass while the difference keeps its digits.
+        const double less = Z - R;
+        if (!Q && rejected > 1 && less > 1e-6) {
+            Z = less;
+            fresh = again && fresh;
         } else {
-            ++rejected;
-            C += Z;
-            Z = mass(j + 1);
+            mass(node(rejected));
+            Z = total;
+            fresh = true;
         }
     }
-    // the next token: the first v whose running sum of R exceeds u Z
-    double total = rejected ? Z : mass(0);
+    // ---- the draw: the first v whose running sum of R exceeds u total
+    if (!fresh) mass(node(rejected));
     if (rejected && !(total > 0.0)) {  // nothing left: the target's own row
         rejected = 0;
         C = 0.0;
-        total = mass(0);
+        mass(node(0));
     }
-    int next = -1;
-    if (total > 0.0 && total <= 1.7e308) {
-        const T *pr = P + (r0 + cur) * a.p_stride, *qr = Q && rejected ? Q + (r0 + cur) * a.q_stride : nullptr;
-        const Pair c = split(C);
+    const bool drawn = total > 0.0 && total <= 1.7e308;
+    if (!drawn) {
+        if (rank == 0 && tid == 0) {
+            raise_flag(a.err_flag, PA_FLAG_PROBABILITY);
+            tokens_out[n - 1] = -1;
+        }
+    } else {
         const double target = (double)a.u_final[s] * total;
-        // each warp sums an equal run of the vocabulary; the run that passes the target is
-        // scanned by its warp
-        const int run = (a.V + kWarps - 1) / kWarps, begin = min(a.V, warp * run), end = min(a.V, begin + run);
-        auto weigh = [&](int v) -> double {
-            if (!Q && rejected && is_rejected(v, L)) return 0.0;
-            const Pair w = weight(pr, qr, c, v);
-            return (double)w.hi + (double)w.lo;
-        };
-        double d = 0.0;
-        int last = -1;  // the last v with any weight
-        for (int v = begin + lane; v < end; v += 32) {
-            const double w = weigh(v);
-            d += w;
-            if (w > 0.0) last = v;
+        const double *part = sh.part[(pass - 1) & 1];
+        double before = 0.0, from = 0.0;
+        int owner = -1, last = 0;
+        for (int c = 0; c < a.cluster; ++c) {
+            if (part[c] > 0.0) last = c;
+            if (owner < 0 && before + part[c] > target) {
+                owner = c;
+                from = before;
+            }
+            before += part[c];
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            d += __shfl_xor_sync(0xffffffffu, d, o);
-            last = max(last, __shfl_xor_sync(0xffffffffu, last, o));
+        if (owner < 0) {  // a number of 1 or more: the last entry with weight
+            owner = last;
+            from = before;
         }
-        __syncthreads();
-        if (lane == 0) s_sum[warp] = d;
-        if (tid == 0) s_next = -1;
-        __syncthreads();
-        double before = 0.0;
-        for (int w = 0; w < warp; ++w) before += s_sum[w];
-        if (last >= 0) atomicMax(&s_next, last);
-        __syncthreads();
-        const int fallback = s_next;
-        __syncthreads();
-        if (tid == 0) s_next = 0x7fffffff;
-        __syncthreads();
-        if (before <= target && before + d > target) {
-            double at = before;
-            for (int v0 = begin; v0 < end; v0 += 32) {
-                const int v = v0 + lane;
-                double w = v < end ? weigh(v) : 0.0, scan = w;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const double y = __shfl_up_sync(0xffffffffu, scan, o);
-                    if (lane >= o) scan += y;
+        if (owner == rank) {
+            int mine = -1;
+            last = 0;
+            double at = from, start = from;
+            for (int w = 0; w < kWarps; ++w) {
+                if (sh.run[w] > 0.0) last = w;
+                if (mine < 0 && at + sh.run[w] > target) {
+                    mine = w;
+                    start = at;
                 }
-                const unsigned hit = __ballot_sync(0xffffffffu, w > 0.0 && at + scan > target);
-                if (hit) {
-                    if (lane == 0) atomicMin(&s_next, v0 + __ffs(hit) - 1);
-                    break;
-                }
-                at += __shfl_sync(0xffffffffu, scan, 31);
+                at += sh.run[w];
+            }
+            if (mine < 0) {
+                mine = last;
+                start = at;
+            }
+            if (warp == mine) {
+                const int v = run_find(node(rejected), begin, end, start, target, lane);
+                if (lane == 0) tokens_out[n - 1] = v;
             }
         }
-        __syncthreads();
-        next = s_next == 0x7fffffff ? fallback : s_next;
-    } else if (tid == 0) {
-        raise_flag(a.err_flag, PA_FLAG_PROBABILITY);
     }
+    // ---- the branch
+    if (rank != 0) return;
+    for (int j = n + tid; j < a.W; j += kThreads) tokens_out[j] = path[j] = -1;
     __syncthreads();
     if (tid == 0) a.n_out[s] = n;
     for (int j = tid; j < L; j += kThreads) {
-        const int place = s_place[j];
+        const int place = sh.place[j];
         int64_t slot = -1;
         if (place >= 0) {
-            a.path[(int64_t)s * a.W + place] = r0 + j;
-            if (place > 0) a.tokens_out[(int64_t)s * a.W + place - 1] = a.tokens[r0 + j];
-            if (place == n - 1) a.tokens_out[(int64_t)s * a.W + place] = next;
+            path[place] = r0 + j;
+            if (place > 0) tokens_out[place - 1] = sh.token[j];
             if (a.slots) {
                 const int64_t pos = (int64_t)max(a.context_lens[s], 0) + place;
                 const int b = pos / a.bs < a.M ? a.block_tables[(int64_t)s * a.M + pos / a.bs] : -1;
@@ -255,6 +439,23 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
         }
         if (a.slots) a.slots[r0 + j] = slot;
     }
+}
+
+template <typename T>
+cudaError_t launch_verify(const VerifyArgs &a, int S, cudaStream_t stream) {
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = a.cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)S * a.cluster);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, verify_kernel<T>, a);
 }
 
 }  // namespace
@@ -316,7 +517,14 @@ extern "C" pa_status pa_verify_tree(int32_t *tokens_out, int32_t *path, int32_t 
     a.M = M;
     a.bs = bs;
     a.N = N;
-    launch_dependent(prob_dtype == PA_PROB_F32 ? verify_kernel<float> : verify_kernel<uint16_t>, dim3(S), dim3(kThreads), 0,
-                     (cudaStream_t)stream, a);
+    // small vocabularies: one CTA, whose sums need no cluster barrier
+    a.cluster = V > 8192 ? kMaxCluster : 1;
+    const int64_t runs = (int64_t)a.cluster * kWarps;
+    a.run = (int)align_up((size_t)((V + runs - 1) / runs), 8);
+    const int64_t elem = prob_dtype == PA_PROB_F32 ? 4 : 2;
+    auto rows16 = [&](const void *p, int64_t stride) { return aligned16(p) && stride * elem % 16 == 0; };
+    a.vector = rows16(target_probs, target_stride) && (!draft_probs || rows16(draft_probs, draft_stride));
+    prob_dtype == PA_PROB_F32 ? launch_verify<float>(a, S, (cudaStream_t)stream)
+                              : launch_verify<uint16_t>(a, S, (cudaStream_t)stream);
     return check_launch(fn);
 }
