@@ -107,10 +107,13 @@ __device__ __forceinline__ void add(Pair &s, Pair x) {
 
 __device__ __forceinline__ double value(Pair x) { return (double)x.hi + (double)x.lo; }
 
-__device__ __forceinline__ double warp_sum(double x) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
+// The sum over the first `lanes` (a power of two) lanes' pairs, in each of them.
+__device__ __forceinline__ Pair lanes_sum(Pair s, int lanes) {
+    for (int o = lanes / 2; o > 0; o >>= 1) {
+        const Pair x{__shfl_xor_sync(0xffffffffu, s.hi, o), __shfl_xor_sync(0xffffffffu, s.lo, o)};
+        add(s, x);
+    }
+    return s;
 }
 
 // Inclusive sums over the lanes.
@@ -123,10 +126,21 @@ __device__ __forceinline__ double warp_scan(double x, int lane) {
     return x;
 }
 
+// What the first warp asks of all: a pass over the node's residual, or nothing more.
+struct Task {
+    int cur, rejected;  // the node and its rejected children
+    Pair c;
+    int more;
+    int n;              // rows on the path so far
+};
+
 struct Shared {
-    double part[2][kMaxCluster];            // the CTAs' sums of a pass, by its parity
-    double run[kWarps];                     // the warps' sums of the last pass
-    double tp[PA_TREE_MAX_NODES], tq[PA_TREE_MAX_NODES];  // p and q of each row's token at its parent
+    Pair part[2][kMaxCluster];              // the CTAs' sums of a pass, by its parity
+    Pair run[kWarps];                       // the warps' sums of the last pass
+    double from, target;                    // the draw: R's sum before the owner's run, and its place
+    int owner_run;                          // the run of this CTA that holds it, or -1
+    Task task;
+    float tp[PA_TREE_MAX_NODES], tq[PA_TREE_MAX_NODES];  // p and q of each row's token at its parent
     int parent[PA_TREE_MAX_NODES], token[PA_TREE_MAX_NODES], place[PA_TREE_MAX_NODES];
     float u[PA_TREE_MAX_NODES];
     int gone[PA_TREE_MAX_NODES];            // the current node's rejected tokens (no drafter)
@@ -150,12 +164,12 @@ struct Residual {
 };
 
 // The sum of R over a warp's run [begin, end).
-template <typename T>
-__device__ __forceinline__ double run_sum(const Residual<T> &R, int64_t begin, int64_t end, bool vector, int lane) {
+template <typename T, bool DRAFTED>
+__device__ __forceinline__ Pair run_sum(const Residual<T> &R, int64_t begin, int64_t end, bool vector, int lane) {
     constexpr int N = kVec<T>;
     Pair s{0.f, 0.f};
     bool plain = true;  // no token of the run is gone
-    if (!R.q) {
+    if (!DRAFTED && R.n_gone > 0) {
         bool in = false;
         for (int i = lane; i < R.n_gone; i += 32) in |= R.gone[i] >= begin && R.gone[i] < end;
         plain = !__any_sync(0xffffffffu, in);
@@ -168,15 +182,15 @@ __device__ __forceinline__ double run_sum(const Residual<T> &R, int64_t begin, i
 #pragma unroll
             for (int i = 0; i < U; ++i) {
                 a[i] = __ldg(reinterpret_cast<const uint4 *>(R.p + v + (i * 32 + lane) * N));
-                if (R.q) b[i] = __ldg(reinterpret_cast<const uint4 *>(R.q + v + (i * 32 + lane) * N));
+                if (DRAFTED) b[i] = __ldg(reinterpret_cast<const uint4 *>(R.q + v + (i * 32 + lane) * N));
             }
 #pragma unroll
             for (int i = 0; i < U; ++i) {
                 float x[N], y[N];
                 unpack(a[i], x);
-                if (R.q) unpack(b[i], y);
+                if (DRAFTED) unpack(b[i], y);
 #pragma unroll
-                for (int e = 0; e < N; ++e) add(s, R.q ? residual(x[e], y[e], R.c) : Pair{x[e], 0.f});
+                for (int e = 0; e < N; ++e) add(s, DRAFTED ? residual(x[e], y[e], R.c) : Pair{x[e], 0.f});
             }
         }
     }
@@ -187,44 +201,70 @@ __device__ __forceinline__ double run_sum(const Residual<T> &R, int64_t begin, i
 #pragma unroll
             for (int i = 0; i < U; ++i) {
                 x[i] = prob(R.p, v + i * 32 + lane);
-                if (R.q) y[i] = prob(R.q, v + i * 32 + lane);
+                if (DRAFTED) y[i] = prob(R.q, v + i * 32 + lane);
             }
 #pragma unroll
-            for (int i = 0; i < U; ++i) add(s, R.q ? residual(x[i], y[i], R.c) : Pair{x[i], 0.f});
+            for (int i = 0; i < U; ++i) add(s, DRAFTED ? residual(x[i], y[i], R.c) : Pair{x[i], 0.f});
         }
     }
     for (v += lane; v < end; v += 32) add(s, R(v));
-    return warp_sum(value(s));
+    return lanes_sum(s, 32);
 }
 
 // The first v of a warp's run whose running sum, from `at`, exceeds the target; the last v
-// with weight where rounding leaves none; -1 if none has weight.
+// with weight where rounding leaves none; -1 if none has weight.  Groups of 128 entries are
+// summed by the warp, four to a lane, lane g keeping the sum of group g; the group that
+// passes the target is scanned.
 template <typename T>
 __device__ __forceinline__ int run_find(const Residual<T> &R, int64_t begin, int64_t end, double at, double target, int lane) {
-    // lanes sum consecutive pieces, the piece that passes the target is scanned by the warp
-    const int64_t piece = (end - begin + 31) / 32;
-    const int64_t b0 = min(end, begin + lane * piece), b1 = min(end, b0 + piece);
-    Pair s{0.f, 0.f};
-#pragma unroll 8
-    for (int64_t v = b0; v < b1; ++v) add(s, R(v));
-    const double mine = value(s), upto = warp_scan(mine, lane);
-    unsigned hit = __ballot_sync(0xffffffffu, mine > 0.0 && at + upto > target);
-    const unsigned any = __ballot_sync(0xffffffffu, mine > 0.0);
-    if (!any) return -1;
-    const int from = hit ? __ffs(hit) - 1 : 31 - __clz(any);
-    at += __shfl_sync(0xffffffffu, upto - mine, from);
-    const int64_t p0 = min(end, begin + from * piece), p1 = min(end, p0 + piece);
-    int last = -1;
-    for (int64_t v0 = p0; v0 < p1; v0 += 32) {
-        const int64_t v = v0 + lane;
-        const double w = v < p1 ? value(R(v)) : 0.0, scan = warp_scan(w, lane);
-        hit = __ballot_sync(0xffffffffu, w > 0.0 && at + scan > target);
-        if (hit) return (int)(v0 + __ffs(hit) - 1);
-        const unsigned pos = __ballot_sync(0xffffffffu, w > 0.0);
-        if (pos) last = (int)(v0 + 31 - __clz(pos));
-        at += __shfl_sync(0xffffffffu, scan, 31);
+    int64_t group = -1, last_group = -1;  // first entry of the group that passes; of the last with weight
+    double last_at = at;
+    for (int64_t v0 = begin; v0 < end && group < 0; v0 += 32 * 128) {
+        Pair mine{0.f, 0.f};
+#pragma unroll 4
+        for (int g = 0; g < 32; ++g) {
+            const int64_t v = v0 + g * 128 + lane * 4;
+            if (v0 + g * 128 >= end) break;
+            Pair s{0.f, 0.f};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (v + e < end) add(s, R(v + e));
+            s = lanes_sum(s, 32);
+            if (lane == g) mine = s;
+        }
+        const double w = value(mine), upto = warp_scan(w, lane);
+        const unsigned hit = __ballot_sync(0xffffffffu, w > 0.0 && at + upto > target);
+        const unsigned any = __ballot_sync(0xffffffffu, w > 0.0);
+        if (any) {
+            const int g = hit ? __ffs(hit) - 1 : 31 - __clz(any);
+            const double before = at + __shfl_sync(0xffffffffu, upto - w, g);
+            last_group = v0 + g * 128;
+            last_at = before;
+            if (hit) group = last_group;
+        }
+        at += __shfl_sync(0xffffffffu, upto, 31);
     }
-    return last;
+    if (last_group < 0) return -1;
+    double w[4], sum = 0.0;
+    const int64_t v = last_group + lane * 4;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        w[e] = v + e < end ? value(R(v + e)) : 0.0;
+        sum += w[e];
+    }
+    const double upto = warp_scan(sum, lane);
+    double run = last_at + (upto - sum);
+    int first = 4, last = -1;  // of this lane's entries: the first past the target, the last with weight
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        run += w[e];
+        if (w[e] > 0.0) last = e;
+        if (first == 4 && w[e] > 0.0 && run > target) first = e;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, first < 4), any = __ballot_sync(0xffffffffu, last >= 0);
+    const int from = hit ? __ffs(hit) - 1 : 31 - __clz(any);
+    const int e = __shfl_sync(0xffffffffu, hit ? first : last, from);
+    return (int)(last_group + from * 4 + e);
 }
 
 template <typename T>
@@ -248,10 +288,10 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
             sh.place[j] = j ? -1 : 0;
             sh.u[j] = j ? a.u[r0 + j] : 0.f;
             // every test needs p and q at the row's token, at its parent
-            double tp = 0.0, tq = 0.0;
+            float tp = 0.f, tq = 0.f;
             if (p >= 0 && p < j && x >= 0 && x < a.V) {
                 tp = prob(P + (r0 + p) * a.p_stride, x);
-                tq = Q ? prob(Q + (r0 + p) * a.q_stride, x) : 1.0;
+                tq = Q ? prob(Q + (r0 + p) * a.q_stride, x) : 1.f;
             }
             sh.tp[j] = tp;
             sh.tq[j] = tq;
@@ -271,156 +311,152 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
         return;
     }
     const int64_t begin = min((int64_t)a.V, ((int64_t)rank * kWarps + warp) * a.run), end = min((int64_t)a.V, begin + a.run);
-    int pass = 0;
-    double total = 0.0;
-    // one pass: the sum of R over the vocabulary; sh.run and sh.part keep its pieces
-    auto mass = [&](const Residual<T> &R) {
-        const double d = run_sum(R, begin, end, a.vector != 0, lane);
-        __syncthreads();  // the last pass's pieces have been read
+    // ---- the walk, in the first warp (fp64 is scarce: two lanes per SM and clock); the other
+    // warps join it for the passes.  A row is tested after its parent and its older siblings.
+    int cur = 0, n = 1, rejected = 0, j = 1, pass = 0;
+    double C = 0.0, Z = 1.0, total = 0.0;
+    bool fresh = false;  // `total` is of the current residual
+    Task task;
+    for (;;) {
+        if (warp == 0) {
+            bool need = false;
+            if (pass > 0) {  // back from a pass
+                total = value(lanes_sum(lane < a.cluster ? sh.part[(pass - 1) & 1][lane] : Pair{0.f, 0.f}, kMaxCluster));
+                total = __shfl_sync(0xffffffffu, total, 0);
+                if (rejected) Z = total;
+                fresh = true;
+            }
+            while (!need && j < L) {
+                // the next child of cur from row j on
+                int at = L;
+                for (int base = j & ~31; base < L; base += 32) {
+                    const int i = base + lane;
+                    const unsigned m = __ballot_sync(0xffffffffu, i >= j && i < L && sh.parent[i] == cur);
+                    if (m) {
+                        at = base + __ffs(m) - 1;
+                        break;
+                    }
+                }
+                j = at + 1;
+                if (at >= L) break;
+                const int x = sh.token[at];
+                const double q = sh.tq[at];
+                double R = sh.tp[at];
+                bool again = false;  // no drafter: the token was rejected before
+                if (Q) {
+                    R = fmax(R - C * q, 0.0);
+                } else {
+                    for (int i = 0; i < rejected; ++i) again |= sh.gone[i] == x;
+                    if (again) R = 0.0;
+                }
+                const bool inside = x >= 0 && x < a.V;
+                if (!inside && rank == 0 && lane == 0) raise_flag(a.err_flag, PA_FLAG_TOKEN_OUT_OF_RANGE);
+                if (inside && (double)sh.u[at] * Z * q < R) {
+                    cur = at;
+                    C = 0.0;
+                    Z = 1.0;
+                    rejected = 0;
+                    fresh = false;
+                    if (lane == 0) sh.place[at] = n;
+                    ++n;
+                    continue;
+                }
+                C += Z;
+                __syncwarp();
+                if (!Q && lane == 0) sh.gone[rejected] = x;
+                __syncwarp();
+                ++rejected;
+                // Without a drafter the mass after the first rejection falls by what is
+                // rejected: no pass while the difference keeps its digits.
+                const double less = Z - R;
+                if (!Q && rejected > 1 && less > 1e-6) {
+                    Z = less;
+                    fresh = again && fresh;
+                } else {
+                    need = true;
+                }
+            }
+            if (!need && !fresh) need = true;  // the draw needs the sums
+            if (!need && rejected && !(total > 0.0)) {
+                // nothing left: the target's own row
+                rejected = 0;
+                C = 0.0;
+                need = true;
+            }
+            if (lane == 0) sh.task = Task{cur, rejected, split(C), need, n};
+        }
+        __syncthreads();
+        task = sh.task;
+        if (!task.more) break;
+        Residual<T> R;
+        R.p = P + (r0 + task.cur) * a.p_stride;
+        R.q = Q && task.rejected > 0 ? Q + (r0 + task.cur) * a.q_stride : nullptr;
+        R.c = task.c;
+        R.gone = sh.gone;
+        R.n_gone = Q ? 0 : task.rejected;
+        const Pair d = R.q ? run_sum<T, true>(R, begin, end, a.vector != 0, lane) : run_sum<T, false>(R, begin, end, a.vector != 0, lane);
         if (lane == 0) sh.run[warp] = d;
         __syncthreads();
-        double *part = sh.part[pass & 1];
-        if (tid < a.cluster) {
-            double mine = 0.0;
-            for (int w = 0; w < kWarps; ++w) mine += sh.run[w];
-            uint32_t to = (uint32_t)__cvta_generic_to_shared(part + rank);
-            asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(to) : "r"(tid));
-            asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(to), "d"(mine) : "memory");
-        }
-        if (a.cluster > 1) {
-            asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-        } else {
-            __syncthreads();
-        }
-        total = 0.0;
-        for (int c = 0; c < a.cluster; ++c) total += part[c];
-        ++pass;
-    };
-    // ---- the walk: every warp follows it alike; a row is tested after its parent and its
-    // older siblings
-    int cur = 0, n = 1, rejected = 0;
-    double C = 0.0, Z = 1.0;
-    bool fresh = false;  // `total` and the pieces are of the current residual
-    auto node = [&](int k) {
-        Residual<T> R;
-        R.p = P + (r0 + cur) * a.p_stride;
-        R.q = Q && k > 0 ? Q + (r0 + cur) * a.q_stride : nullptr;
-        R.c = split(C);
-        R.gone = sh.gone;
-        R.n_gone = Q ? 0 : k;
-        return R;
-    };
-    for (int j = 1;;) {
-        // the next child of cur from row j on
-        int at = L;
-        for (int base = j & ~31; base < L; base += 32) {
-            const int i = base + lane;
-            const unsigned m = __ballot_sync(0xffffffffu, i >= j && i < L && sh.parent[i] == cur);
-            if (m) {
-                at = base + __ffs(m) - 1;
-                break;
+        if (warp == 0) {
+            const Pair mine = lanes_sum(lane < kWarps ? sh.run[lane] : Pair{0.f, 0.f}, kWarps);
+            if (lane < a.cluster) {
+                uint32_t to = (uint32_t)__cvta_generic_to_shared(&sh.part[pass & 1][rank]);
+                asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(to) : "r"(lane));
+                asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(mine.hi), "f"(mine.lo) : "memory");
             }
         }
-        if (at >= L) break;
-        j = at + 1;
-        const int x = sh.token[at];
-        double R = sh.tp[at];
-        const double q = sh.tq[at];
-        bool again = false;  // no drafter: the token was rejected before
-        if (Q) {
-            R = fmax(R - C * q, 0.0);
-        } else {
-            for (int i = 0; i < rejected; ++i) again |= sh.gone[i] == x;
-            if (again) R = 0.0;
-        }
-        const bool inside = x >= 0 && x < a.V;
-        if (!inside && rank == 0 && tid == 0) raise_flag(a.err_flag, PA_FLAG_TOKEN_OUT_OF_RANGE);
-        if (inside && (double)sh.u[at] * Z * q < R) {
-            cur = at;
-            C = 0.0;
-            Z = 1.0;
-            rejected = 0;
-            fresh = false;
-            __syncthreads();  // gone has been read
-            if (tid == 0) sh.place[at] = n;
-            ++n;
-            continue;
-        }
-        C += Z;
-        if (!Q) {
+        if (a.cluster > 1)
+            asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+        else
             __syncthreads();
-            if (tid == 0) sh.gone[rejected] = x;
-            __syncthreads();
-        }
-        ++rejected;
-        // Without a drafter the mass after the first rejection falls by what is rejected: no
-        // pass while the difference keeps its digits.
-        const double less = Z - R;
-        if (!Q && rejected > 1 && less > 1e-6) {
-            Z = less;
-            fresh = again && fresh;
-        } else {
-            mass(node(rejected));
-            Z = total;
-            fresh = true;
-        }
+        ++pass;
     }
     // ---- the draw: the first v whose running sum of R exceeds u total
-    if (!fresh) mass(node(rejected));
-    if (rejected && !(total > 0.0)) {  // nothing left: the target's own row
-        rejected = 0;
-        C = 0.0;
-        mass(node(0));
+    if (warp == 0) {
+        const bool drawn = total > 0.0 && total <= 1.7e308;
+        int owner_run = -1;
+        double from = 0.0, target = 0.0;
+        if (!drawn) {
+            if (rank == 0 && lane == 0) {
+                raise_flag(a.err_flag, PA_FLAG_PROBABILITY);
+                tokens_out[n - 1] = -1;
+            }
+        } else {
+            target = (double)a.u_final[s] * total;
+            // first of the CTAs' parts, then of this CTA's runs; past all of them (numbers of 1
+            // or more, rounding) the last with weight
+            const double w = lane < a.cluster ? value(sh.part[(pass - 1) & 1][lane]) : 0.0, upto = warp_scan(w, lane);
+            const unsigned hit = __ballot_sync(0xffffffffu, w > 0.0 && upto > target), any = __ballot_sync(0xffffffffu, w > 0.0);
+            const int owner = hit ? __ffs(hit) - 1 : 31 - __clz(any);
+            if (owner == rank) {
+                const double start = __shfl_sync(0xffffffffu, upto - w, owner);
+                const double r = lane < kWarps ? value(sh.run[lane]) : 0.0, to = start + warp_scan(r, lane);
+                const unsigned h = __ballot_sync(0xffffffffu, r > 0.0 && to > target), y = __ballot_sync(0xffffffffu, r > 0.0);
+                owner_run = h ? __ffs(h) - 1 : 31 - __clz(y);
+                from = __shfl_sync(0xffffffffu, to - r, owner_run);
+            }
+        }
+        if (lane == 0) {
+            sh.owner_run = owner_run;
+            sh.from = from;
+            sh.target = target;
+        }
     }
-    const bool drawn = total > 0.0 && total <= 1.7e308;
-    if (!drawn) {
-        if (rank == 0 && tid == 0) {
-            raise_flag(a.err_flag, PA_FLAG_PROBABILITY);
-            tokens_out[n - 1] = -1;
-        }
-    } else {
-        const double target = (double)a.u_final[s] * total;
-        const double *part = sh.part[(pass - 1) & 1];
-        double before = 0.0, from = 0.0;
-        int owner = -1, last = 0;
-        for (int c = 0; c < a.cluster; ++c) {
-            if (part[c] > 0.0) last = c;
-            if (owner < 0 && before + part[c] > target) {
-                owner = c;
-                from = before;
-            }
-            before += part[c];
-        }
-        if (owner < 0) {  // a number of 1 or more: the last entry with weight
-            owner = last;
-            from = before;
-        }
-        if (owner == rank) {
-            int mine = -1;
-            last = 0;
-            double at = from, start = from;
-            for (int w = 0; w < kWarps; ++w) {
-                if (sh.run[w] > 0.0) last = w;
-                if (mine < 0 && at + sh.run[w] > target) {
-                    mine = w;
-                    start = at;
-                }
-                at += sh.run[w];
-            }
-            if (mine < 0) {
-                mine = last;
-                start = at;
-            }
-            if (warp == mine) {
-                const int v = run_find(node(rejected), begin, end, start, target, lane);
-                if (lane == 0) tokens_out[n - 1] = v;
-            }
-        }
+    __syncthreads();
+    n = task.n;
+    if (warp == sh.owner_run) {
+        Residual<T> R;
+        R.p = P + (r0 + task.cur) * a.p_stride;
+        R.q = Q && task.rejected > 0 ? Q + (r0 + task.cur) * a.q_stride : nullptr;
+        R.c = task.c;
+        R.gone = sh.gone;
+        R.n_gone = Q ? 0 : task.rejected;
+        const int v = run_find(R, begin, end, sh.from, sh.target, lane);
+        if (lane == 0) tokens_out[n - 1] = v;
     }
     // ---- the branch
     if (rank != 0) return;
     for (int j = n + tid; j < a.W; j += kThreads) tokens_out[j] = path[j] = -1;
-    __syncthreads();
     if (tid == 0) a.n_out[s] = n;
     for (int j = tid; j < L; j += kThreads) {
         const int place = sh.place[j];
