@@ -463,39 +463,70 @@ def decode_workspace(query, k_cache, max_context_len: int) -> torch.Tensor | Non
 
 
 # ------------------------------------------------- speculative decoding (include/pa_draft.h)
-def _heads(t, name: str) -> int:
-    """Check a [T][heads][D] bf16 CUDA tensor with dense heads; its token stride in elements."""
+# These calls are short, so their checks are kept short as well: one pass over a tensor's
+# properties that gives its address, and the named error only where something is wrong.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _need(t, name: str, dtype: torch.dtype, ndim: int, index: int) -> int:
+    """Address of a contiguous tensor of this type on device `index`."""
+    if t.dtype is dtype and t.get_device() == index and t.dim() == ndim and t.is_contiguous():
+        return t.data_ptr()
+    _cuda(t, name, dtype, ndim)
+    raise ValueError(f"{name}: all tensors must live on one CUDA device")
+
+
+def _heads(t, name: str, index: int) -> int:
+    """Token stride, in elements, of a [T][heads][D] bf16 tensor with dense heads on device `index`."""
+    if t.dtype is torch.bfloat16 and t.get_device() == index and t.dim() == 3:
+        _, heads, D = t.shape
+        by_token, by_head, by_element = t.stride()
+        if (by_element == 1 or D <= 1) and (by_head == D or heads <= 1):
+            return by_token if t.shape[0] > 1 else heads * D
+        raise ValueError(f"{name}: the heads of a token must be dense")
+    if t.is_contiguous():
+        _cuda(t, name, torch.bfloat16, 3)
+    elif t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
+    elif t.dim() != 3:
+        raise ValueError(f"{name}: expected 3 dimensions, got {t.dim()}")
+    raise ValueError(f"{name}: all tensors must live on one CUDA device")
+
+
+def _first_device(t, name: str) -> int:
+    """Index of the CUDA device a call runs on: that of its first tensor."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must live on a CUDA device")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != 3:
-        raise ValueError(f"{name}: expected 3 dimensions, got {t.dim()}")
-    T, heads, D = t.shape
-    by_token, by_head, by_element = t.stride()
-    if (D > 1 and by_element != 1) or (heads > 1 and by_head != D):
-        raise ValueError(f"{name}: the heads of a token must be dense")
-    return by_token if T > 1 else heads * D
+    return t.get_device()
 
 
-def _one_device(*tensors) -> torch.device:
-    """The device all tensors live on."""
-    index = tensors[0].get_device()
-    for t in tensors:
-        if t is not None and t.get_device() != index:
-            raise ValueError("all tensors must live on one CUDA device")
-    return tensors[0].device
+def _scales(k_scale, v_scale, N: int, Hkv: int, bs: int, kv_dtype: int, index: int, fn: str):
+    """Addresses of an 8-bit cache's scales; (None, None) for a bf16 cache."""
+    if kv_dtype == PA_KV_BF16:
+        return None, None
+    if k_scale is None or v_scale is None:
+        raise ValueError("an int8 or fp8 cache needs k_scale and v_scale")
+    ks, vs = _need(k_scale, "k_scale", torch.float32, 3, index), _need(v_scale, "v_scale", torch.float32, 3, index)
+    if tuple(k_scale.shape) != (N, Hkv, bs) or v_scale.shape != k_scale.shape:
+        raise ValueError(f"{fn}: scale shapes")
+    return ks, vs
 
 
-def _call(function, device, stream, *args) -> None:
-    """Call a library function with `device` current and the stream as its last argument."""
-    if torch.cuda.current_device() == device.index:
-        _check(function(*args, _stream(stream, device)))
+def _call(function, index: int, stream, *args) -> None:
+    """Call a library function with device `index` current and the stream as its last argument."""
+    if stream is None and _raw_stream is not None:
+        raw = _raw_stream(index)
     else:
-        with torch.cuda.device(device):
-            _check(function(*args, _stream(stream, device)))
+        raw = _stream(stream, index)
+    if torch.cuda.current_device() == index:
+        status = function(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            status = function(*args, raw)
+    if status != PA_OK:
+        _check(status)
 
 
 def pa_rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: int = PA_ROTARY_PLAIN, factor: float = 1.0,
@@ -527,47 +558,38 @@ def pa_rotary_and_cache(query_out, query, key, positions, table, interleaved: bo
     2 * len(table) elements of each head; write query_out, key_out if given, and append the
     rotated keys and the values if a cache is given.  query, key and value may be slices of
     one tensor (dense heads, any token stride that is a multiple of 8)."""
-    q_stride, k_stride = _heads(query, "query"), _heads(key, "key")
+    dev = _first_device(query, "query")
+    q_stride, k_stride = _heads(query, "query", dev), _heads(key, "key", dev)
     T, Hq, D = query.shape
-    Hkv = key.shape[1]
-    _cuda(query_out, "query_out", torch.bfloat16, 3)
-    _cuda(positions, "positions", torch.int64, 1)
-    _cuda(table, "table", torch.int64, 1)
-    if query_out.shape != query.shape or key.shape[0] != T or key.shape[2] != D or positions.shape[0] != T:
+    T2, Hkv, D2 = key.shape
+    qo = _need(query_out, "query_out", torch.bfloat16, 3, dev)
+    pos = _need(positions, "positions", torch.int64, 1, dev)
+    tab = _need(table, "table", torch.int64, 1, dev)
+    if query_out.shape != query.shape or T2 != T or D2 != D or positions.shape[0] != T:
         raise ValueError("pa_rotary_and_cache: shape mismatch")
+    ko = None
     if key_out is not None:
-        _cuda(key_out, "key_out", torch.bfloat16, 3)
+        ko = _need(key_out, "key_out", torch.bfloat16, 3, dev)
         if key_out.shape != key.shape:
             raise ValueError("pa_rotary_and_cache: shape mismatch")
     v_stride, kv_dtype, bs, N = 0, PA_KV_BF16, 16, 1
+    vp = kc = vc = ks = vs = slots = None
     if k_cache is not None or v_cache is not None:
         if k_cache is None or v_cache is None or value is None or slot_mapping is None:
             raise ValueError("appending needs k_cache, v_cache, value and slot_mapping")
-        v_stride, kv_dtype = _heads(value, "value"), kv_dtype_of(k_cache)
-        _cuda(k_cache, "k_cache", k_cache.dtype, 4)
-        _cuda(v_cache, "v_cache", k_cache.dtype, 4)
-        _cuda(slot_mapping, "slot_mapping", torch.int64, 1)
-        N, heads, bs, D2 = k_cache.shape
-        if value.shape != key.shape or v_cache.shape != k_cache.shape or heads != Hkv or D2 != D \
-                or slot_mapping.shape[0] != T:
+        v_stride, vp, kv_dtype = _heads(value, "value", dev), value.data_ptr(), kv_dtype_of(k_cache)
+        kc = _need(k_cache, "k_cache", k_cache.dtype, 4, dev)
+        vc = _need(v_cache, "v_cache", k_cache.dtype, 4, dev)
+        slots = _need(slot_mapping, "slot_mapping", torch.int64, 1, dev)
+        shape = k_cache.shape
+        N, heads, bs, D2 = shape
+        if value.shape != key.shape or v_cache.shape != shape or heads != Hkv or D2 != D or slot_mapping.shape[0] != T:
             raise ValueError("pa_rotary_and_cache: shape mismatch")
-        if kv_dtype != PA_KV_BF16:
-            if k_scale is None or v_scale is None:
-                raise ValueError("an int8 or fp8 cache needs k_scale and v_scale")
-            _cuda(k_scale, "k_scale", torch.float32, 3)
-            _cuda(v_scale, "v_scale", torch.float32, 3)
-            if tuple(k_scale.shape) != (N, Hkv, bs) or v_scale.shape != k_scale.shape:
-                raise ValueError("pa_rotary_and_cache: scale shapes")
-        else:
-            k_scale = v_scale = None
-    else:
-        value = slot_mapping = k_scale = v_scale = None
-    device = _one_device(query, query_out, key, key_out, positions, table, value, k_cache, v_cache, slot_mapping,
-                         k_scale, v_scale, err_flag)
-    _call(load_library().pa_rotary_and_cache, device, stream, _ptr(query_out), _ptr(key_out), _ptr(query), q_stride,
-          _ptr(key), k_stride, _ptr(value), v_stride, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-          kv_dtype, _ptr(slot_mapping), _ptr(positions), _ptr(table), 2 * table.shape[0], int(interleaved),
-          float(attention_factor), T, Hq, Hkv, D, bs, N, _flag(err_flag))
+        ks, vs = _scales(k_scale, v_scale, N, Hkv, bs, kv_dtype, dev, "pa_rotary_and_cache")
+    flag = None if err_flag is None else _need(err_flag, "err_flag", torch.int32, err_flag.dim(), dev)
+    _call(load_library().pa_rotary_and_cache, dev, stream, qo, ko, query.data_ptr(), q_stride, key.data_ptr(), k_stride,
+          vp, v_stride, kc, vc, ks, vs, kv_dtype, slots, pos, tab, 2 * table.shape[0], 1 if interleaved else 0,
+          attention_factor, T, Hq, Hkv, D, bs, N, flag)
 
 
 def pa_tree_workspace_size(S: int, T: int, Hq: int, Hkv: int, D: int, bs: int, kv_dtype: int,
@@ -582,60 +604,49 @@ def pa_tree_attention(out, query, key, value, k_cache, v_cache, block_tables, co
     """Rows of drafted tokens attend their sequence's cached context and, among the rows
     (key/value [T][Hkv][D] beside the cache), themselves and their ancestors.  workspace
     defaults to a fresh allocation."""
-    _cuda(out, "out", torch.bfloat16, 3)
-    _cuda(query, "query", torch.bfloat16, 3)
-    k_stride, v_stride = _heads(key, "key"), _heads(value, "value")
-    kv_dtype = kv_dtype_of(k_cache)
-    _cuda(k_cache, "k_cache", k_cache.dtype, 4)
-    _cuda(v_cache, "v_cache", k_cache.dtype, 4)
-    _cuda(block_tables, "block_tables", torch.int32, 2)
-    _cuda(context_lens, "context_lens", torch.int32, 1)
-    _cuda(query_start, "query_start", torch.int32, 1)
-    _cuda(parents, "parents", torch.int32, 1)
-    T, Hq, D = query.shape
-    N, Hkv, bs, D2 = k_cache.shape
+    dev = _first_device(query, "query")
+    qp = _need(query, "query", torch.bfloat16, 3, dev)
+    op = _need(out, "out", torch.bfloat16, 3, dev)
+    k_stride, v_stride, kv_dtype = _heads(key, "key", dev), _heads(value, "value", dev), kv_dtype_of(k_cache)
+    kc = _need(k_cache, "k_cache", k_cache.dtype, 4, dev)
+    vc = _need(v_cache, "v_cache", k_cache.dtype, 4, dev)
+    tables = _need(block_tables, "block_tables", torch.int32, 2, dev)
+    lens = _need(context_lens, "context_lens", torch.int32, 1, dev)
+    starts = _need(query_start, "query_start", torch.int32, 1, dev)
+    up = _need(parents, "parents", torch.int32, 1, dev)
+    shape, cache_shape = query.shape, k_cache.shape
+    T, Hq, D = shape
+    N, Hkv, bs, D2 = cache_shape
     S, M = block_tables.shape
-    if kv_dtype != PA_KV_BF16:
-        if k_scale is None or v_scale is None:
-            raise ValueError("an int8 or fp8 cache needs k_scale and v_scale")
-        _cuda(k_scale, "k_scale", torch.float32, 3)
-        _cuda(v_scale, "v_scale", torch.float32, 3)
-        if tuple(k_scale.shape) != (N, Hkv, bs) or v_scale.shape != k_scale.shape:
-            raise ValueError("pa_tree_attention: scale shapes")
-    else:
-        k_scale = v_scale = None
-    if out.shape != query.shape or tuple(key.shape) != (T, Hkv, D) or value.shape != key.shape \
-            or v_cache.shape != k_cache.shape or D2 != D or context_lens.shape[0] != S \
-            or query_start.shape[0] != S + 1 or parents.shape[0] != T:
+    ks, vs = _scales(k_scale, v_scale, N, Hkv, bs, kv_dtype, dev, "pa_tree_attention")
+    if out.shape != shape or key.shape != (T, Hkv, D) or value.shape != key.shape or v_cache.shape != cache_shape \
+            or D2 != D or context_lens.shape[0] != S or query_start.shape[0] != S + 1 or parents.shape[0] != T:
         raise ValueError("pa_tree_attention: shape mismatch")
     if workspace is None:
         n = pa_tree_workspace_size(S, T, Hq, Hkv, D, bs, kv_dtype, max_context_len, max_query_len)
         workspace = torch.empty(n, dtype=torch.uint8, device=query.device) if n else None
-    ws_bytes = 0
+    ws, ws_bytes = None, 0
     if workspace is not None:
-        _cuda(workspace, "workspace", workspace.dtype)
+        ws = _need(workspace, "workspace", workspace.dtype, workspace.dim(), dev)
         ws_bytes = workspace.numel() * workspace.element_size()
-    device = _one_device(query, out, key, value, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
-                         query_start, parents, workspace, err_flag)
-    _call(load_library().pa_tree_attention, device, stream, _ptr(out), _ptr(query), _ptr(key), k_stride, _ptr(value),
-          v_stride, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), kv_dtype, _ptr(block_tables), M,
-          _ptr(context_lens), _ptr(query_start), _ptr(parents), S, T, Hq, Hkv, D, bs, N, float(scale),
-          int(max_context_len), int(max_query_len), _ptr(workspace), ws_bytes, _flag(err_flag))
+    flag = None if err_flag is None else _need(err_flag, "err_flag", torch.int32, err_flag.dim(), dev)
+    _call(load_library().pa_tree_attention, dev, stream, op, qp, key.data_ptr(), k_stride, value.data_ptr(), v_stride, kc,
+          vc, ks, vs, kv_dtype, tables, M, lens, starts, up, S, T, Hq, Hkv, D, bs, N, scale, max_context_len,
+          max_query_len, ws, ws_bytes, flag)
 
 
-def _probabilities(t, name: str, T: int, V: int, dtype: torch.dtype) -> int:
-    """Check [T][V] probabilities with dense rows; the row stride in elements."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must live on a CUDA device")
-    if t.dtype != dtype:
+def _probabilities(t, name: str, T: int, V: int, dtype: torch.dtype, index: int) -> int:
+    """Row stride, in elements, of [T][V] probabilities with dense rows on device `index`."""
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if tuple(t.shape) != (T, V):
+    if t.get_device() != index:
+        raise ValueError(f"{name} must live on the CUDA device of the other tensors")
+    if t.shape != (T, V):
         raise ValueError(f"{name}: expected shape {(T, V)}, got {tuple(t.shape)}")
-    if V > 1 and t.stride(1) != 1:
+    by_row, by_entry = t.stride()
+    if V > 1 and by_entry != 1:
         raise ValueError(f"{name}: the probabilities of a row must be dense")
-    return t.stride(0) if T > 1 else V
+    return by_row if T > 1 else V
 
 
 def pa_verify_tree(tokens_out, path, n_out, draft_tokens, target_probs, query_start, parents, uniforms,
@@ -645,45 +656,47 @@ def pa_verify_tree(tokens_out, path, n_out, draft_tokens, target_probs, query_st
     uniform numbers, draw each sequence's next token, and write the accepted branch: tokens_out
     and path [S][max_query_len], n_out [S], and (with block_tables, context_lens, block_size
     and num_blocks) slot_mapping [T]."""
-    _cuda(tokens_out, "tokens_out", torch.int32, 2)
-    _cuda(path, "path", torch.int32, 2)
-    _cuda(n_out, "n_out", torch.int32, 1)
-    _cuda(draft_tokens, "draft_tokens", torch.int32, 1)
-    _cuda(query_start, "query_start", torch.int32, 1)
-    _cuda(parents, "parents", torch.int32, 1)
-    _cuda(uniforms, "uniforms", torch.float32, 1)
-    _cuda(final_uniforms, "final_uniforms", torch.float32, 1)
+    dev = _first_device(target_probs, "target_probs")
+    said = _need(tokens_out, "tokens_out", torch.int32, 2, dev)
+    way = _need(path, "path", torch.int32, 2, dev)
+    count = _need(n_out, "n_out", torch.int32, 1, dev)
+    tokens = _need(draft_tokens, "draft_tokens", torch.int32, 1, dev)
+    starts = _need(query_start, "query_start", torch.int32, 1, dev)
+    up = _need(parents, "parents", torch.int32, 1, dev)
+    u = _need(uniforms, "uniforms", torch.float32, 1, dev)
+    u_final = _need(final_uniforms, "final_uniforms", torch.float32, 1, dev)
     T, S = draft_tokens.shape[0], n_out.shape[0]
+    dtype = target_probs.dtype
     if target_probs.dim() != 2:
         raise ValueError("target_probs: expected 2 dimensions")
-    if target_probs.dtype not in (torch.float32, torch.bfloat16):
+    if dtype is not torch.float32 and dtype is not torch.bfloat16:
         raise TypeError("target_probs: expected float32 or bfloat16")
     V = target_probs.shape[1]
-    p_stride = _probabilities(target_probs, "target_probs", T, V, target_probs.dtype)
-    q_stride = 0 if draft_probs is None else _probabilities(draft_probs, "draft_probs", T, V, target_probs.dtype)
-    W = tokens_out.shape[1]
-    if tokens_out.shape[0] != S or path.shape != tokens_out.shape or query_start.shape[0] != S + 1 \
-            or parents.shape[0] != T or uniforms.shape[0] != T or final_uniforms.shape[0] != S:
+    p_stride = _probabilities(target_probs, "target_probs", T, V, dtype, dev)
+    qp, q_stride = None, 0
+    if draft_probs is not None:
+        if draft_probs.dim() != 2:
+            raise ValueError("draft_probs: expected 2 dimensions")
+        qp, q_stride = draft_probs.data_ptr(), _probabilities(draft_probs, "draft_probs", T, V, dtype, dev)
+    shape = tokens_out.shape
+    W = shape[1]
+    if shape[0] != S or path.shape != shape or query_start.shape[0] != S + 1 or parents.shape[0] != T \
+            or uniforms.shape[0] != T or final_uniforms.shape[0] != S:
         raise ValueError("pa_verify_tree: shape mismatch")
-    M = 0
+    M, slots, tables, lens = 0, None, None, None
     if slot_mapping is not None:
         if block_tables is None or context_lens is None:
             raise ValueError("slot_mapping needs block_tables and context_lens")
-        _cuda(slot_mapping, "slot_mapping", torch.int64, 1)
-        _cuda(block_tables, "block_tables", torch.int32, 2)
-        _cuda(context_lens, "context_lens", torch.int32, 1)
+        slots = _need(slot_mapping, "slot_mapping", torch.int64, 1, dev)
+        tables = _need(block_tables, "block_tables", torch.int32, 2, dev)
+        lens = _need(context_lens, "context_lens", torch.int32, 1, dev)
         if slot_mapping.shape[0] != T or block_tables.shape[0] != S or context_lens.shape[0] != S:
             raise ValueError("pa_verify_tree: shape mismatch")
         M = block_tables.shape[1]
-    else:
-        block_tables = context_lens = None
-    device = _one_device(target_probs, draft_probs, tokens_out, path, n_out, slot_mapping, draft_tokens, query_start,
-                         parents, uniforms, final_uniforms, block_tables, context_lens, err_flag)
-    _call(load_library().pa_verify_tree, device, stream, _ptr(tokens_out), _ptr(path), _ptr(n_out), _ptr(slot_mapping),
-          _ptr(draft_tokens), _ptr(target_probs), p_stride, _ptr(draft_probs), q_stride,
-          PA_PROB_F32 if target_probs.dtype == torch.float32 else PA_PROB_BF16, _ptr(query_start), _ptr(parents),
-          _ptr(uniforms), _ptr(final_uniforms), S, T, V, W, _ptr(block_tables), M, _ptr(context_lens),
-          int(block_size), int(num_blocks), _flag(err_flag))
+    flag = None if err_flag is None else _need(err_flag, "err_flag", torch.int32, err_flag.dim(), dev)
+    _call(load_library().pa_verify_tree, dev, stream, said, way, count, slots, tokens, target_probs.data_ptr(), p_stride,
+          qp, q_stride, PA_PROB_F32 if dtype is torch.float32 else PA_PROB_BF16, starts, up, u, u_final, S, T, V, W,
+          tables, M, lens, block_size, num_blocks, flag)
 
 
 # ------------------------------------------------------------------ block manager
