@@ -7,7 +7,7 @@
 namespace pa {
 
 // The context's part on the tcgen05 kernel.  The contexts are cut into 128-token tiles and
-// all (sequence, kv head) units laid end to end; group g of min(`groups`, total) takes tiles
+// all (sequence, kv head) units laid end to end; group g of min(`groups`, total) takes positions
 // [g * total / groups, (g + 1) * total / groups), whatever the lengths of the sequences, and
 // the `members` CTAs of a group take `cols` (row, query head) columns each.  A unit that
 // lies in one group leaves one partial per column in `whole`; a cut one leaves one in a slot
@@ -20,7 +20,7 @@ struct TreeContext {
     const int32_t *block_tables, *context_lens, *query_start;
     float *whole_acc, *whole_ml;  // [T][Hq][128], [T][Hq][2]
     float *cut_acc, *cut_ml;      // [CTA][2][cols][128], [CTA][2][cols][2]
-    int64_t *prefix;              // [S + 1]: first tile of each sequence (written by the kernel)
+    int64_t *prefix;              // [S + 1]: first position of each sequence (written by the kernel)
     int *err_flag;
     int M, S, T, Hq, Hkv, G, N, g_shift;
     int members, groups, cols;
@@ -29,8 +29,12 @@ struct TreeContext {
 };
 
 constexpr int kTreeTile = 128;  // cached tokens per tile
+// Each unit is laid out with a head start of kTreePad positions before its tiles, about what
+// changing over to it costs in tiles, so that shares of many short units are smaller.
+constexpr int kTreePad = 2;
+__host__ __device__ inline int64_t tree_unit_len(int64_t tiles) { return tiles > 0 ? tiles + kTreePad : 0; }
 
-// Group whose range holds tile x of `total`.
+// Group whose range holds position x of `total`.
 __host__ __device__ inline int64_t tree_group_of(int64_t x, int64_t total, int64_t groups) {
     return ((x + 1) * groups - 1) / total;
 }

@@ -2,29 +2,37 @@
 //
 // Every (row, query head) column of a sequence and kv head attends every cached token: one
 // softmax over the context without a mask, S = Q K^T, P = 2^(S - m), O = P V, with the
-// running maximum m and sum l of each column in registers and O in tensor memory.
+// running base m and sum l of each column in registers and O in tensor memory.
 //
 // One CTA per SM (224 KB of shared memory, all 512 tensor-memory columns) works through its
-// share of all tiles of the batch (pa_tree.cuh): 128 tokens of K and V at a time, staged by
-// TMA into a ring of five 32 KB stages that runs on across units.  Warps with fixed roles,
-// coupled by mbarriers:
+// share of all tiles of the batch (pa_tree.cuh), 128 tokens of K and V at a time, in a ring
+// of 32 KB stages that runs on across units.  Warps with fixed roles, coupled by mbarriers:
 //   * warps 0-3 and 4-7 are two lanes of 128 columns, a thread per column.  With more than
 //     128 columns the lanes take the two halves of 256 columns and share every staged
 //     tile; with at most 128 they take the same columns and alternate tiles, and are
 //     joined at the end of a unit.  Either way one lane's exponentials run while the
 //     tensor cores work for the other;
-//   * warp 8 copies K and V tiles; one thread each of warps 9 and 10 issues a lane's products.
-//     (Warp 11 fills the warpgroup, whose spare registers go to the columns.)
-// Tensor memory: S of the lanes at columns 0 and 128 (overwritten by P as bf16 pairs, the A
+//   * warp 8 copies K and V tiles (TMA); one thread each of warps 9 and 10 issues a lane's
+//     products; warp 11 stages the units' queries, a unit ahead where it has a buffer;
+//   * 8-bit caches: warp 8 copies codes into a ring of 16 KB stages, and warps 12-15 turn
+//     them into exact fp16 in the stages the products read.
+// Tensor memory: S of the lanes at columns 0 and 128 (overwritten by P as 16-bit pairs, the A
 // operand of P V), O at 256 and 384.
-// Bounds: up to 128 columns, or 256 shared ones, the 64 KB of a K and V tile take 2800 SM
+// 8-bit caches: a score is (q . code) x key scale, the query rows being fp16 scaled by a power
+// of two each; the weight fed to the product is p x value scale in fp16, so the base m is
+// kept above the scores plus the exponent of the tile's largest value scale: no weight
+// leaves fp16's range whatever the scales.
+// Bounds: up to 128 columns, or 256 shared ones, the 64 KB of a bf16 K and V tile take 2800 SM
 // clocks at the measured HBM rate and the products 1024 / 2048, so HBM bounds; more columns
 // reread the tiles through L2 and the products bound.
 // Every wait is bounded; a wait that gives up stops the CTA (PA_FLAG_TIMEOUT).
+#include <cuda_fp16.h>
 #include <math.h>
 
 #include <atomic>
+#include <type_traits>
 
+#include "pa_mma.cuh"
 #include "pa_tc.cuh"
 #include "pa_tree.cuh"
 
@@ -37,40 +45,59 @@ constexpr int kTile = kTreeTile;
 constexpr int kD = 128;
 constexpr int kLaneCols = 128;
 constexpr int kTileBytes = kTile * kD * 2;   // 32 KB
+constexpr int kRawBytes = kTile * kD;        // 16 KB of 8-bit codes
 // A staged tile: groups of 8 rows, each as two 64-dim halves of 8 x 128 B (one swizzle atom
 // each).  A cache block is then one copy of bs x 256 contiguous bytes, and the atoms of a
 // half lie a constant 2 KB apart, as the matrix descriptors need.
 constexpr int kHalf = 1024, kGroup = 2048;
-constexpr int kStages = 5;
-// Ring position p lands in stage p % kStages and completes barrier p % kFull.  With
-// alternating lanes a lane sees only its own positions, up to three apart, and copies land
-// in any order, so a stage's own barrier could still be at the other lane's copy of
-// position p - 5 when position p is asked for, and that phase has the parity of p's
-// predecessor's predecessor.  With two barriers a stage the predecessor is p - 10, and a
-// copy past p - 5 is only issued once p - 10 was consumed.
-constexpr int kFull = 2 * kStages;
-constexpr int kOffQ = 0, kOffRing = 2 * kTileBytes, kOffShared = kOffRing + kStages * kTileBytes;
-constexpr int kThreads = 384;  // three warpgroups: two lanes of columns; copies and products
-constexpr int kRegsColumns = 192, kRegsOther = 120;  // 2 x 128 x 192 + 128 x 120 = 384 x 168 at launch
 constexpr uint32_t kTmemS = 0, kTmemO = 256;  // + 128 per lane
 constexpr float kRescaleLog2 = 8.0f;
+constexpr int kScaleSlots = 4;
 
+// Shared memory and threads of a kernel.  Ring position p lands in stage p % kStages and
+// completes barrier p % kFull.  With alternating lanes a lane sees only its own positions,
+// up to three apart, and copies land in any order, so a stage's own barrier could still be
+// at the other lane's copy of the stage's previous position when p is asked for, and that
+// phase has the parity of the one p waits for.  With two barriers a stage the predecessor
+// on a barrier is two uses of the stage back, and a copy after that is only issued once it
+// was consumed.
+template <typename KV, bool SPLIT>
+struct Geo {
+    static constexpr bool kQuant = sizeof(KV) == 1;
+    static constexpr int kStages = kQuant ? 3 : 5, kFull = 2 * kStages;
+    // query buffers: one per lane; lanes on the same columns share one, and alternate two
+    // from unit to unit where there is room
+    static constexpr int kQueries = kQuant && SPLIT ? 1 : 2;
+    static constexpr int kRaw = !kQuant ? 0 : SPLIT ? 5 : 3;  // stages of codes
+    static constexpr int kOffRing = kQueries * kTileBytes, kOffRaw = kOffRing + kStages * kTileBytes;
+    static constexpr int kOffShared = kOffRaw + kRaw * kRawBytes;
+    static constexpr int kThreads = kQuant ? 512 : 384;
+    // registers a thread: the columns' warps take what the others leave of the launch's
+    // 168 (three warpgroups) or 128 (four)
+    static constexpr int kRegsColumns = kQuant ? 184 : 200, kRegsOther = kQuant ? 72 : 104;
+};
+
+template <typename G>
 struct Shared {
-    float2 ml[2][kLaneCols];                    // lanes joined: each one's (max, sum) per column
-    uint64_t full[kFull], free[kStages];        // ring positions landed / stages consumed
+    float2 ml[2][kLaneCols];                    // lanes joined: each one's (base, sum) per column
+    float ks[G::kQuant ? kScaleSlots : 1][G::kQuant ? kTile : 1];  // tiles' scales, 0 behind the context
+    float vs[G::kQuant ? kScaleSlots : 1][G::kQuant ? kTile : 1];
+    float rs[2][G::kQuant ? kLaneCols : 1];     // columns' score factors, by query buffer
+    uint64_t full[G::kFull], free[G::kStages];  // ring positions landed / stages consumed
+    uint64_t raw_full[G::kQuant ? G::kRaw : 1], raw_free[G::kQuant ? G::kRaw : 1];
+    uint64_t scales[2 * kScaleSlots], scales_free[kScaleSlots];
     uint64_t sfull[2], pfull[2], odone[2];      // per lane: S written, P written, P V done
-    uint64_t qfull[2];                          // per lane: the unit's queries are staged
-    uint64_t mlready, oread;                    // lanes joined: both (max, sum) and O in / read
+    uint64_t qfull[2], qfree[2];                // query buffers: staged / products with it issued and done
+    uint64_t qfirst;                            // the first unit's queries are staged
+    uint64_t mlready, oread;                    // lanes joined: both (base, sum) and O in / read
     uint64_t turn[2];                           // shared tiles: the lane may issue its next products
     uint64_t drain[2];
-    int64_t total, first_tile;                  // of all tiles; of the first sequence
+    int64_t total, first_tile;                  // of all positions; of the first sequence
     int first_seq;
-    int wsum[kThreads / 32];
+    int wsum[16];
     uint32_t taddr;
     int abort;
 };
-constexpr int kSmem = kOffShared + (int)sizeof(Shared);
-static_assert(kSmem <= 232448, "shared memory of one CTA per SM");
 
 __device__ __forceinline__ void raise_flag(int *err_flag, int bit) {
     if (err_flag) atomicOr(err_flag, bit);
@@ -103,7 +130,7 @@ __device__ __forceinline__ uint32_t tile_chunk(int r, int ch) {
     return (r >> 3) * kGroup + (ch >> 3) * kHalf + (r & 7) * 128 + (((ch & 7) ^ (r & 7)) << 4);
 }
 
-// One block of a pool, [bs / 8][2][8][64] in the order of a staged tile.
+// One block of a bf16 pool, [bs / 8][2][8][64] in the order of a staged tile.
 __device__ __forceinline__ void tma_block(uint32_t dst, const CUtensorMap *map, int group, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3}], [%4];" ::"r"(dst),
@@ -111,17 +138,36 @@ __device__ __forceinline__ void tma_block(uint32_t dst, const CUtensorMap *map, 
         : "memory");
 }
 
+// Plain bytes, 16-byte aligned on both sides.
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// Eight floats, one 32-byte sector.
+__device__ __forceinline__ void store8(float *p, const float *v) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+                 "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+}
+
 __device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// The next range of tiles of one (sequence, kv head) in a CTA's share.
+// A range of tiles of one (sequence, kv head).
+struct Unit {
+    int s, kvh, t0, n, tiles, ctx, r0, ncols;
+};
+
+// The units of a CTA's share, in order.
 struct Walk {
-    int64_t pos, end, before;  // tiles: here, end of the share, before sequence s
+    int64_t pos, end, before;  // positions: here, end of the share, before sequence s
     int s, tiles;              // sequence and its tiles per kv head (-1: not read yet)
-    int kvh, t0, n, ctx, r0, ncols;
+    int ctx, r0, ncols;
 
-    __device__ __forceinline__ bool next(const TreeContext &a) {
-        if (pos >= end) return false;
-        for (;;) {
+    __device__ __forceinline__ bool next(const TreeContext &a, Unit &u) {
+        while (pos < end) {
             if (tiles < 0) {
                 const int r1 = a.query_start[s + 1];
                 r0 = a.query_start[s];
@@ -130,26 +176,54 @@ struct Walk {
                 ncols = L * a.G;
                 tiles = r0 >= 0 && r1 <= a.T && L >= 1 && L <= a.max_query_len ? (ctx + kTile - 1) / kTile : 0;
             }
-            if (pos < before + (int64_t)tiles * a.Hkv) break;
-            before += (int64_t)tiles * a.Hkv;
-            ++s;
-            tiles = -1;
+            const int64_t len = tree_unit_len(tiles);
+            if (pos >= before + len * a.Hkv) {
+                before += len * a.Hkv;
+                ++s;
+                tiles = -1;
+                continue;
+            }
+            const int64_t in = pos - before;
+            const int off = (int)(in % len);
+            const int64_t step = min(len - off, end - pos);
+            pos += step;
+            u.s = s;
+            u.kvh = (int)(in / len);
+            u.t0 = max(0, off - kTreePad);
+            u.n = (int)(off + step) - kTreePad - u.t0;
+            u.tiles = tiles;
+            u.ctx = ctx;
+            u.r0 = r0;
+            u.ncols = ncols;
+            if (u.n > 0) return true;  // else only the unit's head start
         }
-        const int64_t in = pos - before;
-        kvh = (int)(in / tiles);
-        t0 = (int)(in % tiles);
-        n = (int)min((int64_t)(tiles - t0), end - pos);
-        pos += n;
-        return true;
+        return false;
     }
 };
 
-template <int BS, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, 1)
+// Sixteen codes of one row as sixteen exact fp16 (two 16-byte words).
+template <typename KV>
+__device__ __forceinline__ void exact_f16(const uint4 &c, uint4 &lo, uint4 &hi) {
+    tiled::codes_to_f16_exact<KV>(c, lo, hi);
+}
+template <>
+__device__ __forceinline__ void exact_f16<uint16_t>(const uint4 &, uint4 &, uint4 &) {}
+
+// Exponent e with |x| < 2^e, from -60 up.
+__device__ __forceinline__ float exponent_over(uint32_t bits) {
+    return (float)max((int)((bits >> 23) & 0xffu) - 126, -60);
+}
+
+template <typename KV, int BS, bool SPLIT>
+__global__ void __launch_bounds__(Geo<KV, SPLIT>::kThreads, 1)
 tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CUtensorMap kmap,
                const __grid_constant__ CUtensorMap vmap) {
+    using G = Geo<KV, SPLIT>;
+    constexpr bool QUANT = G::kQuant;
+    constexpr int kThreads = G::kThreads, kStages = G::kStages, kFull = G::kFull;
+    static_assert(G::kOffShared + sizeof(Shared<G>) <= 232448, "shared memory of one CTA per SM");
     extern __shared__ __align__(1024) unsigned char smem[];
-    Shared &sh = *reinterpret_cast<Shared *>(smem + kOffShared);
+    Shared<G> &sh = *reinterpret_cast<Shared<G> *>(smem + G::kOffShared);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if ((tc_smem(smem) & 1023) != 0) {  // the swizzled tiles need their alignment
         if (tid == 0) raise_flag(a.err_flag, PA_FLAG_TIMEOUT);
@@ -157,25 +231,31 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
     }
     const int group = blockIdx.x / a.members, member = blockIdx.x % a.members;
     if (tid == 0) {
-        for (int i = 0; i < kFull; ++i) mbar_init(tc_smem(&sh.full[i]));
-        for (int i = 0; i < kStages; ++i) {
-            mbar_init_n(tc_smem(&sh.free[i]), SPLIT ? 1 : 2);  // lanes that read a stage
+        for (int i = 0; i < kFull; ++i) mbar_init_n(tc_smem(&sh.full[i]), QUANT ? 128 : 1);
+        for (int i = 0; i < kStages; ++i) mbar_init_n(tc_smem(&sh.free[i]), SPLIT ? 1 : 2);  // lanes that read a stage
+        for (int i = 0; i < G::kRaw; ++i) {
+            mbar_init(tc_smem(&sh.raw_full[i]));
+            mbar_init_n(tc_smem(&sh.raw_free[i]), 128);
         }
+        for (int i = 0; i < 2 * kScaleSlots; ++i) mbar_init_n(tc_smem(&sh.scales[i]), 2 * 128);
+        for (int i = 0; i < kScaleSlots; ++i) mbar_init_n(tc_smem(&sh.scales_free[i]), SPLIT ? kLaneCols : 2 * kLaneCols);
         for (int w = 0; w < 2; ++w) {
             mbar_init(tc_smem(&sh.sfull[w]));
             mbar_init(tc_smem(&sh.odone[w]));
             mbar_init_n(tc_smem(&sh.pfull[w]), kLaneCols);
-            mbar_init_n(tc_smem(&sh.qfull[w]), kLaneCols);
+            mbar_init(tc_smem(&sh.qfull[w]));
+            // the lanes' products that read it; 8-bit: and their columns, which read its factors
+            mbar_init_n(tc_smem(&sh.qfree[w]), (SPLIT ? 2 : 1) * (QUANT ? 1 + kLaneCols : 1));
+            mbar_init(tc_smem(&sh.turn[w]));
+            mbar_init(tc_smem(&sh.drain[w]));
         }
+        mbar_init(tc_smem(&sh.qfirst));
         mbar_init_n(tc_smem(&sh.mlready), 2 * kLaneCols);
         mbar_init_n(tc_smem(&sh.oread), 2 * kLaneCols);
-        mbar_init(tc_smem(&sh.turn[0]));
-        mbar_init(tc_smem(&sh.turn[1]));
-        mbar_init(tc_smem(&sh.drain[0]));
-        mbar_init(tc_smem(&sh.drain[1]));
         sh.abort = 0;
         sh.first_seq = 0;
         sh.first_tile = 0;
+        sh.total = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 0) {
@@ -186,31 +266,30 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    // ---- the batch's tiles: their number, then the sequence this share begins in
-    auto tiles_of = [&](int s, bool report) -> int {
+    // ---- the batch's positions: their number, then the sequence this share begins in
+    auto len_of = [&](int s, bool report) -> int {
         const int lim = a.max_context_len;
         const int ctx = a.context_lens[s], r0 = a.query_start[s], r1 = a.query_start[s + 1], L = r1 - r0;
         const bool ok = r0 >= 0 && r1 <= a.T && L >= 0 && L <= a.max_query_len;
         if (report && (ctx < 0 || ctx > lim)) raise_flag(a.err_flag, PA_FLAG_CONTEXT_OUT_OF_RANGE);
         if (report && !ok) raise_flag(a.err_flag, PA_FLAG_QUERY_OUT_OF_RANGE);
-        return ok && L > 0 ? (min(max(ctx, 0), lim) + kTile - 1) / kTile : 0;
+        return ok && L > 0 ? (int)tree_unit_len((min(max(ctx, 0), lim) + kTile - 1) / kTile) : 0;
     };
-    const int n_first = tid < a.S ? tiles_of(tid, blockIdx.x == 0) : 0;
+    const int n_first = tid < a.S ? len_of(tid, blockIdx.x == 0) : 0;
     int64_t sum = n_first;
-    for (int s = tid + kThreads; s < a.S; s += kThreads) sum += tiles_of(s, blockIdx.x == 0);
+    for (int s = tid + kThreads; s < a.S; s += kThreads) sum += len_of(s, blockIdx.x == 0);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (tid == 0) sh.total = 0;
     __syncthreads();
     if (lane == 0 && sum) atomicAdd(reinterpret_cast<unsigned long long *>(&sh.total), (unsigned long long)sum);
     __syncthreads();
     const int64_t total = sh.total * a.Hkv;
-    const int64_t groups = min((int64_t)a.groups, total);  // no share is empty: a cut unit's are consecutive
+    const int64_t groups = min((int64_t)a.groups, total);
     const int64_t begin = group < groups ? group * total / groups : total;
     const int64_t end = group < groups ? (group + 1) * total / groups : total;
     int64_t carry = 0;
     for (int base = 0; base < a.S; base += kThreads) {
-        const int s = base + tid, n = base == 0 ? n_first : s < a.S ? tiles_of(s, false) : 0;
+        const int s = base + tid, n = base == 0 ? n_first : s < a.S ? len_of(s, false) : 0;
         int v = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -237,128 +316,175 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.taddr;
-    Walk w{begin, end, sh.first_tile, sh.first_seq, -1};
+    Walk w{begin, end, sh.first_tile, sh.first_seq, -1, 0, 0, 0};
     int *abort = &sh.abort;
 
     // lane 1 has work: its half of the columns, or (lanes on the same columns) a second tile
-    auto second = [&](const Walk &u) { return SPLIT ? u.n > 1 : u.ncols - member * a.cols > kLaneCols; };
-    // the member has columns of this sequence at all
-    auto mine = [&](const Walk &u) { return u.ncols > member * a.cols; };
+    auto second = [&](const Unit &u) { return SPLIT ? u.n > 1 : u.ncols - member * a.cols > kLaneCols; };
+    // the member's next unit with columns
+    auto next_unit = [&](Unit &u) {
+        while (w.next(a, u))
+            if (u.ncols > member * a.cols) return true;
+        return false;
+    };
     // Ring positions of tile t's K and V within a unit of n tiles, in the order they are used:
     // K0 V0 K1 V1 .. (shared tiles), K0 K1 V0 K2 V1 .. (alternating lanes).
     auto k_at = [](int t, int n) { return SPLIT ? (t == 0 ? 0 : 2 * t - 1) : 2 * t; };
     auto v_at = [](int t, int n) { return SPLIT ? (t < n - 1 ? 2 * t + 2 : 2 * n - 1) : 2 * t + 1; };
 
     if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(G::kRegsOther));
     if (warp == 8) {
         // ---- copies: lane i takes block i of a tile
         constexpr int kBlocks = kTile / BS, kGroups = BS / 8;  // 8-row groups of a block and kv head
-        const int oob = a.N * a.Hkv * kGroups;  // past the pool: the copy fills zeros
-        const uint32_t box = tc_smem(smem + kOffRing) + lane * BS * 256;
-        int st = 0;
-        uint32_t phase = 0;   // of the stage's next wait for `free`
-        int issued = 0;
+        constexpr int kSlots = QUANT ? G::kRaw : kStages;
+        const int oob = QUANT ? a.N * a.Hkv * BS : a.N * a.Hkv * kGroups;  // past the pool: the copy fills zeros
+        const uint32_t box = tc_smem(smem + (QUANT ? G::kOffRaw : G::kOffRing)) + lane * BS * (QUANT ? kD : 2 * kD);
+        int st = 0, issued = 0, tile = 0;  // stage, ring position, tile of the share
+        uint32_t phase = 0;                // of the stage's next wait for its release
         bool ok = true, first = true;
-        auto fill = [&](const CUtensorMap *map, int y) {
-            if (issued >= kStages) ok = wait_for(&sh.free[st], phase ^ 1, abort);
+        Unit u{}, nu;
+        bool have = next_unit(nu);
+        // K (map, y) or V of this lane's block; 8-bit: the block's scales too, none where b < 0
+        auto fill = [&](bool is_k, int y, int b, int j) {
+            if (issued >= kSlots) ok = wait_for(QUANT ? &sh.raw_free[st] : &sh.free[st], phase ^ 1, abort);
+            if constexpr (QUANT) {
+                // the tile's scale slot: read by the lanes four tiles ago
+                if (ok && is_k && j >= kScaleSlots) ok = wait_for(&sh.scales_free[j % kScaleSlots], (j / kScaleSlots - 1) & 1, abort);
+            }
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) return;
-            const uint32_t bar = tc_smem(&sh.full[issued % kFull]);
-            if (lane == 0) mbar_expect(bar, kTileBytes);
-            __syncwarp();
-            if (lane < kBlocks) tma_block(box + st * kTileBytes, map, y, bar);
+            const CUtensorMap *map = is_k ? &kmap : &vmap;
+            if constexpr (QUANT) {
+                const uint32_t bar = tc_smem(&sh.raw_full[st]);
+                const bool scaled = lane < kBlocks && b >= 0;
+                const int blocks = __popc(__ballot_sync(0xffffffffu, scaled));
+                float *slot = (is_k ? sh.ks : sh.vs)[j % kScaleSlots] + (lane < kBlocks ? lane : 0) * BS;
+                if (lane < kBlocks && b < 0)
+#pragma unroll
+                    for (int i = 0; i < BS; i += 4) *reinterpret_cast<float4 *>(slot + i) = make_float4(0.f, 0.f, 0.f, 0.f);
+                __syncwarp();
+                if (lane == 0) mbar_expect(bar, kRawBytes + blocks * BS * 4);
+                __syncwarp();
+                if (lane < kBlocks) tma_load(box + st * kRawBytes, map, 0, y, bar);
+                if (scaled) bulk_copy(tc_smem(slot), (is_k ? a.k_scale : a.v_scale) + ((int64_t)b * a.Hkv + u.kvh) * BS, BS * 4, bar);
+            } else {
+                const uint32_t bar = tc_smem(&sh.full[issued % kFull]);
+                if (lane == 0) mbar_expect(bar, kTileBytes);
+                __syncwarp();
+                if (lane < kBlocks) tma_block(box + st * kTileBytes, map, y, bar);
+            }
             ++issued;
-            if (++st == kStages) {
+            if (++st == kSlots) {
                 st = 0;
                 phase ^= 1;
             }
         };
-        while (ok && w.next(a)) {
-            if (!mine(w)) continue;
-            const int nblk = (w.ctx + BS - 1) / BS;
-            const int32_t *table = a.block_tables + (int64_t)w.s * a.M;
+        while (ok && have) {
+            u = nu;
+            const int nblk = (u.ctx + BS - 1) / BS;
+            const int32_t *table = a.block_tables + (int64_t)u.s * a.M;
             // the raw table entry of this lane's block of tile t; -2 for blocks past the context
             auto entry = [&](int t) {
-                const int idx = (w.t0 + t) * kBlocks + lane;
-                return t < w.n && lane < kBlocks && idx < nblk ? __ldg(table + idx) : -2;
+                const int idx = (u.t0 + t) * kBlocks + lane;
+                return t < u.n && lane < kBlocks && idx < nblk ? __ldg(table + idx) : -2;
             };
-            auto row_of = [&](int t, int b) {
-                if (b >= 0 && b < a.N) return (b * a.Hkv + w.kvh) * kGroups;
-                const int idx = (w.t0 + t) * kBlocks + lane;
-                if (t < w.n && lane < kBlocks && idx < nblk && member == 0) raise_flag(a.err_flag, PA_FLAG_BLOCK_OUT_OF_RANGE);
-                return oob;
+            auto checked = [&](int t, int b) {  // -1 where nothing is read
+                if (b >= 0 && b < a.N) return b;
+                const int idx = (u.t0 + t) * kBlocks + lane;
+                if (t < u.n && lane < kBlocks && idx < nblk && member == 0) raise_flag(a.err_flag, PA_FLAG_BLOCK_OUT_OF_RANGE);
+                return -1;
             };
+            auto row_of = [&](int b) { return b >= 0 ? (b * a.Hkv + u.kvh) * (QUANT ? BS : kGroups) : oob; };
             // With the ring's copies of all SMs queued up, a load that misses L2 takes several
             // microseconds: the unit's table entries are fetched into L2 at its start (32 to a
             // line) and loaded two tiles ahead of their copies, and the first unit's queries
             // go before all copies but one.
-            for (int i = lane * 32; i < w.n * kBlocks; i += 32 * 32) prefetch_l2(table + min(w.t0 * kBlocks + i, nblk - 1));
-            int y = row_of(0, entry(0)), e1 = entry(1), e2 = entry(2);
-            fill(&kmap, y);
+            for (int i = lane * 32; i < u.n * kBlocks; i += 32 * 32) prefetch_l2(table + min(u.t0 * kBlocks + i, nblk - 1));
+            int b = checked(0, entry(0)), e1 = entry(1), e2 = entry(2);
+            fill(true, row_of(b), b, tile);
             if (first) {
                 first = false;
-                ok = wait_for(&sh.qfull[0], 0, abort);
-                if (second(w) && ok) ok = wait_for(&sh.qfull[1], 0, abort);
+                if (ok) ok = wait_for(&sh.qfirst, 0, abort);
                 ok = __all_sync(0xffffffffu, ok);
             }
-            for (int t = 0; ok && t < w.n; ++t) {
-                const int yn = row_of(t + 1, e1);
+            have = next_unit(nu);
+            for (int t = 0; ok && t < u.n; ++t) {
+                const int bn = checked(t + 1, e1);
                 e1 = e2;
                 e2 = entry(t + 3);
-                if (SPLIT && t + 1 < w.n) fill(&kmap, yn);
-                if (ok) fill(&vmap, y);
-                if (!SPLIT && ok && t + 1 < w.n) fill(&kmap, yn);
-                y = yn;
+                if (SPLIT && t + 1 < u.n) fill(true, row_of(bn), bn, tile + t + 1);
+                if (ok) fill(false, row_of(b), b, tile + t);
+                if (!SPLIT && ok && t + 1 < u.n) fill(true, row_of(bn), bn, tile + t + 1);
+                b = bn;
             }
+            tile += u.n;
         }
         if (!ok) {
             // stopping early: copies already issued may still be landing in shared memory
-            for (int i = max(0, issued - kStages); i < issued; ++i)
-                mbar_wait(tc_smem(&sh.full[i % kFull]), (i / kFull) & 1);
+            for (int i = max(0, issued - kSlots); i < issued; ++i) {
+                if constexpr (QUANT)
+                    mbar_wait(tc_smem(&sh.raw_full[i % kSlots]), (i / kSlots) & 1);
+                else
+                    mbar_wait(tc_smem(&sh.full[i % kFull]), (i / kFull) & 1);
+            }
         }
     } else if (warp < 11) {
         // ---- products of lane l: one thread waits and issues (a thread per lane, so that one
         // lane's waits do not hold up the other's products)
         if (lane == 0) {
             const int l = warp - 9;
-            int ring = 0;
-            uint32_t pv = 0, qs = 0, taken = 0;
+            int ring = 0, units = 0;
+            uint32_t pv = 0, staged = 0, taken = 0;
             bool ok = true;
             const uint32_t t_s = tmem + kTmemS + l * 128, t_o = tmem + kTmemO + l * 128;
-            const uint64_t qd = sw128_desc(tc_smem(smem + kOffQ + l * kTileBytes), 16, kGroup);
-            const uint64_t kd = sw128_desc(tc_smem(smem + kOffRing), 16, kGroup);
-            const uint64_t vd = sw128_desc(tc_smem(smem + kOffRing), kHalf, kGroup);
+            const uint64_t qd = sw128_desc(tc_smem(smem), 16, kGroup);
+            const uint64_t kd = sw128_desc(tc_smem(smem + G::kOffRing), 16, kGroup);
+            const uint64_t vd = sw128_desc(tc_smem(smem + G::kOffRing), kHalf, kGroup);
+            // fp16 operands (8-bit caches) have type code 0 where bf16 has 1
+            constexpr uint32_t kType = QUANT ? (1u << 7) | (1u << 10) : 0u;
+            constexpr uint32_t kScores = bf16_idesc(128, kTile, 0) ^ kType, kWeighted = bf16_idesc(128, kD, 1) ^ kType;
             const uint32_t sfull = tc_smem(&sh.sfull[l]), odone = tc_smem(&sh.odone[l]);
-            while (ok && w.next(a)) {
-                if (!mine(w)) continue;
-                if (l == 1 && !second(w)) {
-                    // the other lane reads these tiles alone
-                    if constexpr (!SPLIT)
-                        for (int at = ring; ok && at < ring + 2 * w.n; ++at) {
+            Unit u, nu;
+            bool have = next_unit(nu);
+            while (ok && have) {
+                u = nu;
+                const bool two = second(u);
+                const int qb = SPLIT ? units++ % G::kQueries : l;
+                if (l == 1 && !two) {
+                    if constexpr (SPLIT) {
+                        // the buffer's other reader, once it is staged
+                        ok = wait_for(&sh.qfull[qb], (G::kQueries == 1 ? units - 1 : (units - 1) / 2) & 1, abort);
+                        if (ok) mbar_arrive(tc_smem(&sh.qfree[qb]));
+                    } else {
+                        // the other lane reads these tiles alone
+                        for (int at = ring; ok && at < ring + 2 * u.n; ++at) {
                             ok = wait_for(&sh.full[at % kFull], (at / kFull) & 1, abort);
                             if (ok) mbar_arrive(tc_smem(&sh.free[at % kStages]));
                         }
-                    ring += 2 * w.n;
+                    }
+                    ring += 2 * u.n;
+                    have = next_unit(nu);
                     continue;
                 }
                 auto landed = [&](int at) { return wait_for(&sh.full[at % kFull], (at / kFull) & 1, abort); };
-                auto scores = [&](int at) {
+                auto scores = [&](int at, bool last) {
                     tc_fence_after();
-                    const uint64_t k0 = kd + (uint64_t)(at % kStages * (kTileBytes >> 4));
+                    const uint64_t q0 = qd + (uint64_t)(qb * (kTileBytes >> 4)), k0 = kd + (uint64_t)(at % kStages * (kTileBytes >> 4));
 #pragma unroll
                     for (int kk = 0; kk < kD / 16; ++kk) {
                         const uint64_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
-                        umma(t_s, qd + off, k0 + off, bf16_idesc(128, kTile, 0), kk > 0);
+                        umma(t_s, q0 + off, k0 + off, kScores, kk > 0);
                     }
                     umma_commit(sfull);
+                    if (last) umma_commit(tc_smem(&sh.qfree[qb]));
                 };
                 auto weighted = [&](int at, bool first) {
                     tc_fence_after();
                     const uint64_t v0 = vd + (uint64_t)(at % kStages * (kTileBytes >> 4));
 #pragma unroll
                     for (int kk = 0; kk < kTile / 16; ++kk)
-                        umma_ts(t_o, t_s + kk * 8, v0 + (kk * 2 * kGroup >> 4), bf16_idesc(128, kD, 1), !first || kk > 0);
+                        umma_ts(t_o, t_s + kk * 8, v0 + (kk * 2 * kGroup >> 4), kWeighted, !first || kk > 0);
                     umma_commit(odone);
                     ++pv;
                 };
@@ -367,27 +493,32 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                 // Lanes that share their tiles take turns at the tensor cores, P V and the next
                 // S at a time: left alone they fall into step, both computing exponentials and
                 // then both waiting for products.  What a turn needs is waited for before it.
-                const bool turns = !SPLIT && second(w);
-                int k_pos = ring + k_at(t_first, w.n);
-                // (the queries first: their lane has seen every earlier unit's end)
-                ok = wait_for(&sh.qfull[l], qs++ & 1, abort) && landed(k_pos);
+                const bool turns = !SPLIT && two;
+                int k_pos = ring + k_at(t_first, u.n);
+                // the queries first: with alternating lanes they are staged once the unit before
+                // the last is done, which bounds how far ahead of the ring a lane asks
+                const uint32_t qphase = !SPLIT ? staged++ : (uint32_t)(G::kQueries == 1 ? units - 1 : (units - 1) / 2);
+                ok = wait_for(&sh.qfull[qb], qphase & 1, abort);
+                // S overwrites P: the lane's last P V is done
+                if (ok && pv > 0) ok = wait_for(&sh.odone[l], (pv - 1) & 1, abort);
+                if (ok) ok = landed(k_pos);
                 if (ok) {
-                    scores(k_pos);
+                    scores(k_pos, t_first + kStep >= u.n);
                     umma_commit(tc_smem(&sh.free[k_pos % kStages]));
                 }
-                for (int t = t_first; ok && t < w.n; t += kStep) {
-                    const bool more = t + kStep < w.n;
-                    const int v_pos = ring + v_at(t, w.n);
-                    k_pos = ring + k_at(t + kStep, w.n);
+                have = next_unit(nu);
+                for (int t = t_first; ok && t < u.n; t += kStep) {
+                    const bool more = t + kStep < u.n;
+                    const int v_pos = ring + v_at(t, u.n);
+                    k_pos = ring + k_at(t + kStep, u.n);
                     ok = landed(v_pos) && (SPLIT || !more || landed(k_pos)) && wait_for(&sh.pfull[l], pv & 1, abort);
                     if (ok && turns && (l == 1 || taken > 0)) ok = wait_for(&sh.turn[l], (l == 1 ? taken : taken - 1) & 1, abort);
                     if (!ok) break;
                     weighted(v_pos, t == t_first);
-                    // S overwrites P: P V is done first (this also orders O for its rows)
                     if (more) {
                         ok = wait_for(&sh.odone[l], (pv - 1) & 1, abort) && (!SPLIT || landed(k_pos));
                         if (!ok) break;
-                        scores(k_pos);
+                        scores(k_pos, t + 2 * kStep >= u.n);
                     }
                     if (turns) {
                         mbar_arrive(tc_smem(&sh.turn[l ^ 1]));
@@ -396,7 +527,7 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                     umma_commit(tc_smem(&sh.free[v_pos % kStages]));
                     if (more) umma_commit(tc_smem(&sh.free[k_pos % kStages]));
                 }
-                ring += 2 * w.n;
+                ring += 2 * u.n;
             }
             if (!ok) {
                 // stopping early: every product already issued finishes before tensor memory is released
@@ -405,81 +536,190 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
             }
         }
         __syncwarp();
+    } else if (warp == 11) {
+        // ---- queries: half a warp per row, copied asynchronously into the unit's buffer
+        // once the products that read its last contents are done
+        Unit u;
+        int units = 0, uses[2] = {0, 0};
+        bool ok = true;
+        const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;  // the columns take |scale|
+        while (ok && next_unit(u)) {
+            for (int l = 0; ok && l < (SPLIT || !second(u) ? 1 : 2); ++l) {
+                const int qb = SPLIT ? units % G::kQueries : l, use = uses[qb]++;
+                if (use > 0) ok = wait_for(&sh.qfree[qb], (use - 1) & 1, abort);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                unsigned char *buf = smem + qb * kTileBytes;
+                const int c0 = member * a.cols + l * kLaneCols, ch = lane & 15;
+#pragma unroll 4
+                for (int r = lane >> 4; r < kLaneCols; r += 2) {
+                    const int c = c0 + r;
+                    const int tok = a.g_shift >= 0 ? c >> a.g_shift : c / a.G, head = c - tok * a.G;
+                    const bool col = c < u.ncols;
+                    const int64_t pair = (int64_t)(u.r0 + tok) * a.Hq + u.kvh * a.G + head;
+                    tiled::cp_async16(tc_smem(buf + tile_chunk(r, ch)), col ? a.q + pair * kD + ch * 8 : a.q, col ? 16 : 0);
+                }
+                tiled::cp_async_wait_all();
+                if (QUANT || flip) {
+                    // 8-bit caches: as fp16 scaled by 2^sig per row, sig putting the row's largest
+                    // |q| in [2^13, 2^14).  Each lane rewrites what it copied itself.
+#pragma unroll 2
+                    for (int r = lane >> 4; r < kLaneCols; r += 2) {
+                        uint4 *at = reinterpret_cast<uint4 *>(buf + tile_chunk(r, ch));
+                        uint4 x = *at;
+                        uint32_t q[4] = {x.x ^ flip, x.y ^ flip, x.z ^ flip, x.w ^ flip};
+                        if constexpr (QUANT) {
+                            float f[8], amax = 0.f;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                f[2 * e] = __uint_as_float(q[e] << 16);
+                                f[2 * e + 1] = __uint_as_float(q[e] & 0xffff0000u);
+                                amax = fmaxf(amax, fmaxf(fabsf(f[2 * e]), fabsf(f[2 * e + 1])));
+                            }
+#pragma unroll
+                            for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                            const int sig = amax > 0.f ? min(100, max(-100, 14 - tiled::exponent_above(amax))) : 0;
+                            const float up = ldexpf(1.f, sig);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) q[e] = tiled::f16x2(f[2 * e] * up, f[2 * e + 1] * up);
+                            if (ch == 0) sh.rs[qb][r] = fabsf(a.scale_log2) * ldexpf(1.f, -sig);
+                        }
+                        *at = make_uint4(q[0], q[1], q[2], q[3]);
+                    }
+                }
+                fence_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(tc_smem(&sh.qfull[qb]));
+            }
+            if (units++ == 0 && lane == 0) mbar_arrive(tc_smem(&sh.qfirst));
+        }
+    } else if (QUANT) {
+        // ---- 8-bit caches: codes to fp16, a piece of 16 codes of a row at a time
+        const int me = tid - 12 * 32;
+        int ring = 0, tile = 0;
+        bool ok = true;
+        Unit u;
+        while (ok && next_unit(u)) {
+            // positions in the order of use: tile and kind of position i
+            for (int i = 0; ok && i < 2 * u.n; ++i, ++ring) {
+                bool is_k;
+                int t;
+                if (SPLIT) {
+                    is_k = i == 0 || ((i & 1) && i < 2 * u.n - 1);
+                    t = is_k ? (i + 1) / 2 : i == 2 * u.n - 1 ? u.n - 1 : i / 2 - 1;
+                } else {
+                    is_k = !(i & 1);
+                    t = i / 2;
+                }
+                const int rst = ring % (G::kRaw ? G::kRaw : 1), st = ring % kStages, j = tile + t;
+                ok = wait_for(&sh.raw_full[rst], ring / (G::kRaw ? G::kRaw : 1) & 1, abort);
+                if (ok && ring >= kStages) ok = wait_for(&sh.free[st], (ring / kStages - 1) & 1, abort);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                const int left = u.ctx - (u.t0 + t) * kTile;  // tokens of the context from the tile on
+                // tokens behind the context: scales may hold anything
+                if (me >= left) (is_k ? sh.ks : sh.vs)[j % kScaleSlots][me] = 0.f;
+                mbar_arrive(tc_smem(&sh.scales[j % (2 * kScaleSlots)]));
+                const unsigned char *raw = smem + G::kOffRaw + rst * kRawBytes;
+                unsigned char *to = smem + G::kOffRing + st * kTileBytes;
+                const int c = me & 7, sw = c >> 2;  // piece of the row; which half is stored first (no bank conflicts)
+#pragma unroll
+                for (int r = me >> 3; r < kTile; r += 16) {
+                    uint4 h[2];
+                    exact_f16<KV>(*reinterpret_cast<const uint4 *>(raw + r * kD + c * 16), h[0], h[1]);
+                    if (r >= left) h[0] = h[1] = make_uint4(0u, 0u, 0u, 0u);  // a code may be a NaN
+                    *reinterpret_cast<uint4 *>(to + tile_chunk(r, 2 * c + sw)) = sw ? h[1] : h[0];
+                    *reinterpret_cast<uint4 *>(to + tile_chunk(r, 2 * c + 1 - sw)) = sw ? h[0] : h[1];
+                }
+                fence_async();
+                mbar_arrive(tc_smem(&sh.full[ring % kFull]));
+                mbar_arrive(tc_smem(&sh.raw_free[rst]));
+            }
+            tile += u.n;
+        }
     }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsColumns));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(G::kRegsColumns));
         // ---- a lane's columns: thread = column = tensor-memory lane
         const int l = warp >> 2, row = tid & 127;
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t t_s = tmem + lane_off + kTmemS + l * 128, t_o = tmem + lane_off + kTmemO + l * 128;
-        unsigned char *qbuf = smem + kOffQ + l * kTileBytes;
-        int done = 0, ring = 0, joins = 0;  // tiles of this lane; ring position; units joined
+        int done = 0, ring = 0, joins = 0, tile = 0, units = 0, staged = 0;  // tiles of this lane; ring position; ..
         bool ok = true;
-        while (ok && w.next(a)) {
-            if (!mine(w)) continue;
-            const bool two = second(w);
+        Unit u, nu;
+        bool have = next_unit(nu);
+        while (ok && have) {
+            u = nu;
+            const bool two = second(u);
             const bool active = l == 0 || two;
+            const int qb = SPLIT ? units % G::kQueries : l;
+            const uint32_t qphase = SPLIT ? units / G::kQueries : staged;
+            ++units;
+            have = next_unit(nu);
             if (!SPLIT && !active) {
-                ring += 2 * w.n;
+                if constexpr (QUANT) {  // the other lane reads these tiles' scales alone
+                    for (int t = 0; ok && t < u.n; ++t) {
+                        const int j = tile + t;
+                        ok = wait_for(&sh.scales[j % (2 * kScaleSlots)], j / (2 * kScaleSlots) & 1, abort);
+                        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                        mbar_arrive(tc_smem(&sh.scales_free[j % kScaleSlots]));
+                    }
+                }
+                ring += 2 * u.n;
+                tile += u.n;
                 continue;
             }
+            ++staged;
             const int c = member * a.cols + (SPLIT ? 0 : l * kLaneCols) + row;
-            const bool col = c < w.ncols;
-            const int tok = a.g_shift >= 0 ? c >> a.g_shift : c / a.G, head = c - tok * a.G;
-            const int64_t pair = (int64_t)(w.r0 + tok) * a.Hq + w.kvh * a.G + head;
-            float m = -INFINITY, sum_l = 0.f;
-            if (active) {
-                // the unit's queries (this lane's products with the last unit's are done): a
-                // row at a time by half a warp
-                uint4 x[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int r = 2 * i + (lane >> 4);
-                    const int64_t from = __shfl_sync(0xffffffffu, col ? pair : -1, r);
-                    x[i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (from >= 0) x[i] = __ldg(reinterpret_cast<const uint4 *>(a.q + from * kD) + (lane & 15));
-                }
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    *reinterpret_cast<uint4 *>(qbuf + tile_chunk((warp & 3) * 32 + 2 * i + (lane >> 4), lane & 15)) = x[i];
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                mbar_arrive(tc_smem(&sh.qfull[l]));
-            }
-            // the next unit's queries into L2, long before they are loaded
-            {
-                Walk u = w;
-                if (u.next(a) && mine(u) && (SPLIT || l == 0 || second(u)) && c < u.ncols) {
-                    const uint16_t *src = a.q + ((int64_t)(u.r0 + tok) * a.Hq + u.kvh * a.G + head) * kD;
-                    prefetch_l2(src);
-                    prefetch_l2(src + 64);
-                }
+            const bool col = c < u.ncols;
+            float m = -INFINITY, sum_l = 0.f, rs = fabsf(a.scale_log2);
+            if constexpr (QUANT) {
+                ok = wait_for(&sh.qfull[qb], qphase & 1, abort);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                rs = sh.rs[qb][row];
+                mbar_arrive(tc_smem(&sh.qfree[qb]));
             }
             // a warp none of whose columns is real keeps step without computing
-            const bool idle = member * a.cols + (SPLIT ? 0 : l * kLaneCols) + (warp & 3) * 32 >= w.ncols;
-            for (int t = SPLIT ? l : 0; t < w.n; t += SPLIT ? 2 : 1) {
+            const bool idle = member * a.cols + (SPLIT ? 0 : l * kLaneCols) + (warp & 3) * 32 >= u.ncols;
+            for (int t = SPLIT ? l : 0; t < u.n; t += SPLIT ? 2 : 1) {
+                const int j = tile + t;
                 ok = wait_for(&sh.sfull[l], done & 1, abort);
+                if (QUANT && ok) ok = wait_for(&sh.scales[j % (2 * kScaleSlots)], j / (2 * kScaleSlots) & 1, abort);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 tc_fence_after();
-                const int k0 = (w.t0 + t) * kTile;
+                const int k0 = (u.t0 + t) * kTile;
                 if (!idle) {
                     float sv[kTile];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) tmem_ld32(t_s + 32 * q, sv + 32 * q);
                     tmem_wait_ld();
-                    if (k0 + kTile > w.ctx) {
+                    float over = 0.f;  // 8-bit: exponent of the tile's largest value scale
+                    if constexpr (QUANT) {
+                        const float4 *ks = reinterpret_cast<const float4 *>(sh.ks[j % kScaleSlots]);
+#pragma unroll
+                        for (int k = 0; k < kTile / 4; ++k) {
+                            const float4 x = ks[k];
+                            sv[4 * k] *= x.x;
+                            sv[4 * k + 1] *= x.y;
+                            sv[4 * k + 2] *= x.z;
+                            sv[4 * k + 3] *= x.w;
+                        }
+                        const float4 x = reinterpret_cast<const float4 *>(sh.vs[j % kScaleSlots])[lane];
+                        const uint32_t top = __float_as_uint(fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))));
+                        over = exponent_over(__reduce_max_sync(0xffffffffu, top));
+                    }
+                    if (k0 + kTile > u.ctx) {
 #pragma unroll
                         for (int k = 0; k < kTile; ++k)
-                            if (k0 + k >= w.ctx) sv[k] = -INFINITY;
+                            if (k0 + k >= u.ctx) sv[k] = -INFINITY;
                     }
                     float mx[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) mx[i] = sv[i];
 #pragma unroll
                     for (int k = 8; k < kTile; ++k) mx[k & 7] = fmaxf(mx[k & 7], sv[k]);
-                    const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                                            fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) *
-                                      a.scale_log2;
-                    // the running maximum is raised only by more than 2^8; then l and O shrink
+                    const float top = fmaf(fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                                 fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))),
+                                           rs, over);
+                    // the running base is raised only by more than 2^8; then l and O shrink
                     float f = 1.f;
                     bool shrink = false;
                     if (top > m + kRescaleLog2) {
@@ -507,59 +747,55 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                     for (int q = 0; q < 2; ++q) {
                         float pw[32];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const int k = 64 * q + 2 * i;
-                            const float p0 = tc_exp2(fmaf(sv[k], a.scale_log2, -base));
-                            const float p1 = tc_exp2(fmaf(sv[k + 1], a.scale_log2, -base));
-                            ls[i & 3] += p0 + p1;
-                            pw[i] = __uint_as_float(tc_bf16x2(p0, p1));
+                        for (int i = 0; i < 32; i += 2) {
+                            float p[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                p[e] = tc_exp2(fmaf(sv[64 * q + 2 * i + e], rs, -base));
+                                ls[e] += p[e];
+                            }
+                            if constexpr (QUANT) {
+                                const float4 x = reinterpret_cast<const float4 *>(sh.vs[j % kScaleSlots])[16 * q + i / 2];
+                                pw[i] = __uint_as_float(tiled::f16x2(p[0] * x.x, p[1] * x.y));
+                                pw[i + 1] = __uint_as_float(tiled::f16x2(p[2] * x.z, p[3] * x.w));
+                            } else {
+                                pw[i] = __uint_as_float(tc_bf16x2(p[0], p[1]));
+                                pw[i + 1] = __uint_as_float(tc_bf16x2(p[2], p[3]));
+                            }
                         }
                         tmem_st32(t_s + 32 * q, pw);
                     }
                     sum_l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
                     tmem_wait_st();
                 }
-                // rows past the context inside its last block may hold anything, and a zero
-                // weight times a NaN is a NaN: zero them in the V stage
-                if (k0 + kTile > w.ctx && w.ctx % BS != 0) {
-                    const int at = ring + v_at(t, w.n), st = at % kStages;
+                if constexpr (QUANT) {
+                    mbar_arrive(tc_smem(&sh.scales_free[j % kScaleSlots]));
+                } else if (k0 + kTile > u.ctx && u.ctx % BS != 0) {
+                    // rows past the context inside its last block may hold anything, and a zero
+                    // weight times a NaN is a NaN: zero them in the V stage
+                    const int at = ring + v_at(t, u.n), st = at % kStages;
                     ok = wait_for(&sh.full[at % kFull], (at / kFull) & 1, abort);
                     if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                    const int lo = w.ctx - k0, hi = min(kTile, (w.ctx + BS - 1) / BS * BS - k0);
-                    unsigned char *vst = smem + kOffRing + st * kTileBytes;
+                    const int lo = u.ctx - k0, hi = min(kTile, (u.ctx + BS - 1) / BS * BS - k0);
+                    unsigned char *vst = smem + G::kOffRing + st * kTileBytes;
                     for (int i = row; i < (hi - lo) * 16; i += kLaneCols)
                         *reinterpret_cast<uint4 *>(vst + tile_chunk(lo + i / 16, i % 16)) = make_uint4(0u, 0u, 0u, 0u);
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    fence_async();
                 }
                 tc_fence_before();
                 mbar_arrive(tc_smem(&sh.pfull[l]));
                 ++done;
             }
-            ring += 2 * w.n;
+            ring += 2 * u.n;
+            tile += u.n;
             if (!ok) break;
-            // ---- the columns' partials, 32 dims at a time through the query buffer (the unit's
-            // products with it are done): rows by threads in, 128-byte pieces of rows out
-            const bool all = w.t0 == 0 && w.n == w.tiles;
-            const int64_t at = all ? pair : ((int64_t)blockIdx.x * 2 + (w.t0 == 0 ? 1 : 0)) * a.cols + (c - member * a.cols);
-            float *acc = all ? a.whole_acc : a.cut_acc;
+            // ---- the columns' partials: a thread's row, a sector at a time
+            const int tok = a.g_shift >= 0 ? c >> a.g_shift : c / a.G, head = c - tok * a.G;
+            const int64_t pair = (int64_t)(u.r0 + tok) * a.Hq + u.kvh * a.G + head;
+            const bool all = u.t0 == 0 && u.n == u.tiles;
+            const int64_t at = all ? pair : ((int64_t)blockIdx.x * 2 + (u.t0 == 0 ? 1 : 0)) * a.cols + (c - member * a.cols);
+            float *acc = (all ? a.whole_acc : a.cut_acc) + at * kD;
             float2 *ml = reinterpret_cast<float2 *>(all ? a.whole_ml : a.cut_ml) + at;
-            constexpr int kPitch = 144;  // of a staged row of 128 bytes: no bank conflicts
-            unsigned char *stage = qbuf + (warp & 3) * 32 * kPitch;
-            auto put = [&](const float (&ov)[32], int q) {
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    *reinterpret_cast<float4 *>(stage + lane * kPitch + i * 16) =
-                        make_float4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int r = 4 * i + (lane >> 3);
-                    const int64_t to = __shfl_sync(0xffffffffu, col ? at : -1, r);
-                    const float4 x = *reinterpret_cast<const float4 *>(stage + r * kPitch + (lane & 7) * 16);
-                    if (to >= 0) *reinterpret_cast<float4 *>(acc + to * kD + 32 * q + (lane & 7) * 4) = x;
-                }
-            };
             if (active) ok = wait_for(&sh.odone[l], (done - 1) & 1, abort);
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
             tc_fence_after();
@@ -569,7 +805,11 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                     float ov[32];
                     tmem_ld32(t_o + 32 * q, ov);
                     tmem_wait_ld();
-                    put(ov, q);
+                    if (col) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) store8(acc + 32 * q + 8 * i, ov + 8 * i);
+                    }
+                    __syncwarp();
                 }
                 if (col) *ml = make_float2(m, sum_l);
             } else {
@@ -597,7 +837,11 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
 #pragma unroll
                         for (int i = 0; i < 32; ++i) ov[i] = fmaf(other[i], fy, ov[i]);
                     }
-                    put(ov, q);
+                    if (col) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) store8(acc + 32 * q + 8 * i, ov + 8 * i);
+                    }
+                    __syncwarp();
                 }
                 if (col && l == 0) *ml = make_float2(top, x.y * fx + y.y * fy);
                 // O may be overwritten, and ml, once both lanes have read them
@@ -618,47 +862,68 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
     if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
-// A cache pool [N][Hkv][bs][128] bf16 as [8-row group][64-dim half][8 rows][64], copied a
-// block at a time with the 128-byte swizzle.
-bool pool_map(CUtensorMap *map, const void *pool, int groups, int bs) {
+// A bf16 pool [N][Hkv][bs][128] as [8-row group][64-dim half][8 rows][64], copied a block at
+// a time with the 128-byte swizzle; a pool of 8-bit codes as rows of 128 bytes, copied a
+// block at a time as they are.
+bool pool_map(CUtensorMap *map, const void *pool, int rows, int bs, bool codes) {
     const EncodeTiled fn = encode_tiled();
     if (!fn) return false;
-    const cuuint64_t dims[4] = {64, 8, 2, (cuuint64_t)groups};
+    const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    if (codes) {
+        const cuuint64_t dims[2] = {(cuuint64_t)kD, (cuuint64_t)rows};
+        const cuuint64_t strides[1] = {(cuuint64_t)kD};
+        const cuuint32_t box[2] = {(cuuint32_t)kD, (cuuint32_t)bs};
+        return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(pool), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    }
+    const cuuint64_t dims[4] = {64, 8, 2, (cuuint64_t)(rows / 8)};
     const cuuint64_t strides[3] = {kD * 2, 128, 8 * kD * 2};
     const cuuint32_t box[4] = {64u, 8u, 2u, (cuuint32_t)(bs / 8)};
-    const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(pool), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BS, bool SPLIT>
+template <typename KV, int BS, bool SPLIT>
 cudaError_t launch_typed(const TreeContext &a, cudaStream_t stream) {
+    using G = Geo<KV, SPLIT>;
+    constexpr int kSmem = G::kOffShared + (int)sizeof(Shared<G>);
     CUtensorMap kmap, vmap;
     if ((int64_t)a.N * a.Hkv * BS >= (int64_t)INT32_MAX) return cudaErrorInvalidValue;  // TMA coordinates
-    const int groups = a.N * a.Hkv * (BS / 8);
-    if (!pool_map(&kmap, a.k_cache, groups, BS) || !pool_map(&vmap, a.v_cache, groups, BS)) return cudaErrorInvalidValue;
+    const int rows = a.N * a.Hkv * BS;
+    if (!pool_map(&kmap, a.k_cache, rows, BS, G::kQuant) || !pool_map(&vmap, a.v_cache, rows, BS, G::kQuant))
+        return cudaErrorInvalidValue;
     static std::atomic<bool> configured[64];  // per device: the shared-memory attribute is set
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!configured[dev].load(std::memory_order_acquire)) {
         const cudaError_t e =
-            cudaFuncSetAttribute(tree_tc_kernel<BS, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+            cudaFuncSetAttribute(tree_tc_kernel<KV, BS, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return e;
         configured[dev].store(true, std::memory_order_release);
     }
-    return launch_dependent(tree_tc_kernel<BS, SPLIT>, dim3(a.groups * a.members), dim3(kThreads), kSmem, stream, a, kmap,
-                            vmap);
+    return launch_dependent(tree_tc_kernel<KV, BS, SPLIT>, dim3(a.groups * a.members), dim3(G::kThreads), kSmem, stream, a,
+                            kmap, vmap);
+}
+
+template <typename KV>
+cudaError_t launch_kv(const TreeContext &a, int bs, cudaStream_t stream) {
+    if (a.cols == kLaneCols)
+        return bs == 16 ? launch_typed<KV, 16, true>(a, stream) : launch_typed<KV, 32, true>(a, stream);
+    return bs == 16 ? launch_typed<KV, 16, false>(a, stream) : launch_typed<KV, 32, false>(a, stream);
 }
 
 }  // namespace
 
-bool tree_tc_eligible(int D, int kv_dtype) { return D == kD && kv_dtype == PA_KV_BF16; }
+bool tree_tc_eligible(int D, int kv_dtype) {
+    return D == kD && (kv_dtype == PA_KV_BF16 || kv_dtype == PA_KV_INT8 || kv_dtype == PA_KV_FP8);
+}
 
 cudaError_t launch_tree_tc(const TreeContext &a, int bs, int kv_dtype, cudaStream_t stream) {
-    if (kv_dtype != PA_KV_BF16) return cudaErrorInvalidValue;
-    if (a.cols == kLaneCols) return bs == 16 ? launch_typed<16, true>(a, stream) : launch_typed<32, true>(a, stream);
-    return bs == 16 ? launch_typed<16, false>(a, stream) : launch_typed<32, false>(a, stream);
+    if (kv_dtype == PA_KV_INT8) return launch_kv<int8_t>(a, bs, stream);
+    if (kv_dtype == PA_KV_FP8) return launch_kv<tiled::e4m3_tag>(a, bs, stream);
+    return launch_kv<uint16_t>(a, bs, stream);
 }
 
 }  // namespace pa
