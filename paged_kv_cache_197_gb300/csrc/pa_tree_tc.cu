@@ -12,8 +12,11 @@
 //     tile; with at most 128 they take the same columns and alternate tiles, and are
 //     joined at the end of a unit.  Either way one lane's exponentials run while the
 //     tensor cores work for the other;
+//     The columns' threads also stage their lane's queries: the next unit's are copied
+//     asynchronously once the last S of a unit is in, behind its last exponentials and the
+//     write of its partials;
 //   * warp 8 copies K and V tiles (TMA); one thread each of warps 9 and 10 issues a lane's
-//     products; warp 11 stages the units' queries, a unit ahead where it has a buffer;
+//     products (warp 11 fills the warpgroup, whose spare registers go to the columns);
 //   * 8-bit caches: warp 8 copies codes into a ring of 16 KB stages, and warps 12-15 turn
 //     them into exact fp16 in the stages the products read.
 // Tensor memory: S of the lanes at columns 0 and 128 (overwritten by P as 16-bit pairs, the A
@@ -65,9 +68,10 @@ template <typename KV, bool SPLIT>
 struct Geo {
     static constexpr bool kQuant = sizeof(KV) == 1;
     static constexpr int kStages = kQuant ? 3 : 5, kFull = 2 * kStages;
-    // query buffers: one per lane; lanes on the same columns share one, and alternate two
-    // from unit to unit where there is room
+    // query buffers: one per lane, or one for both lanes where they have the same columns and
+    // codes need the room
     static constexpr int kQueries = kQuant && SPLIT ? 1 : 2;
+    static constexpr bool kShared = kQueries == 1;
     static constexpr int kRaw = !kQuant ? 0 : SPLIT ? 5 : 3;  // stages of codes
     static constexpr int kOffRing = kQueries * kTileBytes, kOffRaw = kOffRing + kStages * kTileBytes;
     static constexpr int kOffShared = kOffRaw + kRaw * kRawBytes;
@@ -87,8 +91,7 @@ struct Shared {
     uint64_t raw_full[G::kQuant ? G::kRaw : 1], raw_free[G::kQuant ? G::kRaw : 1];
     uint64_t scales[2 * kScaleSlots], scales_free[kScaleSlots];
     uint64_t sfull[2], pfull[2], odone[2];      // per lane: S written, P written, P V done
-    uint64_t qfull[2], qfree[2];                // query buffers: staged / products with it issued and done
-    uint64_t qfirst;                            // the first unit's queries are staged
+    uint64_t qfull[2];                          // query buffers staged
     uint64_t mlready, oread;                    // lanes joined: both (base, sum) and O in / read
     uint64_t turn[2];                           // shared tiles: the lane may issue its next products
     uint64_t drain[2];
@@ -184,11 +187,14 @@ struct Walk {
                 continue;
             }
             const int64_t in = pos - before;
-            const int off = (int)(in % len);
+            if (len * a.Hkv <= 0x7fffffff)
+                u.kvh = (int)((uint32_t)in / (uint32_t)len);
+            else
+                u.kvh = (int)(in / len);
+            const int off = (int)(in - u.kvh * len);
             const int64_t step = min(len - off, end - pos);
             pos += step;
             u.s = s;
-            u.kvh = (int)(in / len);
             u.t0 = max(0, off - kTreePad);
             u.n = (int)(off + step) - kTreePad - u.t0;
             u.tiles = tiles;
@@ -230,32 +236,30 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
         return;
     }
     const int group = blockIdx.x / a.members, member = blockIdx.x % a.members;
-    if (tid == 0) {
-        for (int i = 0; i < kFull; ++i) mbar_init_n(tc_smem(&sh.full[i]), QUANT ? 128 : 1);
-        for (int i = 0; i < kStages; ++i) mbar_init_n(tc_smem(&sh.free[i]), SPLIT ? 1 : 2);  // lanes that read a stage
-        for (int i = 0; i < G::kRaw; ++i) {
+    if (warp == 1) {
+        for (int i = lane; i < kFull; i += 32) mbar_init_n(tc_smem(&sh.full[i]), QUANT ? 128 : 1);
+        for (int i = lane; i < kStages; i += 32) mbar_init_n(tc_smem(&sh.free[i]), SPLIT ? 1 : 2);  // lanes that read a stage
+        for (int i = lane; i < G::kRaw; i += 32) {
             mbar_init(tc_smem(&sh.raw_full[i]));
             mbar_init_n(tc_smem(&sh.raw_free[i]), 128);
         }
-        for (int i = 0; i < 2 * kScaleSlots; ++i) mbar_init_n(tc_smem(&sh.scales[i]), 2 * 128);
-        for (int i = 0; i < kScaleSlots; ++i) mbar_init_n(tc_smem(&sh.scales_free[i]), SPLIT ? kLaneCols : 2 * kLaneCols);
-        for (int w = 0; w < 2; ++w) {
-            mbar_init(tc_smem(&sh.sfull[w]));
-            mbar_init(tc_smem(&sh.odone[w]));
-            mbar_init_n(tc_smem(&sh.pfull[w]), kLaneCols);
-            mbar_init(tc_smem(&sh.qfull[w]));
-            // the lanes' products that read it; 8-bit: and their columns, which read its factors
-            mbar_init_n(tc_smem(&sh.qfree[w]), (SPLIT ? 2 : 1) * (QUANT ? 1 + kLaneCols : 1));
-            mbar_init(tc_smem(&sh.turn[w]));
-            mbar_init(tc_smem(&sh.drain[w]));
+        if (QUANT && lane < 2 * kScaleSlots) mbar_init_n(tc_smem(&sh.scales[lane]), 2 * 128);
+        if (QUANT && lane < kScaleSlots) mbar_init_n(tc_smem(&sh.scales_free[lane]), SPLIT ? kLaneCols : 2 * kLaneCols);
+        if (lane < 2) {
+            mbar_init(tc_smem(&sh.sfull[lane]));
+            mbar_init(tc_smem(&sh.odone[lane]));
+            mbar_init_n(tc_smem(&sh.pfull[lane]), kLaneCols);
+            mbar_init_n(tc_smem(&sh.qfull[lane]), G::kShared ? 2 * kLaneCols : kLaneCols);
+            mbar_init(tc_smem(&sh.turn[lane]));
+            mbar_init(tc_smem(&sh.drain[lane]));
+            mbar_init_n(tc_smem(lane ? &sh.mlready : &sh.oread), 2 * kLaneCols + (lane && G::kShared ? 1 : 0));
         }
-        mbar_init(tc_smem(&sh.qfirst));
-        mbar_init_n(tc_smem(&sh.mlready), 2 * kLaneCols);
-        mbar_init_n(tc_smem(&sh.oread), 2 * kLaneCols);
-        sh.abort = 0;
-        sh.first_seq = 0;
-        sh.first_tile = 0;
-        sh.total = 0;
+        if (lane == 0) {
+            sh.abort = 0;
+            sh.first_seq = 0;
+            sh.first_tile = 0;
+            sh.total = 0;
+        }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 0) {
@@ -404,8 +408,8 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
             int b = checked(0, entry(0)), e1 = entry(1), e2 = entry(2);
             fill(true, row_of(b), b, tile);
             if (first) {
-                first = false;
-                if (ok) ok = wait_for(&sh.qfirst, 0, abort);
+                first = false;  // (their barrier's next phase needs this unit's other tiles)
+                if (ok) ok = wait_for(&sh.qfull[0], 0, abort);
                 ok = __all_sync(0xffffffffu, ok);
             }
             have = next_unit(nu);
@@ -434,7 +438,7 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
         // lane's waits do not hold up the other's products)
         if (lane == 0) {
             const int l = warp - 9;
-            int ring = 0, units = 0;
+            int ring = 0;
             uint32_t pv = 0, staged = 0, taken = 0;
             bool ok = true;
             const uint32_t t_s = tmem + kTmemS + l * 128, t_o = tmem + kTmemO + l * 128;
@@ -450,25 +454,25 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
             while (ok && have) {
                 u = nu;
                 const bool two = second(u);
-                const int qb = SPLIT ? units++ % G::kQueries : l;
+                const int qb = G::kShared ? 0 : l;
                 if (l == 1 && !two) {
-                    if constexpr (SPLIT) {
-                        // the buffer's other reader, once it is staged
-                        ok = wait_for(&sh.qfull[qb], (G::kQueries == 1 ? units - 1 : (units - 1) / 2) & 1, abort);
-                        if (ok) mbar_arrive(tc_smem(&sh.qfree[qb]));
-                    } else {
-                        // the other lane reads these tiles alone
-                        for (int at = ring; ok && at < ring + 2 * u.n; ++at) {
-                            ok = wait_for(&sh.full[at % kFull], (at / kFull) & 1, abort);
-                            if (ok) mbar_arrive(tc_smem(&sh.free[at % kStages]));
-                        }
+                    // shared queries are staged for every unit: the unit does not end before this
+                    // thread has seen its own (a phase later the parity would say nothing)
+                    if (G::kShared) {
+                        ok = wait_for(&sh.qfull[0], staged++ & 1, abort);
+                        if (ok) mbar_arrive(tc_smem(&sh.mlready));
+                    }
+                    // the other lane reads these tiles alone
+                    for (int at = ring; !SPLIT && ok && at < ring + 2 * u.n; ++at) {
+                        ok = wait_for(&sh.full[at % kFull], (at / kFull) & 1, abort);
+                        if (ok) mbar_arrive(tc_smem(&sh.free[at % kStages]));
                     }
                     ring += 2 * u.n;
                     have = next_unit(nu);
                     continue;
                 }
                 auto landed = [&](int at) { return wait_for(&sh.full[at % kFull], (at / kFull) & 1, abort); };
-                auto scores = [&](int at, bool last) {
+                auto scores = [&](int at) {
                     tc_fence_after();
                     const uint64_t q0 = qd + (uint64_t)(qb * (kTileBytes >> 4)), k0 = kd + (uint64_t)(at % kStages * (kTileBytes >> 4));
 #pragma unroll
@@ -477,7 +481,6 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                         umma(t_s, q0 + off, k0 + off, kScores, kk > 0);
                     }
                     umma_commit(sfull);
-                    if (last) umma_commit(tc_smem(&sh.qfree[qb]));
                 };
                 auto weighted = [&](int at, bool first) {
                     tc_fence_after();
@@ -495,15 +498,15 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                 // then both waiting for products.  What a turn needs is waited for before it.
                 const bool turns = !SPLIT && two;
                 int k_pos = ring + k_at(t_first, u.n);
-                // the queries first: with alternating lanes they are staged once the unit before
-                // the last is done, which bounds how far ahead of the ring a lane asks
-                const uint32_t qphase = !SPLIT ? staged++ : (uint32_t)(G::kQueries == 1 ? units - 1 : (units - 1) / 2);
-                ok = wait_for(&sh.qfull[qb], qphase & 1, abort);
+                // the queries first: they are staged when the lane's last unit is done, which
+                // bounds how far ahead of the ring a lane asks
+                ok = wait_for(&sh.qfull[qb], staged++ & 1, abort);
+                if (ok && G::kShared && l == 1) mbar_arrive(tc_smem(&sh.mlready));
                 // S overwrites P: the lane's last P V is done
                 if (ok && pv > 0) ok = wait_for(&sh.odone[l], (pv - 1) & 1, abort);
                 if (ok) ok = landed(k_pos);
                 if (ok) {
-                    scores(k_pos, t_first + kStep >= u.n);
+                    scores(k_pos);
                     umma_commit(tc_smem(&sh.free[k_pos % kStages]));
                 }
                 have = next_unit(nu);
@@ -518,7 +521,7 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                     if (more) {
                         ok = wait_for(&sh.odone[l], (pv - 1) & 1, abort) && (!SPLIT || landed(k_pos));
                         if (!ok) break;
-                        scores(k_pos, t + 2 * kStep >= u.n);
+                        scores(k_pos);
                     }
                     if (turns) {
                         mbar_arrive(tc_smem(&sh.turn[l ^ 1]));
@@ -536,63 +539,7 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
             }
         }
         __syncwarp();
-    } else if (warp == 11) {
-        // ---- queries: half a warp per row, copied asynchronously into the unit's buffer
-        // once the products that read its last contents are done
-        Unit u;
-        int units = 0, uses[2] = {0, 0};
-        bool ok = true;
-        const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;  // the columns take |scale|
-        while (ok && next_unit(u)) {
-            for (int l = 0; ok && l < (SPLIT || !second(u) ? 1 : 2); ++l) {
-                const int qb = SPLIT ? units % G::kQueries : l, use = uses[qb]++;
-                if (use > 0) ok = wait_for(&sh.qfree[qb], (use - 1) & 1, abort);
-                if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                unsigned char *buf = smem + qb * kTileBytes;
-                const int c0 = member * a.cols + l * kLaneCols, ch = lane & 15;
-#pragma unroll 4
-                for (int r = lane >> 4; r < kLaneCols; r += 2) {
-                    const int c = c0 + r;
-                    const int tok = a.g_shift >= 0 ? c >> a.g_shift : c / a.G, head = c - tok * a.G;
-                    const bool col = c < u.ncols;
-                    const int64_t pair = (int64_t)(u.r0 + tok) * a.Hq + u.kvh * a.G + head;
-                    tiled::cp_async16(tc_smem(buf + tile_chunk(r, ch)), col ? a.q + pair * kD + ch * 8 : a.q, col ? 16 : 0);
-                }
-                tiled::cp_async_wait_all();
-                if (QUANT || flip) {
-                    // 8-bit caches: as fp16 scaled by 2^sig per row, sig putting the row's largest
-                    // |q| in [2^13, 2^14).  Each lane rewrites what it copied itself.
-#pragma unroll 2
-                    for (int r = lane >> 4; r < kLaneCols; r += 2) {
-                        uint4 *at = reinterpret_cast<uint4 *>(buf + tile_chunk(r, ch));
-                        uint4 x = *at;
-                        uint32_t q[4] = {x.x ^ flip, x.y ^ flip, x.z ^ flip, x.w ^ flip};
-                        if constexpr (QUANT) {
-                            float f[8], amax = 0.f;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                f[2 * e] = __uint_as_float(q[e] << 16);
-                                f[2 * e + 1] = __uint_as_float(q[e] & 0xffff0000u);
-                                amax = fmaxf(amax, fmaxf(fabsf(f[2 * e]), fabsf(f[2 * e + 1])));
-                            }
-#pragma unroll
-                            for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                            const int sig = amax > 0.f ? min(100, max(-100, 14 - tiled::exponent_above(amax))) : 0;
-                            const float up = ldexpf(1.f, sig);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) q[e] = tiled::f16x2(f[2 * e] * up, f[2 * e + 1] * up);
-                            if (ch == 0) sh.rs[qb][r] = fabsf(a.scale_log2) * ldexpf(1.f, -sig);
-                        }
-                        *at = make_uint4(q[0], q[1], q[2], q[3]);
-                    }
-                }
-                fence_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(tc_smem(&sh.qfull[qb]));
-            }
-            if (units++ == 0 && lane == 0) mbar_arrive(tc_smem(&sh.qfirst));
-        }
-    } else if (QUANT) {
+    } else if (QUANT && warp >= 12) {
         // ---- 8-bit caches: codes to fp16, a piece of 16 codes of a row at a time
         const int me = tid - 12 * 32;
         int ring = 0, tile = 0;
@@ -642,17 +589,70 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
         const int l = warp >> 2, row = tid & 127;
         const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t t_s = tmem + lane_off + kTmemS + l * 128, t_o = tmem + lane_off + kTmemO + l * 128;
-        int done = 0, ring = 0, joins = 0, tile = 0, units = 0, staged = 0;  // tiles of this lane; ring position; ..
+        int done = 0, ring = 0, joins = 0, tile = 0;  // tiles of this lane; ring position; units joined; tile
         bool ok = true;
         Unit u, nu;
         bool have = next_unit(nu);
+        const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;  // the columns take |scale|
+        // Staging the lane's queries of unit x: pieces of 16 bytes, a row by 16 threads, copied
+        // asynchronously by `stage` and made ready by `staged`.
+        constexpr int kRowsAtOnce = (G::kShared ? 256 : 128) / 16;
+        const int me = G::kShared ? tid : row, piece = me & 15;
+        unsigned char *qbuf = smem + (G::kShared ? 0 : l) * kTileBytes;
+        const int lane_col = member * a.cols + (SPLIT ? 0 : l * kLaneCols);  // the lane's first column
+        auto stage = [&](const Unit &x) {
+#pragma unroll 4
+            for (int r = me >> 4; r < kLaneCols; r += kRowsAtOnce) {
+                const int cc = lane_col + r;
+                const int tok = a.g_shift >= 0 ? cc >> a.g_shift : cc / a.G, head = cc - tok * a.G;
+                const bool real = cc < x.ncols;
+                const int64_t at = ((int64_t)(x.r0 + tok) * a.Hq + x.kvh * a.G + head) * kD + piece * 8;
+                tiled::cp_async16(tc_smem(qbuf + tile_chunk(r, piece)), real ? a.q + at : a.q, real ? 16 : 0);
+            }
+        };
+        auto staged = [&] {
+            tiled::cp_async_wait_all();
+            if (QUANT || flip) {
+                // 8-bit caches: as fp16 scaled by 2^sig per row, sig putting the row's largest |q|
+                // in [2^13, 2^14).  Each thread rewrites what it copied itself.
+#pragma unroll 2
+                for (int r = me >> 4; r < kLaneCols; r += kRowsAtOnce) {
+                    uint4 *at = reinterpret_cast<uint4 *>(qbuf + tile_chunk(r, piece));
+                    const uint4 x = *at;
+                    uint32_t q[4] = {x.x ^ flip, x.y ^ flip, x.z ^ flip, x.w ^ flip};
+                    if constexpr (QUANT) {
+                        float f[8], amax = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            f[2 * e] = __uint_as_float(q[e] << 16);
+                            f[2 * e + 1] = __uint_as_float(q[e] & 0xffff0000u);
+                            amax = fmaxf(amax, fmaxf(fabsf(f[2 * e]), fabsf(f[2 * e + 1])));
+                        }
+#pragma unroll
+                        for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                        const int sig = amax > 0.f ? min(100, max(-100, 14 - tiled::exponent_above(amax))) : 0;
+                        const float up = __uint_as_float((uint32_t)(127 + sig) << 23);  // 2^sig
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) q[e] = tiled::f16x2(f[2 * e] * up, f[2 * e + 1] * up);
+                        if (piece == 0) sh.rs[G::kShared ? 0 : l][r] = fabsf(a.scale_log2) * __uint_as_float((uint32_t)(127 - sig) << 23);
+                    }
+                    *at = make_uint4(q[0], q[1], q[2], q[3]);
+                }
+            }
+            fence_async();
+            mbar_arrive(tc_smem(&sh.qfull[G::kShared ? 0 : l]));
+        };
+        // whether this lane stages queries for unit x
+        auto stages = [&](const Unit &x) { return G::kShared || l == 0 || second(x); };
+        bool pending = have && stages(nu);
+        if (pending) stage(nu);
+        uint32_t units = 0;  // units whose queries this lane staged
         while (ok && have) {
             u = nu;
             const bool two = second(u);
             const bool active = l == 0 || two;
-            const int qb = SPLIT ? units % G::kQueries : l;
-            const uint32_t qphase = SPLIT ? units / G::kQueries : staged;
-            ++units;
+            if (pending) staged();
+            pending = false;
             have = next_unit(nu);
             if (!SPLIT && !active) {
                 if constexpr (QUANT) {  // the other lane reads these tiles' scales alone
@@ -665,26 +665,36 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                 }
                 ring += 2 * u.n;
                 tile += u.n;
+                if (ok && have && stages(nu)) {
+                    stage(nu);
+                    pending = true;
+                }
                 continue;
             }
-            ++staged;
-            const int c = member * a.cols + (SPLIT ? 0 : l * kLaneCols) + row;
+            const int c = lane_col + row;
             const bool col = c < u.ncols;
             float m = -INFINITY, sum_l = 0.f, rs = fabsf(a.scale_log2);
             if constexpr (QUANT) {
-                ok = wait_for(&sh.qfull[qb], qphase & 1, abort);
+                ok = wait_for(&sh.qfull[G::kShared ? 0 : l], units & 1, abort);  // the factors of all the lane's rows
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                rs = sh.rs[qb][row];
-                mbar_arrive(tc_smem(&sh.qfree[qb]));
+                rs = sh.rs[G::kShared ? 0 : l][row];
             }
+            ++units;
+            // the lane's last tile
+            const int t_last = SPLIT ? u.n - 1 - ((u.n - 1 - l) & 1) : u.n - 1;
             // a warp none of whose columns is real keeps step without computing
-            const bool idle = member * a.cols + (SPLIT ? 0 : l * kLaneCols) + (warp & 3) * 32 >= u.ncols;
+            const bool idle = lane_col + (warp & 3) * 32 >= u.ncols;
             for (int t = SPLIT ? l : 0; t < u.n; t += SPLIT ? 2 : 1) {
                 const int j = tile + t;
                 ok = wait_for(&sh.sfull[l], done & 1, abort);
                 if (QUANT && ok) ok = wait_for(&sh.scales[j % (2 * kScaleSlots)], j / (2 * kScaleSlots) & 1, abort);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 tc_fence_after();
+                if (!G::kShared && t == t_last && have && stages(nu)) {
+                    // the lane's products with this unit's queries are done
+                    stage(nu);
+                    pending = true;
+                }
                 const int k0 = (u.t0 + t) * kTile;
                 if (!idle) {
                     float sv[kTile];
@@ -744,18 +754,18 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                     const float base = m == -INFINITY ? 0.f : m;
                     float ls[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        float pw[32];
+                    for (int q = 0; q < 4; ++q) {
+                        float pw[16];
 #pragma unroll
-                        for (int i = 0; i < 32; i += 2) {
+                        for (int i = 0; i < 16; i += 2) {
                             float p[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                p[e] = tc_exp2(fmaf(sv[64 * q + 2 * i + e], rs, -base));
+                                p[e] = tc_exp2(fmaf(sv[32 * q + 2 * i + e], rs, -base));
                                 ls[e] += p[e];
                             }
                             if constexpr (QUANT) {
-                                const float4 x = reinterpret_cast<const float4 *>(sh.vs[j % kScaleSlots])[16 * q + i / 2];
+                                const float4 x = reinterpret_cast<const float4 *>(sh.vs[j % kScaleSlots])[8 * q + i / 2];
                                 pw[i] = __uint_as_float(tiled::f16x2(p[0] * x.x, p[1] * x.y));
                                 pw[i + 1] = __uint_as_float(tiled::f16x2(p[2] * x.z, p[3] * x.w));
                             } else {
@@ -763,7 +773,7 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                                 pw[i + 1] = __uint_as_float(tc_bf16x2(p[2], p[3]));
                             }
                         }
-                        tmem_st32(t_s + 32 * q, pw);
+                        tmem_st16(t_s + 16 * q, pw);
                     }
                     sum_l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
                     tmem_wait_st();
@@ -850,6 +860,10 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                 ok = wait_for(&sh.oread, joins & 1, abort);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 ++joins;
+                if (!pending && have && stages(nu)) {  // one buffer for both lanes, or no tile in this unit
+                    stage(nu);
+                    pending = true;
+                }
             }
             __syncwarp();
             tc_fence_before();
