@@ -17,14 +17,18 @@
 //     write of its partials;
 //   * warp 8 copies K and V tiles (TMA); one thread each of warps 9 and 10 issues a lane's
 //     products (warp 11 fills the warpgroup, whose spare registers go to the columns);
-//   * 8-bit caches: warp 8 copies codes into a ring of 16 KB stages, and warps 12-15 turn
-//     them into exact fp16 in the stages the products read.
+//   * 8-bit caches: warp 8 copies codes and scales into a ring of 16 KB stages, and warps
+//     12-15 turn them into fp16 in the stages the products read.
 // Tensor memory: S of the lanes at columns 0 and 128 (overwritten by P as 16-bit pairs, the A
 // operand of P V), O at 256 and 384.
-// 8-bit caches: a score is (q . code) x key scale, the query rows being fp16 scaled by a power
-// of two each; the weight fed to the product is p x value scale in fp16, so the base m is
-// kept above the scores plus the exponent of the tile's largest value scale: no weight
-// leaves fp16's range whatever the scales.
+// 8-bit caches: an entry is code x scale in fp16, in units of a power of two per tile (2^e,
+// the tile's largest scale below it), the scale rounded to fp16 and the product once more
+// (together within 2^-11; an entry 2^-24 below the tile's largest is lost); the query rows
+// are fp16 scaled by a power of two each (exact).  The columns take both powers into their
+// score factor, and keep the base m above the scores plus the values' e: a weight p 2^e
+// stays below 2^8 whatever the scales.  Scales in fp32 per element instead, on the scores and
+// on the weights, were slower: 261 us for the fp8 batch of 64 sequences of 128 to 4096
+// tokens and 9 to 16 rows, bound by the columns' reads of the scales.
 // Bounds: up to 128 columns, or 256 shared ones, the 64 KB of a bf16 K and V tile take 2800 SM
 // clocks at the measured HBM rate and the products 1024 / 2048, so HBM bounds; more columns
 // reread the tiles through L2 and the products bound.
@@ -84,12 +88,12 @@ struct Geo {
 template <typename G>
 struct Shared {
     float2 ml[2][kLaneCols];                    // lanes joined: each one's (base, sum) per column
-    float ks[G::kQuant ? kScaleSlots : 1][G::kQuant ? kTile : 1];  // tiles' scales, 0 behind the context
-    float vs[G::kQuant ? kScaleSlots : 1][G::kQuant ? kTile : 1];
+    float raw_scale[G::kQuant ? G::kRaw : 1][G::kQuant ? kTile : 4];  // scales of the codes' stages
+    float2 unit[kScaleSlots];                   // tiles' powers of two, as exponents: K's and V's
     float rs[2][G::kQuant ? kLaneCols : 1];     // columns' score factors, by query buffer
     uint64_t full[G::kFull], free[G::kStages];  // ring positions landed / stages consumed
     uint64_t raw_full[G::kQuant ? G::kRaw : 1], raw_free[G::kQuant ? G::kRaw : 1];
-    uint64_t scales[2 * kScaleSlots], scales_free[kScaleSlots];
+    uint64_t units[2 * kScaleSlots], units_free[kScaleSlots];  // of the powers: both in / read
     uint64_t sfull[2], pfull[2], odone[2];      // per lane: S written, P written, P V done
     uint64_t qfull[2];                          // query buffers staged
     uint64_t mlready, oread;                    // lanes joined: both (base, sum) and O in / read
@@ -207,17 +211,23 @@ struct Walk {
     }
 };
 
-// Sixteen codes of one row as sixteen exact fp16 (two 16-byte words).
+// Sixteen codes of one row times a scale, as sixteen fp16 (two 16-byte words).
 template <typename KV>
-__device__ __forceinline__ void exact_f16(const uint4 &c, uint4 &lo, uint4 &hi) {
-    tiled::codes_to_f16_exact<KV>(c, lo, hi);
+__device__ __forceinline__ void scaled_f16(const uint4 &c, __half2 scale, uint4 &lo, uint4 &hi) {
+    if constexpr (sizeof(KV) == 1) {
+        tiled::codes_to_f16_exact<KV>(c, lo, hi);
+        uint32_t *w[8] = {&lo.x, &lo.y, &lo.z, &lo.w, &hi.x, &hi.y, &hi.z, &hi.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const __half2 x = __hmul2(*reinterpret_cast<const __half2 *>(w[i]), scale);
+            *w[i] = *reinterpret_cast<const uint32_t *>(&x);
+        }
+    }
 }
-template <>
-__device__ __forceinline__ void exact_f16<uint16_t>(const uint4 &, uint4 &, uint4 &) {}
 
-// Exponent e with |x| < 2^e, from -60 up.
-__device__ __forceinline__ float exponent_over(uint32_t bits) {
-    return (float)max((int)((bits >> 23) & 0xffu) - 126, -60);
+// Exponent e with |x| < 2^e for the bits of a positive x, kept in -100 .. 100.
+__device__ __forceinline__ int exponent_over(uint32_t bits) {
+    return min(max((int)((bits >> 23) & 0xffu) - 126, -100), 100);
 }
 
 template <typename KV, int BS, bool SPLIT>
@@ -243,8 +253,8 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
             mbar_init(tc_smem(&sh.raw_full[i]));
             mbar_init_n(tc_smem(&sh.raw_free[i]), 128);
         }
-        if (QUANT && lane < 2 * kScaleSlots) mbar_init_n(tc_smem(&sh.scales[lane]), 2 * 128);
-        if (QUANT && lane < kScaleSlots) mbar_init_n(tc_smem(&sh.scales_free[lane]), SPLIT ? kLaneCols : 2 * kLaneCols);
+        if (QUANT && lane < 2 * kScaleSlots) mbar_init_n(tc_smem(&sh.units[lane]), 2);
+        if (QUANT && lane < kScaleSlots) mbar_init_n(tc_smem(&sh.units_free[lane]), SPLIT ? kLaneCols : 2 * kLaneCols);
         if (lane < 2) {
             mbar_init(tc_smem(&sh.sfull[lane]));
             mbar_init(tc_smem(&sh.odone[lane]));
@@ -344,18 +354,14 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
         constexpr int kSlots = QUANT ? G::kRaw : kStages;
         const int oob = QUANT ? a.N * a.Hkv * BS : a.N * a.Hkv * kGroups;  // past the pool: the copy fills zeros
         const uint32_t box = tc_smem(smem + (QUANT ? G::kOffRaw : G::kOffRing)) + lane * BS * (QUANT ? kD : 2 * kD);
-        int st = 0, issued = 0, tile = 0;  // stage, ring position, tile of the share
+        int st = 0, issued = 0;            // stage, ring position
         uint32_t phase = 0;                // of the stage's next wait for its release
         bool ok = true, first = true;
         Unit u{}, nu;
         bool have = next_unit(nu);
         // K (map, y) or V of this lane's block; 8-bit: the block's scales too, none where b < 0
-        auto fill = [&](bool is_k, int y, int b, int j) {
+        auto fill = [&](bool is_k, int y, int b) {
             if (issued >= kSlots) ok = wait_for(QUANT ? &sh.raw_free[st] : &sh.free[st], phase ^ 1, abort);
-            if constexpr (QUANT) {
-                // the tile's scale slot: read by the lanes four tiles ago
-                if (ok && is_k && j >= kScaleSlots) ok = wait_for(&sh.scales_free[j % kScaleSlots], (j / kScaleSlots - 1) & 1, abort);
-            }
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) return;
             const CUtensorMap *map = is_k ? &kmap : &vmap;
@@ -363,7 +369,7 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                 const uint32_t bar = tc_smem(&sh.raw_full[st]);
                 const bool scaled = lane < kBlocks && b >= 0;
                 const int blocks = __popc(__ballot_sync(0xffffffffu, scaled));
-                float *slot = (is_k ? sh.ks : sh.vs)[j % kScaleSlots] + (lane < kBlocks ? lane : 0) * BS;
+                float *slot = sh.raw_scale[st] + (lane < kBlocks ? lane : 0) * BS;
                 if (lane < kBlocks && b < 0)
 #pragma unroll
                     for (int i = 0; i < BS; i += 4) *reinterpret_cast<float4 *>(slot + i) = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -406,7 +412,7 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
             // go before all copies but one.
             for (int i = lane * 32; i < u.n * kBlocks; i += 32 * 32) prefetch_l2(table + min(u.t0 * kBlocks + i, nblk - 1));
             int b = checked(0, entry(0)), e1 = entry(1), e2 = entry(2);
-            fill(true, row_of(b), b, tile);
+            fill(true, row_of(b), b);
             if (first) {
                 first = false;  // (their barrier's next phase needs this unit's other tiles)
                 if (ok) ok = wait_for(&sh.qfull[0], 0, abort);
@@ -417,12 +423,11 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                 const int bn = checked(t + 1, e1);
                 e1 = e2;
                 e2 = entry(t + 3);
-                if (SPLIT && t + 1 < u.n) fill(true, row_of(bn), bn, tile + t + 1);
-                if (ok) fill(false, row_of(b), b, tile + t);
-                if (!SPLIT && ok && t + 1 < u.n) fill(true, row_of(bn), bn, tile + t + 1);
+                if (SPLIT && t + 1 < u.n) fill(true, row_of(bn), bn);
+                if (ok) fill(false, row_of(b), b);
+                if (!SPLIT && ok && t + 1 < u.n) fill(true, row_of(bn), bn);
                 b = bn;
             }
-            tile += u.n;
         }
         if (!ok) {
             // stopping early: copies already issued may still be landing in shared memory
@@ -562,19 +567,35 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                 if (ok && ring >= kStages) ok = wait_for(&sh.free[st], (ring / kStages - 1) & 1, abort);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 const int left = u.ctx - (u.t0 + t) * kTile;  // tokens of the context from the tile on
-                // tokens behind the context: scales may hold anything
-                if (me >= left) (is_k ? sh.ks : sh.vs)[j % kScaleSlots][me] = 0.f;
-                mbar_arrive(tc_smem(&sh.scales[j % (2 * kScaleSlots)]));
-                const unsigned char *raw = smem + G::kOffRaw + rst * kRawBytes;
+                // the tile's power of two (scales behind the context may hold anything)
+                const float *scale = sh.raw_scale[rst];
+                const float4 s4 = reinterpret_cast<const float4 *>(scale)[lane];
+                const float top = fmaxf(fmaxf(4 * lane < left ? s4.x : 0.f, 4 * lane + 1 < left ? s4.y : 0.f),
+                                        fmaxf(4 * lane + 2 < left ? s4.z : 0.f, 4 * lane + 3 < left ? s4.w : 0.f));
+                const int e = exponent_over(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+                const float down = __uint_as_float((uint32_t)(127 - e) << 23);  // 2^-e
+                if (me == 0) {
+                    // the lanes have read this slot's last tile
+                    if (j >= kScaleSlots) ok = wait_for(&sh.units_free[j % kScaleSlots], (j / kScaleSlots - 1) & 1, abort);
+                    (is_k ? sh.unit[j % kScaleSlots].x : sh.unit[j % kScaleSlots].y) = (float)e;
+                    mbar_arrive(tc_smem(&sh.units[j % (2 * kScaleSlots)]));
+                }
+                // this thread's piece c of rows r0, r0 + 16, ..: two 8-value chunks each, the odd
+                // half of the row stored in the other order (no bank conflicts)
+                const int r0 = me >> 3, c = me & 7, sw = c >> 2;
+                const unsigned char *from = smem + G::kOffRaw + rst * kRawBytes + r0 * kD + c * 16;
                 unsigned char *to = smem + G::kOffRing + st * kTileBytes;
-                const int c = me & 7, sw = c >> 2;  // piece of the row; which half is stored first (no bank conflicts)
+                unsigned char *to0 = to + tile_chunk(r0, 2 * c + sw), *to1 = to + tile_chunk(r0, 2 * c + 1 - sw);
+                uint4 code[kTile / 16];
 #pragma unroll
-                for (int r = me >> 3; r < kTile; r += 16) {
-                    uint4 h[2];
-                    exact_f16<KV>(*reinterpret_cast<const uint4 *>(raw + r * kD + c * 16), h[0], h[1]);
-                    if (r >= left) h[0] = h[1] = make_uint4(0u, 0u, 0u, 0u);  // a code may be a NaN
-                    *reinterpret_cast<uint4 *>(to + tile_chunk(r, 2 * c + sw)) = sw ? h[1] : h[0];
-                    *reinterpret_cast<uint4 *>(to + tile_chunk(r, 2 * c + 1 - sw)) = sw ? h[0] : h[1];
+                for (int k = 0; k < kTile / 16; ++k) code[k] = *reinterpret_cast<const uint4 *>(from + k * 16 * kD);
+#pragma unroll
+                for (int k = 0; k < kTile / 16; ++k) {
+                    uint4 lo, hi;
+                    scaled_f16<KV>(code[k], __float2half2_rn(scale[r0 + 16 * k] * down), lo, hi);
+                    if (r0 + 16 * k >= left) lo = hi = make_uint4(0u, 0u, 0u, 0u);  // codes and scales of no token
+                    *reinterpret_cast<uint4 *>(to0 + k * 2 * kGroup) = sw ? hi : lo;
+                    *reinterpret_cast<uint4 *>(to1 + k * 2 * kGroup) = sw ? lo : hi;
                 }
                 fence_async();
                 mbar_arrive(tc_smem(&sh.full[ring % kFull]));
@@ -655,12 +676,12 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
             pending = false;
             have = next_unit(nu);
             if (!SPLIT && !active) {
-                if constexpr (QUANT) {  // the other lane reads these tiles' scales alone
+                if constexpr (QUANT) {  // the other lane reads these tiles' powers alone
                     for (int t = 0; ok && t < u.n; ++t) {
                         const int j = tile + t;
-                        ok = wait_for(&sh.scales[j % (2 * kScaleSlots)], j / (2 * kScaleSlots) & 1, abort);
+                        ok = wait_for(&sh.units[j % (2 * kScaleSlots)], j / (2 * kScaleSlots) & 1, abort);
                         if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                        mbar_arrive(tc_smem(&sh.scales_free[j % kScaleSlots]));
+                        mbar_arrive(tc_smem(&sh.units_free[j % kScaleSlots]));
                     }
                 }
                 ring += 2 * u.n;
@@ -687,7 +708,7 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
             for (int t = SPLIT ? l : 0; t < u.n; t += SPLIT ? 2 : 1) {
                 const int j = tile + t;
                 ok = wait_for(&sh.sfull[l], done & 1, abort);
-                if (QUANT && ok) ok = wait_for(&sh.scales[j % (2 * kScaleSlots)], j / (2 * kScaleSlots) & 1, abort);
+                if (QUANT && ok) ok = wait_for(&sh.units[j % (2 * kScaleSlots)], j / (2 * kScaleSlots) & 1, abort);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 tc_fence_after();
                 if (!G::kShared && t == t_last && have && stages(nu)) {
@@ -701,20 +722,11 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
 #pragma unroll
                     for (int q = 0; q < 4; ++q) tmem_ld32(t_s + 32 * q, sv + 32 * q);
                     tmem_wait_ld();
-                    float over = 0.f;  // 8-bit: exponent of the tile's largest value scale
+                    float factor = rs, over = 0.f;  // of the scores; exponent of the values' unit
                     if constexpr (QUANT) {
-                        const float4 *ks = reinterpret_cast<const float4 *>(sh.ks[j % kScaleSlots]);
-#pragma unroll
-                        for (int k = 0; k < kTile / 4; ++k) {
-                            const float4 x = ks[k];
-                            sv[4 * k] *= x.x;
-                            sv[4 * k + 1] *= x.y;
-                            sv[4 * k + 2] *= x.z;
-                            sv[4 * k + 3] *= x.w;
-                        }
-                        const float4 x = reinterpret_cast<const float4 *>(sh.vs[j % kScaleSlots])[lane];
-                        const uint32_t top = __float_as_uint(fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))));
-                        over = exponent_over(__reduce_max_sync(0xffffffffu, top));
+                        const float2 unit = sh.unit[j % kScaleSlots];
+                        factor = rs * __uint_as_float((uint32_t)(127 + (int)unit.x) << 23);
+                        over = unit.y;
                     }
                     if (k0 + kTile > u.ctx) {
 #pragma unroll
@@ -728,7 +740,7 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                     for (int k = 8; k < kTile; ++k) mx[k & 7] = fmaxf(mx[k & 7], sv[k]);
                     const float top = fmaf(fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
                                                  fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))),
-                                           rs, over);
+                                           factor, over);
                     // the running base is raised only by more than 2^8; then l and O shrink
                     float f = 1.f;
                     bool shrink = false;
@@ -751,7 +763,7 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                             tmem_st32(t_o + 32 * q, ov);
                         }
                     }
-                    const float base = m == -INFINITY ? 0.f : m;
+                    const float base = (m == -INFINITY ? 0.f : m) - over;  // weights come in units of 2^-over
                     float ls[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
@@ -761,13 +773,12 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                             float p[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                p[e] = tc_exp2(fmaf(sv[32 * q + 2 * i + e], rs, -base));
+                                p[e] = tc_exp2(fmaf(sv[32 * q + 2 * i + e], factor, -base));
                                 ls[e] += p[e];
                             }
                             if constexpr (QUANT) {
-                                const float4 x = reinterpret_cast<const float4 *>(sh.vs[j % kScaleSlots])[8 * q + i / 2];
-                                pw[i] = __uint_as_float(tiled::f16x2(p[0] * x.x, p[1] * x.y));
-                                pw[i + 1] = __uint_as_float(tiled::f16x2(p[2] * x.z, p[3] * x.w));
+                                pw[i] = __uint_as_float(tiled::f16x2(p[0], p[1]));
+                                pw[i + 1] = __uint_as_float(tiled::f16x2(p[2], p[3]));
                             } else {
                                 pw[i] = __uint_as_float(tc_bf16x2(p[0], p[1]));
                                 pw[i + 1] = __uint_as_float(tc_bf16x2(p[2], p[3]));
@@ -775,11 +786,12 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                         }
                         tmem_st16(t_s + 16 * q, pw);
                     }
-                    sum_l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+                    const float sum = (ls[0] + ls[1]) + (ls[2] + ls[3]);
+                    sum_l += QUANT ? sum * tc_exp2(-over) : sum;
                     tmem_wait_st();
                 }
                 if constexpr (QUANT) {
-                    mbar_arrive(tc_smem(&sh.scales_free[j % kScaleSlots]));
+                    mbar_arrive(tc_smem(&sh.units_free[j % kScaleSlots]));
                 } else if (k0 + kTile > u.ctx && u.ctx % BS != 0) {
                     // rows past the context inside its last block may hold anything, and a zero
                     // weight times a NaN is a NaN: zero them in the V stage
