@@ -17,8 +17,8 @@
 //     write of its partials;
 //   * warp 8 copies K and V tiles (TMA); one thread each of warps 9 and 10 issues a lane's
 //     products (warp 11 fills the warpgroup, whose spare registers go to the columns);
-//   * 8-bit caches: warp 8 copies codes and scales into a ring of 16 KB stages, and warps
-//     12-15 turn them into fp16 in the stages the products read.
+//   * 8-bit caches: warp 8 copies codes and scales into a ring of 16 KB stages; warps 12-15
+//     turn those of K, warps 16-19 those of V into fp16 in the stages the products read.
 // Tensor memory: S of the lanes at columns 0 and 128 (overwritten by P as 16-bit pairs, the A
 // operand of P V), O at 256 and 384.
 // 8-bit caches: an entry is code x scale in fp16, in units of a power of two per tile (2^e,
@@ -62,16 +62,17 @@ constexpr float kRescaleLog2 = 8.0f;
 constexpr int kScaleSlots = 4;
 
 // Shared memory and threads of a kernel.  Ring position p lands in stage p % kStages and
-// completes barrier p % kFull.  With alternating lanes a lane sees only its own positions,
-// up to three apart, and copies land in any order, so a stage's own barrier could still be
-// at the other lane's copy of the stage's previous position when p is asked for, and that
-// phase has the parity of the one p waits for.  With two barriers a stage the predecessor
-// on a barrier is two uses of the stage back, and a copy after that is only issued once it
-// was consumed.
+// completes barriers p % kFull, of its landing and of its consumption.  With alternating
+// lanes a lane sees only its own positions, up to three apart, and copies land in any
+// order, so a stage's own barrier could still be at the other lane's copy of the stage's
+// previous position when p is asked for, and that phase has the parity of the one p waits
+// for.  With two barriers a stage the predecessor on a barrier is two uses of the stage
+// back, and a copy after that is only issued once it was consumed.  (The two groups that
+// convert codes see every other position as well.)
 template <typename KV, bool SPLIT>
 struct Geo {
     static constexpr bool kQuant = sizeof(KV) == 1;
-    static constexpr int kStages = kQuant ? 3 : 5, kFull = 2 * kStages;
+    static constexpr int kStages = kQuant ? 3 : 5, kFull = 2 * kStages;  // stages, barriers
     // query buffers: one per lane, or one for both lanes where they have the same columns and
     // codes need the room
     static constexpr int kQueries = kQuant && SPLIT ? 1 : 2;
@@ -79,10 +80,11 @@ struct Geo {
     static constexpr int kRaw = !kQuant ? 0 : SPLIT ? 5 : 3;  // stages of codes
     static constexpr int kOffRing = kQueries * kTileBytes, kOffRaw = kOffRing + kStages * kTileBytes;
     static constexpr int kOffShared = kOffRaw + kRaw * kRawBytes;
-    static constexpr int kThreads = kQuant ? 512 : 384;
+    static constexpr int kRawFull = 2 * kRaw;                 // their barriers, as for the ring
+    static constexpr int kThreads = kQuant ? 640 : 384;
     // registers a thread: the columns' warps take what the others leave of the launch's
-    // 168 (three warpgroups) or 128 (four)
-    static constexpr int kRegsColumns = kQuant ? 184 : 200, kRegsOther = kQuant ? 72 : 104;
+    // 3 x 168 or 5 x 96
+    static constexpr int kRegsColumns = kQuant ? 128 : 200, kRegsOther = kQuant ? 72 : 104;
 };
 
 template <typename G>
@@ -91,8 +93,8 @@ struct Shared {
     float raw_scale[G::kQuant ? G::kRaw : 1][G::kQuant ? kTile : 4];  // scales of the codes' stages
     float2 unit[kScaleSlots];                   // tiles' powers of two, as exponents: K's and V's
     float rs[2][G::kQuant ? kLaneCols : 1];     // columns' score factors, by query buffer
-    uint64_t full[G::kFull], free[G::kStages];  // ring positions landed / stages consumed
-    uint64_t raw_full[G::kQuant ? G::kRaw : 1], raw_free[G::kQuant ? G::kRaw : 1];
+    uint64_t full[G::kFull], free[G::kFull];    // ring positions landed / consumed
+    uint64_t raw_full[G::kQuant ? G::kRawFull : 1], raw_free[G::kQuant ? G::kRaw : 1];
     uint64_t units[2 * kScaleSlots], units_free[kScaleSlots];  // of the powers: both in / read
     uint64_t sfull[2], pfull[2], odone[2];      // per lane: S written, P written, P V done
     uint64_t qfull[2];                          // query buffers staged
@@ -101,7 +103,7 @@ struct Shared {
     uint64_t drain[2];
     int64_t total, first_tile;                  // of all positions; of the first sequence
     int first_seq;
-    int wsum[16];
+    int wsum[20];
     uint32_t taddr;
     int abort;
 };
@@ -248,11 +250,9 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
     const int group = blockIdx.x / a.members, member = blockIdx.x % a.members;
     if (warp == 1) {
         for (int i = lane; i < kFull; i += 32) mbar_init_n(tc_smem(&sh.full[i]), QUANT ? 128 : 1);
-        for (int i = lane; i < kStages; i += 32) mbar_init_n(tc_smem(&sh.free[i]), SPLIT ? 1 : 2);  // lanes that read a stage
-        for (int i = lane; i < G::kRaw; i += 32) {
-            mbar_init(tc_smem(&sh.raw_full[i]));
-            mbar_init_n(tc_smem(&sh.raw_free[i]), 128);
-        }
+        for (int i = lane; i < kFull; i += 32) mbar_init_n(tc_smem(&sh.free[i]), SPLIT ? 1 : 2);  // lanes that read a stage
+        for (int i = lane; i < G::kRawFull; i += 32) mbar_init(tc_smem(&sh.raw_full[i]));
+        for (int i = lane; i < G::kRaw; i += 32) mbar_init_n(tc_smem(&sh.raw_free[i]), 128);
         if (QUANT && lane < 2 * kScaleSlots) mbar_init_n(tc_smem(&sh.units[lane]), 2);
         if (QUANT && lane < kScaleSlots) mbar_init_n(tc_smem(&sh.units_free[lane]), SPLIT ? kLaneCols : 2 * kLaneCols);
         if (lane < 2) {
@@ -355,18 +355,20 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
         const int oob = QUANT ? a.N * a.Hkv * BS : a.N * a.Hkv * kGroups;  // past the pool: the copy fills zeros
         const uint32_t box = tc_smem(smem + (QUANT ? G::kOffRaw : G::kOffRing)) + lane * BS * (QUANT ? kD : 2 * kD);
         int st = 0, issued = 0;            // stage, ring position
-        uint32_t phase = 0;                // of the stage's next wait for its release
         bool ok = true, first = true;
         Unit u{}, nu;
         bool have = next_unit(nu);
         // K (map, y) or V of this lane's block; 8-bit: the block's scales too, none where b < 0
         auto fill = [&](bool is_k, int y, int b) {
-            if (issued >= kSlots) ok = wait_for(QUANT ? &sh.raw_free[st] : &sh.free[st], phase ^ 1, abort);
+            const int last = issued - kSlots;  // the stage's last position
+            if (last >= 0)
+                ok = QUANT ? wait_for(&sh.raw_free[st], (last / kSlots) & 1, abort)
+                           : wait_for(&sh.free[last % kFull], (last / kFull) & 1, abort);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) return;
             const CUtensorMap *map = is_k ? &kmap : &vmap;
             if constexpr (QUANT) {
-                const uint32_t bar = tc_smem(&sh.raw_full[st]);
+                const uint32_t bar = tc_smem(&sh.raw_full[issued % (QUANT ? G::kRawFull : 1)]);
                 const bool scaled = lane < kBlocks && b >= 0;
                 const int blocks = __popc(__ballot_sync(0xffffffffu, scaled));
                 float *slot = sh.raw_scale[st] + (lane < kBlocks ? lane : 0) * BS;
@@ -385,10 +387,7 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                 if (lane < kBlocks) tma_block(box + st * kTileBytes, map, y, bar);
             }
             ++issued;
-            if (++st == kSlots) {
-                st = 0;
-                phase ^= 1;
-            }
+            if (++st == kSlots) st = 0;
         };
         while (ok && have) {
             u = nu;
@@ -433,7 +432,7 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
             // stopping early: copies already issued may still be landing in shared memory
             for (int i = max(0, issued - kSlots); i < issued; ++i) {
                 if constexpr (QUANT)
-                    mbar_wait(tc_smem(&sh.raw_full[i % kSlots]), (i / kSlots) & 1);
+                    mbar_wait(tc_smem(&sh.raw_full[i % G::kRawFull]), (i / G::kRawFull) & 1);
                 else
                     mbar_wait(tc_smem(&sh.full[i % kFull]), (i / kFull) & 1);
             }
@@ -470,7 +469,7 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                     // the other lane reads these tiles alone
                     for (int at = ring; !SPLIT && ok && at < ring + 2 * u.n; ++at) {
                         ok = wait_for(&sh.full[at % kFull], (at / kFull) & 1, abort);
-                        if (ok) mbar_arrive(tc_smem(&sh.free[at % kStages]));
+                        if (ok) mbar_arrive(tc_smem(&sh.free[at % kFull]));
                     }
                     ring += 2 * u.n;
                     have = next_unit(nu);
@@ -512,7 +511,7 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                 if (ok) ok = landed(k_pos);
                 if (ok) {
                     scores(k_pos);
-                    umma_commit(tc_smem(&sh.free[k_pos % kStages]));
+                    umma_commit(tc_smem(&sh.free[k_pos % kFull]));
                 }
                 have = next_unit(nu);
                 for (int t = t_first; ok && t < u.n; t += kStep) {
@@ -532,8 +531,8 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                         mbar_arrive(tc_smem(&sh.turn[l ^ 1]));
                         ++taken;
                     }
-                    umma_commit(tc_smem(&sh.free[v_pos % kStages]));
-                    if (more) umma_commit(tc_smem(&sh.free[k_pos % kStages]));
+                    umma_commit(tc_smem(&sh.free[v_pos % kFull]));
+                    if (more) umma_commit(tc_smem(&sh.free[k_pos % kFull]));
                 }
                 ring += 2 * u.n;
             }
@@ -545,26 +544,19 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
         }
         __syncwarp();
     } else if (QUANT && warp >= 12) {
-        // ---- 8-bit caches: codes to fp16, a piece of 16 codes of a row at a time
-        const int me = tid - 12 * 32;
+        // ---- 8-bit caches: codes of K, or of V, to fp16
+        const bool is_k = warp < 16;
+        const int me = tid & 127;
         int ring = 0, tile = 0;
         bool ok = true;
         Unit u;
         while (ok && next_unit(u)) {
-            // positions in the order of use: tile and kind of position i
-            for (int i = 0; ok && i < 2 * u.n; ++i, ++ring) {
-                bool is_k;
-                int t;
-                if (SPLIT) {
-                    is_k = i == 0 || ((i & 1) && i < 2 * u.n - 1);
-                    t = is_k ? (i + 1) / 2 : i == 2 * u.n - 1 ? u.n - 1 : i / 2 - 1;
-                } else {
-                    is_k = !(i & 1);
-                    t = i / 2;
-                }
-                const int rst = ring % (G::kRaw ? G::kRaw : 1), st = ring % kStages, j = tile + t;
-                ok = wait_for(&sh.raw_full[rst], ring / (G::kRaw ? G::kRaw : 1) & 1, abort);
-                if (ok && ring >= kStages) ok = wait_for(&sh.free[st], (ring / kStages - 1) & 1, abort);
+            for (int t = 0; ok && t < u.n; ++t) {
+                constexpr int kRaw = QUANT ? G::kRaw : 1, kRawFull = QUANT ? G::kRawFull : 1;
+                const int at = ring + (is_k ? k_at(t, u.n) : v_at(t, u.n));
+                const int rst = at % kRaw, st = at % kStages, j = tile + t;
+                ok = wait_for(&sh.raw_full[at % kRawFull], (at / kRawFull) & 1, abort);
+                if (ok && at >= kStages) ok = wait_for(&sh.free[(at - kStages) % kFull], ((at - kStages) / kFull) & 1, abort);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 const int left = u.ctx - (u.t0 + t) * kTile;  // tokens of the context from the tile on
                 // the tile's power of two (scales behind the context may hold anything)
@@ -586,21 +578,24 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                 const unsigned char *from = smem + G::kOffRaw + rst * kRawBytes + r0 * kD + c * 16;
                 unsigned char *to = smem + G::kOffRing + st * kTileBytes;
                 unsigned char *to0 = to + tile_chunk(r0, 2 * c + sw), *to1 = to + tile_chunk(r0, 2 * c + 1 - sw);
-                uint4 code[kTile / 16];
+#pragma unroll 1
+                for (int r = r0; r < kTile; r += 32, from += 32 * kD, to0 += 4 * kGroup, to1 += 4 * kGroup) {
+                    uint4 code[2], lo, hi;
 #pragma unroll
-                for (int k = 0; k < kTile / 16; ++k) code[k] = *reinterpret_cast<const uint4 *>(from + k * 16 * kD);
+                    for (int k = 0; k < 2; ++k) code[k] = *reinterpret_cast<const uint4 *>(from + k * 16 * kD);
 #pragma unroll
-                for (int k = 0; k < kTile / 16; ++k) {
-                    uint4 lo, hi;
-                    scaled_f16<KV>(code[k], __float2half2_rn(scale[r0 + 16 * k] * down), lo, hi);
-                    if (r0 + 16 * k >= left) lo = hi = make_uint4(0u, 0u, 0u, 0u);  // codes and scales of no token
-                    *reinterpret_cast<uint4 *>(to0 + k * 2 * kGroup) = sw ? hi : lo;
-                    *reinterpret_cast<uint4 *>(to1 + k * 2 * kGroup) = sw ? lo : hi;
+                    for (int k = 0; k < 2; ++k) {
+                        scaled_f16<KV>(code[k], __float2half2_rn(scale[r + 16 * k] * down), lo, hi);
+                        if (r + 16 * k >= left) lo = hi = make_uint4(0u, 0u, 0u, 0u);  // codes and scales of no token
+                        *reinterpret_cast<uint4 *>(to0 + k * 2 * kGroup) = sw ? hi : lo;
+                        *reinterpret_cast<uint4 *>(to1 + k * 2 * kGroup) = sw ? lo : hi;
+                    }
                 }
                 fence_async();
-                mbar_arrive(tc_smem(&sh.full[ring % kFull]));
+                mbar_arrive(tc_smem(&sh.full[at % kFull]));
                 mbar_arrive(tc_smem(&sh.raw_free[rst]));
             }
+            ring += 2 * u.n;
             tile += u.n;
         }
     }
@@ -718,26 +713,33 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                 }
                 const int k0 = (u.t0 + t) * kTile;
                 if (!idle) {
-                    float sv[kTile];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) tmem_ld32(t_s + 32 * q, sv + 32 * q);
-                    tmem_wait_ld();
                     float factor = rs, over = 0.f;  // of the scores; exponent of the values' unit
                     if constexpr (QUANT) {
                         const float2 unit = sh.unit[j % kScaleSlots];
                         factor = rs * __uint_as_float((uint32_t)(127 + (int)unit.x) << 23);
                         over = unit.y;
                     }
-                    if (k0 + kTile > u.ctx) {
-#pragma unroll
-                        for (int k = 0; k < kTile; ++k)
-                            if (k0 + k >= u.ctx) sv[k] = -INFINITY;
-                    }
+                    // The scores are read twice, for the maximum and for the weights, 64 and 32 at a
+                    // time, in loops that stay loops: all 128 in registers spilled, and code
+                    // unrolled over the tile starved the roles of instructions.
+                    const int left = u.ctx - k0;  // tokens of the context from the tile on
                     float mx[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) mx[i] = sv[i];
+                    for (int i = 0; i < 8; ++i) mx[i] = -INFINITY;
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        float sv[64];
+                        tmem_ld32(t_s + 64 * h, sv);
+                        tmem_ld32(t_s + 64 * h + 32, sv + 32);
+                        tmem_wait_ld();
+                        if (left < kTile) {
 #pragma unroll
-                    for (int k = 8; k < kTile; ++k) mx[k & 7] = fmaxf(mx[k & 7], sv[k]);
+                            for (int k = 0; k < 64; ++k)
+                                if (64 * h + k >= left) sv[k] = -INFINITY;
+                        }
+#pragma unroll
+                        for (int k = 0; k < 64; ++k) mx[k & 7] = fmaxf(mx[k & 7], sv[k]);
+                    }
                     const float top = fmaf(fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
                                                  fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))),
                                            factor, over);
@@ -765,15 +767,20 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                     }
                     const float base = (m == -INFINITY ? 0.f : m) - over;  // weights come in units of 2^-over
                     float ls[4] = {0.f, 0.f, 0.f, 0.f};
+                    // 32 scores into weights, over the columns of scores already read
+                    auto weigh = [&](float (&x)[32], int q) {
+                        if (left < kTile) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
+                            for (int k = 0; k < 32; ++k)
+                                if (32 * q + k >= left) x[k] = -INFINITY;
+                        }
                         float pw[16];
 #pragma unroll
                         for (int i = 0; i < 16; i += 2) {
                             float p[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                p[e] = tc_exp2(fmaf(sv[32 * q + 2 * i + e], factor, -base));
+                                p[e] = tc_exp2(fmaf(x[2 * i + e], factor, -base));
                                 ls[e] += p[e];
                             }
                             if constexpr (QUANT) {
@@ -785,6 +792,17 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                             }
                         }
                         tmem_st16(t_s + 16 * q, pw);
+                    };
+                    float x0[32], x1[32];
+                    tmem_ld32(t_s, x0);
+#pragma unroll 1
+                    for (int q = 0; q < 4; q += 2) {
+                        tmem_wait_ld();
+                        tmem_ld32(t_s + 32 * (q + 1), x1);
+                        weigh(x0, q);
+                        tmem_wait_ld();
+                        if (q == 0) tmem_ld32(t_s + 64, x0);
+                        weigh(x1, q + 1);
                     }
                     const float sum = (ls[0] + ls[1]) + (ls[2] + ls[3]);
                     sum_l += QUANT ? sum * tc_exp2(-over) : sum;
