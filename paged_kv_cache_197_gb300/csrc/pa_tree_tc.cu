@@ -727,18 +727,17 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
 #pragma unroll
                     for (int i = 0; i < 8; ++i) mx[i] = -INFINITY;
 #pragma unroll 1
-                    for (int h = 0; h < 2; ++h) {
-                        float sv[64];
-                        tmem_ld32(t_s + 64 * h, sv);
-                        tmem_ld32(t_s + 64 * h + 32, sv + 32);
+                    for (int h = 0; h < 4; ++h) {
+                        float sv[32];
+                        tmem_ld32(t_s + 32 * h, sv);
                         tmem_wait_ld();
                         if (left < kTile) {
 #pragma unroll
-                            for (int k = 0; k < 64; ++k)
-                                if (64 * h + k >= left) sv[k] = -INFINITY;
+                            for (int k = 0; k < 32; ++k)
+                                if (32 * h + k >= left) sv[k] = -INFINITY;
                         }
 #pragma unroll
-                        for (int k = 0; k < 64; ++k) mx[k & 7] = fmaxf(mx[k & 7], sv[k]);
+                        for (int k = 0; k < 32; ++k) mx[k & 7] = fmaxf(mx[k & 7], sv[k]);
                     }
                     const float top = fmaf(fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
                                                  fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))),
@@ -793,16 +792,12 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                         }
                         tmem_st16(t_s + 16 * q, pw);
                     };
-                    float x0[32], x1[32];
-                    tmem_ld32(t_s, x0);
 #pragma unroll 1
-                    for (int q = 0; q < 4; q += 2) {
+                    for (int q = 0; q < 4; ++q) {
+                        float x[32];
+                        tmem_ld32(t_s + 32 * q, x);
                         tmem_wait_ld();
-                        tmem_ld32(t_s + 32 * (q + 1), x1);
-                        weigh(x0, q);
-                        tmem_wait_ld();
-                        if (q == 0) tmem_ld32(t_s + 64, x0);
-                        weigh(x1, q + 1);
+                        weigh(x, q);
                     }
                     const float sum = (ls[0] + ls[1]) + (ls[2] + ls[3]);
                     sum_l += QUANT ? sum * tc_exp2(-over) : sum;
