@@ -572,23 +572,36 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                     (is_k ? sh.unit[j % kScaleSlots].x : sh.unit[j % kScaleSlots].y) = (float)e;
                     mbar_arrive(tc_smem(&sh.units[j % (2 * kScaleSlots)]));
                 }
-                // this thread's piece c of rows r0, r0 + 16, ..: two 8-value chunks each, the odd
-                // half of the row stored in the other order (no bank conflicts)
-                const int r0 = me >> 3, c = me & 7, sw = c >> 2;
+                // this thread's piece c of rows r0, r0 + 16, ..: two 8-value chunks each.  Eight
+                // lanes take half of two neighbouring rows, whose swizzles differ in the lowest
+                // bit, so their stores meet no bank twice.
+                const int r0 = (me >> 5) * 4 + ((me >> 2) & 1) + ((me >> 3) & 2), c = (me & 3) + ((me >> 1) & 4);
                 const unsigned char *from = smem + G::kOffRaw + rst * kRawBytes + r0 * kD + c * 16;
                 unsigned char *to = smem + G::kOffRing + st * kTileBytes;
-                unsigned char *to0 = to + tile_chunk(r0, 2 * c + sw), *to1 = to + tile_chunk(r0, 2 * c + 1 - sw);
+                unsigned char *to0 = to + tile_chunk(r0, 2 * c), *to1 = to + tile_chunk(r0, 2 * c + 1);
+                constexpr int kAtOnce = 2;
 #pragma unroll 1
-                for (int r = r0; r < kTile; r += 32, from += 32 * kD, to0 += 4 * kGroup, to1 += 4 * kGroup) {
-                    uint4 code[2], lo, hi;
+                for (int r = r0; r < kTile; r += 16 * kAtOnce, from += 16 * kAtOnce * kD, to0 += 2 * kAtOnce * kGroup, to1 += 2 * kAtOnce * kGroup) {
+                    uint4 code[kAtOnce], lo, hi;
+                    float sc[kAtOnce];
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) code[k] = *reinterpret_cast<const uint4 *>(from + k * 16 * kD);
+                    for (int k = 0; k < kAtOnce; ++k) {
+                        code[k] = *reinterpret_cast<const uint4 *>(from + k * 16 * kD);
+                        sc[k] = scale[r + 16 * k] * down;
+                    }
+                    if (left < kTile) {  // codes and scales of no token
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        scaled_f16<KV>(code[k], __float2half2_rn(scale[r + 16 * k] * down), lo, hi);
-                        if (r + 16 * k >= left) lo = hi = make_uint4(0u, 0u, 0u, 0u);  // codes and scales of no token
-                        *reinterpret_cast<uint4 *>(to0 + k * 2 * kGroup) = sw ? hi : lo;
-                        *reinterpret_cast<uint4 *>(to1 + k * 2 * kGroup) = sw ? lo : hi;
+                        for (int k = 0; k < kAtOnce; ++k)
+                            if (r + 16 * k >= left) {
+                                code[k] = make_uint4(0u, 0u, 0u, 0u);
+                                sc[k] = 0.f;
+                            }
+                    }
+#pragma unroll
+                    for (int k = 0; k < kAtOnce; ++k) {
+                        scaled_f16<KV>(code[k], __float2half2_rn(sc[k]), lo, hi);
+                        *reinterpret_cast<uint4 *>(to0 + k * 2 * kGroup) = lo;
+                        *reinterpret_cast<uint4 *>(to1 + k * 2 * kGroup) = hi;
                     }
                 }
                 fence_async();
