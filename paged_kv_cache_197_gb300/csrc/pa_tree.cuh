@@ -31,7 +31,7 @@ struct TreeContext {
 constexpr int kTreeTile = 128;  // cached tokens per tile
 // Each unit is laid out with a head start of kTreePad positions before its tiles, about what
 // changing over to it costs in tiles, so that shares of many short units are smaller.
-constexpr int kTreePad = 2;
+constexpr int kTreePad = 4;
 __host__ __device__ inline int64_t tree_unit_len(int64_t tiles) { return tiles > 0 ? tiles + kTreePad : 0; }
 
 // Group whose range holds position x of `total`.

@@ -573,10 +573,13 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                     mbar_arrive(tc_smem(&sh.units[j % (2 * kScaleSlots)]));
                 }
                 // this thread's piece c of rows r0, r0 + 16, ..: two 8-value chunks each.  Eight
-                // lanes take half of two neighbouring rows, whose swizzles differ in the lowest
-                // bit, so their stores meet no bank twice.
-                const int r0 = (me >> 5) * 4 + ((me >> 2) & 1) + ((me >> 3) & 2), c = (me & 3) + ((me >> 1) & 4);
-                const unsigned char *from = smem + G::kOffRaw + rst * kRawBytes + r0 * kD + c * 16;
+                // lanes take the same half of rows r and r ^ 5: both tiles are swizzled by the
+                // row's low three bits, codes in pieces (the two rows' halves then lie apart: bit
+                // 2) and values in chunks (every other one: bit 0), so neither the loads nor the
+                // stores meet a bank twice.
+                const int low = ((me >> 5) & 1) + ((me >> 3) & 2);  // rows 0 .. 3 of eight, with 5, 4, 7, 6
+                const int r0 = (me >> 6) * 8 + ((me & 4) ? low ^ 5 : low), c = (me & 3) + ((me >> 1) & 4);
+                const unsigned char *from = smem + G::kOffRaw + rst * kRawBytes + r0 * kD + ((c ^ (r0 & 7)) << 4);
                 unsigned char *to = smem + G::kOffRing + st * kTileBytes;
                 unsigned char *to0 = to + tile_chunk(r0, 2 * c), *to1 = to + tile_chunk(r0, 2 * c + 1);
                 constexpr int kAtOnce = 2;
@@ -926,7 +929,7 @@ bool pool_map(CUtensorMap *map, const void *pool, int rows, int bs, bool codes) 
         const cuuint64_t strides[1] = {(cuuint64_t)kD};
         const cuuint32_t box[2] = {(cuuint32_t)kD, (cuuint32_t)bs};
         return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(pool), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
     }
     const cuuint64_t dims[4] = {64, 8, 2, (cuuint64_t)(rows / 8)};
