@@ -27,7 +27,7 @@ struct TreeArgs {
     const int32_t *parents, *query_start, *context_lens;
     int *err_flag;
     int S, T, Hq, Hkv, G;
-    int chunks;                 // ceil(G / 8): query heads a warp takes at once
+    int chunks;                 // groups of query heads a warp takes at once
     int max_context_len, max_query_len;
     float scale_log2;
     // the context's partials: per partition of part_tokens tokens ...
@@ -37,55 +37,66 @@ struct TreeArgs {
     TreeContext tiles;
 };
 
-constexpr int kHeads = 8;
-constexpr int kJoinWarps = 4;
+constexpr int kJoinWarps = 8;      // rows of a CTA
+constexpr int kStagedRows = 96;    // rows of a sequence kept in shared memory
 
-// The sum over the warp of each of eight values, in every lane: three exchanges that halve
-// the values a lane carries, two that sum, and a broadcast (17 shuffles instead of 40).
-__device__ __forceinline__ void sum8(float (&x)[kHeads], int lane) {
+// The sums over the warp of HEADS values; lane i ends with that of value i % HEADS.  Halving
+// exchanges while there is more than one value to a lane, then plain sums: 6 shuffles for
+// four values instead of 20.
+template <int HEADS>
+__device__ __forceinline__ float sums(float (&x)[HEADS], int lane) {
 #pragma unroll
-    for (int o = 16, n = 4; n >= 1; o >>= 1, n >>= 1) {
-        const bool up = lane & o;
+    for (int o = 1, n = HEADS / 2; n >= 1; o <<= 1, n >>= 1) {
+        const bool odd = lane & o;
 #pragma unroll
         for (int i = 0; i < n; ++i) {
-            const float give = up ? x[i] : x[i + n], keep = up ? x[i + n] : x[i];
+            const float give = odd ? x[2 * i] : x[2 * i + 1], keep = odd ? x[2 * i + 1] : x[2 * i];
             x[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
         }
     }
     float s = x[0];
-    s += __shfl_xor_sync(0xffffffffu, s, 2);
-    s += __shfl_xor_sync(0xffffffffu, s, 1);
-    // the lanes with (bit 16, bit 8, bit 4) = (h / 4, h / 2, h) hold value h
 #pragma unroll
-    for (int h = 0; h < kHeads; ++h)
-        x[h] = __shfl_sync(0xffffffffu, s, ((h >> 2) & 1) * 16 + ((h >> 1) & 1) * 8 + (h & 1) * 4);
+    for (int o = HEADS; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
 }
 
-// One warp per (row, kv head, up to eight of its query heads): the row's ancestors from the
-// row up, in fp32, then the context's partials.  Launched as a programmatic dependent: the
-// tree's own part, which the context's kernel does not touch, runs before the wait.
-template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const __grid_constant__ TreeArgs a) {
+// One warp per (row, kv head, up to HEADS of its query heads); a CTA takes eight rows of a
+// sequence, and a lane D / 32 dims of every head.  The softmax scalars of head h are kept by
+// the lanes i with i % HEADS = h, and spread when a row is added up.  First the row's
+// ancestors, from the row up, in fp32, the sequence's keys and values for the kv head
+// staged in shared memory (longer trees read them from L2); then the context's partials.
+// Launched as a programmatic dependent: the first part, which the context's kernel does not
+// touch, runs before the wait.
+template <int D, int HEADS, bool STAGED>
+__global__ void __launch_bounds__(kJoinWarps * 32, 4) tree_join_kernel(const __grid_constant__ TreeArgs a) {
     constexpr int PER = D / 32;
+    extern __shared__ __align__(16) unsigned char rows[];  // [rows][K D, V D] bf16
     __shared__ int s_parent[PA_TREE_MAX_NODES];
-    const int tid = threadIdx.x, lane = tid & 31, s = blockIdx.y;
-    const int job = blockIdx.x * kJoinWarps + (tid >> 5), jobs = a.Hkv * a.chunks;
-    const int i = job / jobs, kvh = job % jobs / a.chunks, h0 = job % a.chunks * kHeads;
+    const int tid = threadIdx.x, lane = tid & 31, s = blockIdx.z;
+    const int kvh = blockIdx.y / a.chunks, h0 = blockIdx.y % a.chunks * HEADS;
+    const int i = blockIdx.x * kJoinWarps + (tid >> 5);
     const int r0 = a.query_start[s], r1 = a.query_start[s + 1], L = r1 - r0;
-    const bool lead = blockIdx.x == 0 && tid == 0;
     if (!(r0 >= 0 && r1 <= a.T && L >= 0 && L <= a.max_query_len)) return;  // flagged by the context's kernel
+    const int top = min(L, ((int)blockIdx.x + 1) * kJoinWarps);  // ancestors are above their rows
+    if ((int)blockIdx.x * kJoinWarps >= L && blockIdx.x > 0) return;
+    if constexpr (STAGED) {
+        constexpr int CH = D / 8;  // 16-byte pieces of a key or value
+        for (int x = tid; x < top * 2 * CH; x += kJoinWarps * 32) {
+            const int r = x / (2 * CH), c = x % (2 * CH);
+            const uint16_t *src = c < CH ? a.k + (r0 + r) * a.k_stride + kvh * D + c * 8
+                                         : a.v + (r0 + r) * a.v_stride + kvh * D + (c - CH) * 8;
+            tiled::cp_async16(tiled::smem_u32(rows + x * 16), src, 16);
+        }
+        tiled::cp_async_commit();
+    }
     bool bad = false;
     for (int j = tid; j < L; j += kJoinWarps * 32) {
         const int p = a.parents[r0 + j];
         s_parent[j] = p;
         bad |= p < -1 || p >= j;
     }
-    if (__syncthreads_or(bad)) {
-        if (lead && a.err_flag) atomicOr(a.err_flag, PA_FLAG_TREE_PARENT);
-        return;
-    }
-    if (i >= L) return;
-    const int heads = min(kHeads, a.G - h0);
+    const int ctx = min(max(a.context_lens[s], 0), a.max_context_len);
+    const int heads = min(HEADS, a.G - h0);
     const int64_t pair = (int64_t)(r0 + i) * a.Hq + kvh * a.G + h0;  // row of the first head
     auto load = [&](const uint16_t *p, float (&x)[PER]) {
 #pragma unroll
@@ -95,56 +106,63 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const __grid
             x[e + 1] = __uint_as_float(w & 0xffff0000u);
         }
     };
-    float q[kHeads][PER], acc[kHeads][PER], m[kHeads], l[kHeads];
+    float q[HEADS][PER], acc[HEADS][PER], m = -INFINITY, l = 0.f;
 #pragma unroll
-    for (int h = 0; h < kHeads; ++h) {
-        load(a.q + (pair + (h < heads ? h : 0)) * D + lane * PER, q[h]);
-        m[h] = -INFINITY;
-        l[h] = 0.f;
+    for (int h = 0; h < HEADS; ++h) {
+        if (i < L) load(a.q + (pair + (h < heads ? h : 0)) * D + lane * PER, q[h]);
 #pragma unroll
         for (int e = 0; e < PER; ++e) acc[h][e] = 0.f;
     }
-    const uint16_t *kp = a.k + (int64_t)r0 * a.k_stride + kvh * D + lane * PER;
-    const uint16_t *vp = a.v + (int64_t)r0 * a.v_stride + kvh * D + lane * PER;
-    // strictly decreasing: at most L steps; the next ancestor's rows are loaded ahead
-    float k[PER], v[PER];
-    load(kp + i * a.k_stride, k);
-    load(vp + i * a.v_stride, v);
-    for (int at = i; at >= 0;) {
-        const int up = s_parent[at];
-        float kn[PER], vn[PER], x[kHeads];
-        if (up >= 0) {
-            load(kp + up * a.k_stride, kn);
-            load(vp + up * a.v_stride, vn);
+    if constexpr (STAGED) tiled::cp_async_wait<0>();
+    if (__syncthreads_or(bad)) {
+        if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0 && a.err_flag) atomicOr(a.err_flag, PA_FLAG_TREE_PARENT);
+        return;
+    }
+    if (i >= L) return;
+    const int mine = lane % HEADS;  // the head whose scalars this lane keeps
+    // acc = acc f + w x, with head h's f and w from the lane that keeps them
+    auto add = [&](float f, float w, auto row) {
+        if (__any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll
+            for (int h = 0; h < HEADS; ++h) {
+                const float fh = __shfl_sync(0xffffffffu, f, h);
+#pragma unroll
+                for (int e = 0; e < PER; ++e) acc[h][e] *= fh;
+            }
         }
 #pragma unroll
-        for (int h = 0; h < kHeads; ++h) {
+        for (int h = 0; h < HEADS; ++h) {
+            const float wh = __shfl_sync(0xffffffffu, w, h);
+#pragma unroll
+            for (int e = 0; e < PER; ++e) acc[h][e] = fmaf(wh, row(h, e), acc[h][e]);
+        }
+    };
+    for (int at = i; at >= 0; at = s_parent[at]) {  // strictly decreasing: at most L steps
+        float k[PER], v[PER], x[HEADS];
+        if constexpr (STAGED) {
+            const uint16_t *row = reinterpret_cast<const uint16_t *>(rows) + at * 2 * D + lane * PER;
+            load(row, k);
+            load(row + D, v);
+        } else {
+            load(a.k + (r0 + at) * a.k_stride + kvh * D + lane * PER, k);
+            load(a.v + (r0 + at) * a.v_stride + kvh * D + lane * PER, v);
+        }
+#pragma unroll
+        for (int h = 0; h < HEADS; ++h) {
             x[h] = 0.f;
 #pragma unroll
             for (int e = 0; e < PER; ++e) x[h] = fmaf(q[h][e], k[e], x[h]);
         }
-        sum8(x, lane);
-#pragma unroll
-        for (int h = 0; h < kHeads; ++h) {
-            const float y = x[h] * a.scale_log2, mn = fmaxf(m[h], y), base = mn == -INFINITY ? 0.f : mn;
-            const float f = ex2(m[h] - base), w = ex2(y - base);
-            m[h] = mn;
-            l[h] = l[h] * f + w;
-#pragma unroll
-            for (int e = 0; e < PER; ++e) acc[h][e] = fmaf(w, v[e], acc[h][e] * f);
-        }
-#pragma unroll
-        for (int e = 0; e < PER; ++e) {
-            k[e] = kn[e];
-            v[e] = vn[e];
-        }
-        at = up;
+        const float y = sums(x, lane) * a.scale_log2, mn = fmaxf(m, y), base = mn == -INFINITY ? 0.f : mn;
+        const float f = m == mn ? 1.f : ex2(m - base), w = ex2(y - base);
+        m = mn;
+        l = l * f + w;
+        add(f, w, [&](int, int e) { return v[e]; });
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int ctx = min(max(a.context_lens[s], 0), a.max_context_len);
-    // where the partials lie: lane h < 8 keeps head h's first row and the step to its next
+    // where the partials lie: lane h < HEADS keeps head h's first row and the step to its next
     const float *acc_in = a.ws_acc, *ml_in = a.ws_ml;
-    int64_t row = (pair + lane) * a.max_parts, step = 1, later = 0;  // later: row of the second partial
+    int64_t row = (pair + mine) * a.max_parts, step = 1, later = 0;  // later: row of the second partial
     int n;
     if (a.tiles.prefix == nullptr) {
         n = (ctx + a.part_tokens - 1) / a.part_tokens;
@@ -160,11 +178,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const __grid
             if (n == 1) {
                 acc_in = c.whole_acc;
                 ml_in = c.whole_ml;
-                row = pair + lane;
+                row = pair + mine;
             } else {
                 acc_in = c.cut_acc;
                 ml_in = c.cut_ml;
-                const int col = i * a.G + h0 + lane, member = col / c.cols, in = col % c.cols;
+                const int col = i * a.G + h0 + mine, member = col / c.cols, in = col % c.cols;
                 const int64_t cta = g0 * c.members + member;
                 row = (cta * 2 + 1) * c.cols + in;
                 later = (cta + c.members) * 2 * c.cols + in;
@@ -173,11 +191,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const __grid
         }
     }
     for (int p = 0; p < n; ++p) {
-        float x[kHeads][PER];
+        float x[HEADS][PER];
         float2 ml = make_float2(-INFINITY, 0.f);
-        if (lane < heads) ml = *reinterpret_cast<const float2 *>(ml_in + row * 2);
+        if (mine < heads) ml = *reinterpret_cast<const float2 *>(ml_in + row * 2);
 #pragma unroll
-        for (int h = 0; h < kHeads; ++h) {
+        for (int h = 0; h < HEADS; ++h) {
             const int64_t r = __shfl_sync(0xffffffffu, row, h < heads ? h : 0);
             const float *src = acc_in + r * D + lane * PER;
             if constexpr (PER == 4) {
@@ -193,26 +211,44 @@ __global__ void __launch_bounds__(kJoinWarps * 32) tree_join_kernel(const __grid
             }
         }
         row = p == 0 ? later : row + step;
-#pragma unroll
-        for (int h = 0; h < kHeads; ++h) {
-            const float pm = __shfl_sync(0xffffffffu, ml.x, h), pl = __shfl_sync(0xffffffffu, ml.y, h);
-            const float mn = fmaxf(m[h], pm), base = mn == -INFINITY ? 0.f : mn;
-            const float f = ex2(m[h] - base), w = ex2(pm - base);
-            m[h] = mn;
-            l[h] = l[h] * f + w * pl;
-#pragma unroll
-            for (int e = 0; e < PER; ++e) acc[h][e] = fmaf(w, x[h][e], acc[h][e] * f);
-        }
+        const float mn = fmaxf(m, ml.x), base = mn == -INFINITY ? 0.f : mn;
+        const float f = m == mn ? 1.f : ex2(m - base), w = ex2(ml.x - base);
+        m = mn;
+        l = l * f + w * ml.y;
+        add(f, w, [&](int h, int e) { return x[h][e]; });
     }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
-    for (int h = 0; h < kHeads; ++h) {
+    for (int h = 0; h < HEADS; ++h) {
+        const float ih = __shfl_sync(0xffffffffu, inv, h);
         if (h >= heads) continue;
-        const float inv = l[h] > 0.f ? 1.f / l[h] : 0.f;
         uint16_t *dst = a.out + (pair + h) * D + lane * PER;
+        uint32_t w[PER / 2];
 #pragma unroll
-        for (int e = 0; e < PER; e += 2)
-            *reinterpret_cast<uint32_t *>(dst + e) = bf16x2(acc[h][e] * inv, acc[h][e + 1] * inv);
+        for (int e = 0; e < PER; e += 2) w[e / 2] = bf16x2(acc[h][e] * ih, acc[h][e + 1] * ih);
+        if constexpr (PER == 4)
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+        else
+            *reinterpret_cast<uint32_t *>(dst) = w[0];
     }
+}
+
+template <int D, int HEADS>
+cudaError_t launch_join(TreeArgs a, cudaStream_t stream) {
+    a.chunks = (a.G + HEADS - 1) / HEADS;
+    const dim3 grid((a.max_query_len + kJoinWarps - 1) / kJoinWarps, a.Hkv * a.chunks, a.S);
+    if (a.max_query_len <= kStagedRows)
+        return launch_dependent(tree_join_kernel<D, HEADS, true>, grid, dim3(kJoinWarps * 32), (size_t)a.max_query_len * 4 * D,
+                                stream, a);
+    return launch_dependent(tree_join_kernel<D, HEADS, false>, grid, dim3(kJoinWarps * 32), 0, stream, a);
+}
+
+// Up to four heads a warp (eight: 126.5 against 123.1 us for the 70B-shaped batch, 105 registers and
+// half the warps per SM; two: 125.8).
+template <int D>
+cudaError_t launch_join_heads(const TreeArgs &a, cudaStream_t stream) {
+    return a.G == 1 ? launch_join<D, 1>(a, stream) : a.G == 2 ? launch_join<D, 2>(a, stream)
+           : launch_join<D, 4>(a, stream);
 }
 
 // Partitions of the contexts and the workspace: as for the multi-token calls, n balanced
@@ -346,7 +382,6 @@ pa_status pa_tree_attention(pa_bf16 *out, const pa_bf16 *query, const pa_bf16 *k
     t.Hq = Hq;
     t.Hkv = Hkv;
     t.G = G;
-    t.chunks = (G + kHeads - 1) / kHeads;
     t.max_context_len = max_context_len;
     t.max_query_len = max_query_len;
     t.scale_log2 = scale * 1.4426950408889634f;
@@ -421,10 +456,11 @@ pa_status pa_tree_attention(pa_bf16 *out, const pa_bf16 *query, const pa_bf16 *k
         cudaGetLastError();
         return fail(PA_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(err));
     }
-    const int64_t jobs = (int64_t)max_query_len * Hkv * t.chunks;
-    const dim3 grid((unsigned)((jobs + kJoinWarps - 1) / kJoinWarps), S);
-    launch_dependent(D == 128 ? tree_join_kernel<128> : tree_join_kernel<64>, grid, dim3(kJoinWarps * 32), 0,
-                     (cudaStream_t)stream, t);
+    err = D == 128 ? launch_join_heads<128>(t, (cudaStream_t)stream) : launch_join_heads<64>(t, (cudaStream_t)stream);
+    if (err != cudaSuccess) {
+        cudaGetLastError();
+        return fail(PA_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(err));
+    }
     return check_launch(fn);
 }
 
