@@ -11,6 +11,7 @@
 #include <cuda_fp8.h>
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "pa_draft.h"
 #include "pa_internal.cuh"
@@ -21,7 +22,7 @@ namespace {
 constexpr int kTokens = 4;           // tokens per CTA
 constexpr int kThreadsPerToken = 64;
 constexpr int kThreads = kTokens * kThreadsPerToken;
-constexpr int kBatch = 4;            // rows a thread has in flight
+constexpr int kBatch = 2;            // rows a thread has in flight
 
 struct RotaryArgs {
     uint16_t *q_out, *k_out;
@@ -57,14 +58,38 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
     return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-// A CTA takes kTokens tokens; 64 threads per token hold D / 8 lanes per head row (16
-// bytes each), and a thread keeps its 8 cosines and sines for all the rows it visits.
-// LAYOUT: 0 = half (partners D/16-multiples of lanes apart: one shuffle), 1 = interleaved
-// (partners in the same lane), 2 = half with rot_dim / 2 not a multiple of 8 (partners
-// read one by one).
+// Eight 8-bit codes of a row with this scale: the cache's rounding rules.
+template <int KV>
+__device__ __forceinline__ uint2 codes8(const float (&x)[8], float scale) {
+    uint32_t code[2] = {0u, 0u};
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+        const float u = __fdiv_rn(x[e], scale), w = __fdiv_rn(x[e + 1], scale);
+        uint32_t two;
+        if constexpr (KV == PA_KV_FP8) {
+            two = __nv_cvt_float2_to_fp8x2(make_float2(u, w), __NV_SATFINITE, __NV_E4M3);
+        } else {
+            const int i0 = (int)fminf(fmaxf(rintf(u), -127.f), 127.f);
+            const int i1 = (int)fminf(fmaxf(rintf(w), -127.f), 127.f);
+            two = (i0 & 0xff) | ((uint32_t)(i1 & 0xff) << 8);
+        }
+        code[e / 4] |= two << (8 * (e & 2));
+    }
+    return make_uint2(code[0], code[1]);
+}
+
+// A CTA takes kTokens tokens, 64 threads each: D / 16 lanes per head row, a lane two 16-byte
+// pieces of it, so that the partners of a pair meet in one lane, and the lane's cosines and
+// sines serve all the rows it visits.
+// LAYOUT: 0 = half (rot_dim / 2 a multiple of 8: pieces c and c + rot_dim / 16, the rest of
+// the head in the other lanes), 1 = interleaved (neighbouring pieces), 2 = half with any
+// other rot_dim (neighbouring pieces, partners read one by one).
+// Bounds: HBM beyond a few hundred tokens.  8192 tokens of 64 + 8 + 8 heads, 336 MB: 5.2
+// TB/s with a piece a lane and partners through shuffles, when the instructions, not the
+// bytes, were most of the time.
 template <int D, int KV, int LAYOUT>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryArgs a) {
-    constexpr int LPR = D / 8;                       // lanes per row
+    constexpr int LPR = D / 16;                      // lanes per row
     constexpr int SLOTS = kThreadsPerToken / LPR;    // rows of a token at once
     __shared__ float2 s_cs[kTokens][D / 2];
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -75,136 +100,177 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
         const int tt = i / half, j = i % half;
         if (t0 + tt >= a.T) break;
         const uint64_t phase = (uint64_t)a.positions[t0 + tt] * a.table[j];
-        // the top 32 bits, rounded, as a signed number of half turns in [-1, 1)
-        const int32_t h = (int32_t)(uint32_t)((phase + 0x80000000ull) >> 32);
+        // the nearest quarter turn, and the signed rest in half turns: at most 1/4, so its fp32
+        // rounding is 2^-27 of a half turn
+        const uint32_t quarter = (uint32_t)((phase + 0x2000000000000000ull) >> 62);
+        const int64_t rest = (int64_t)(phase - ((uint64_t)quarter << 62));
         float s, c;
-        sincospif((float)h * 4.656612873077393e-10f, &s, &c);
-        s_cs[tt][j] = make_float2(c * a.factor, s * a.factor);
+        sincospif((float)rest * 1.0842021724855044e-19f, &s, &c);  // 2^-63
+        const float cq = quarter & 1 ? -s : c, sq = quarter & 1 ? c : s;
+        s_cs[tt][j] = make_float2((quarter & 2 ? -cq : cq) * a.factor, (quarter & 2 ? -sq : sq) * a.factor);
     }
-    __syncthreads();
     const int tt = tid / kThreadsPerToken, in = tid % kThreadsPerToken;
     const int64_t t = t0 + tt;
-    if (t >= a.T) return;
+    const bool real = t < a.T;
+    const bool append = a.k_cache != nullptr;
+    const int64_t slot = append && real ? a.slots[t] : -1;
+    __syncthreads();
+    if (!real) return;
     const int c = in % LPR, slot0 = in / LPR;
-    const unsigned gmask = (LPR == 32 ? 0xffffffffu : ((1u << LPR) - 1u)) << ((tid & 31) / LPR * LPR);
-    // this lane's cosines and signed sines: y[e] = x[e] cs[e] + partner[e] sn[e]
-    float cs[8], sn[8];
+    const unsigned gmask = ((1u << LPR) - 1u) << ((tid & 31) / LPR * LPR);
+    // the lane's pieces (units of 8 elements), and whether pairs in them are turned
+    const int rotated = a.rot / 16;  // LAYOUT 0: lanes with pairs
+    const bool paired = LAYOUT != 0 || c < rotated;
+    const int p0 = LAYOUT == 0 ? (paired ? c : 2 * c) : 2 * c, p1 = LAYOUT == 0 && paired ? c + rotated : p0 + 1;
+    // cosines and sines: of pair e in both pieces (LAYOUT 0), of pairs 2e, 2e + 1 (1), or of
+    // element e, signed (2; elements not turned: 1 and 0)
+    constexpr int NC = LAYOUT == 2 ? 16 : 8;
+    float cs[NC], sn[NC];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const int i = 8 * c + e;
+    for (int e = 0; e < NC; ++e) {
         cs[e] = 1.f;
         sn[e] = 0.f;
-        if (i < a.rot) {
-            const float2 w = s_cs[tt][LAYOUT == 1 ? i / 2 : (i < half ? i : i - half)];
-            cs[e] = w.x;
-            sn[e] = (LAYOUT == 1 ? (i & 1) : i >= half) ? w.y : -w.y;
+        if constexpr (LAYOUT == 2) {
+            const int i = 16 * c + e;
+            if (i < a.rot) {
+                const float2 w = s_cs[tt][i < half ? i : i - half];
+                cs[e] = w.x;
+                sn[e] = i < half ? -w.y : w.y;
+            }
+        } else {
+            const int j = LAYOUT == 0 ? 8 * p0 + e : 8 * c + e;
+            if (paired && j < half) {
+                const float2 w = s_cs[tt][j];
+                cs[e] = w.x;
+                sn[e] = w.y;
+            }
         }
     }
-    // lane holding the partners (LAYOUT 0)
-    const int pl = 8 * c >= a.rot ? c : (8 * c < half ? c + half / 8 : c - half / 8);
-    const bool append = a.k_cache != nullptr;
-    const int64_t slot = append ? a.slots[t] : -1;
+    // 32-bit words of the two pieces that hold turned elements (bf16 words that do not keep
+    // their bits, NaN payloads among them)
+    const int words0 = LAYOUT == 0 ? (paired ? 4 : 0) : min(max((a.rot - 8 * p0) / 2, 0), 4);
+    const int words1 = LAYOUT == 0 ? (paired ? 4 : 0) : min(max((a.rot - 8 * p1) / 2, 0), 4);
     const bool store = slot >= 0 && slot < (int64_t)a.N * a.bs;
     if (append && blockIdx.y == 0 && in == 0 && slot >= (int64_t)a.N * a.bs && a.err_flag)
         atomicOr(a.err_flag, PA_FLAG_SLOT_OUT_OF_RANGE);
     const int64_t blk = store ? slot / a.bs : 0;
     const int off = store ? (int)(slot % a.bs) : 0;
 
-    const int r_end = min(a.rows, ((int)blockIdx.y + 1) * a.rows_per_cta);
-    for (int r0 = blockIdx.y * a.rows_per_cta + slot0; r0 < r_end; r0 += SLOTS * kBatch) {
-        uint4 raw[kBatch];
-        float part[LAYOUT == 2 ? kBatch : 1][8];
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int r = r0 + b * SLOTS;
-            if (r >= r_end) break;
-            const uint16_t *src = r < a.Hq ? a.q + t * a.q_stride + (int64_t)r * D
-                                  : r < a.Hq + a.Hkv ? a.k + t * a.k_stride + (int64_t)(r - a.Hq) * D
-                                                     : a.v + t * a.v_stride + (int64_t)(r - a.Hq - a.Hkv) * D;
-            raw[b] = *reinterpret_cast<const uint4 *>(src + 8 * c);
-            if constexpr (LAYOUT == 2) {
+    auto rotate = [&](const uint4 &r0, const uint4 &r1, const float (&part)[LAYOUT == 2 ? 16 : 1], float (&x)[8], float (&y)[8]) {
+        unpack8(r0, x);
+        unpack8(r1, y);
+        if constexpr (LAYOUT == 0) {
+            if (paired) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const int i = 8 * c + e;
-                    part[b][e] = i < a.rot ? __uint_as_float((uint32_t)src[i < half ? i + half : i - half] << 16) : 0.f;
+                    const float u = x[e], w = y[e];
+                    x[e] = fmaf(-w, sn[e], u * cs[e]);
+                    y[e] = fmaf(u, sn[e], w * cs[e]);
                 }
+            }
+        } else if constexpr (LAYOUT == 1) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (e < words0) {
+                    const float u = x[2 * e], w = x[2 * e + 1];
+                    x[2 * e] = fmaf(-w, sn[e], u * cs[e]);
+                    x[2 * e + 1] = fmaf(u, sn[e], w * cs[e]);
+                }
+                if (e < words1) {
+                    const float u = y[2 * e], w = y[2 * e + 1];
+                    y[2 * e] = fmaf(-w, sn[4 + e], u * cs[4 + e]);
+                    y[2 * e + 1] = fmaf(u, sn[4 + e], w * cs[4 + e]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (16 * c + e < a.rot) x[e] = fmaf(part[e], sn[e], x[e] * cs[e]);
+                if (16 * c + 8 + e < a.rot) y[e] = fmaf(part[8 + e], sn[8 + e], y[e] * cs[8 + e]);
             }
         }
-        // a row may be rotated in place: all its lanes have read it before one writes
-        __syncwarp(gmask);
+    };
+    auto keep = [](const uint4 &raw, uint4 w, int words) {
+        if (words < 1) w.x = raw.x;
+        if (words < 2) w.y = raw.y;
+        if (words < 3) w.z = raw.z;
+        if (words < 4) w.w = raw.w;
+        return w;
+    };
+    // KIND 0: query rows, 1: key rows, 2: value rows; head h of this token at src + h D
+    auto rows = [&](auto kind, int begin, int end, const uint16_t *src, uint16_t *out, void *cache, float *scales) {
+        constexpr int KIND = decltype(kind)::value;
+        src += (int64_t)(begin + slot0) * D;
+        if (out) out += (int64_t)(begin + slot0) * D;
+        int64_t row = (blk * a.Hkv + begin + slot0) * a.bs + off;
+        const int64_t row_step = (int64_t)SLOTS * a.bs;
+        for (int h = begin + slot0; h < end; h += SLOTS * kBatch) {
+            uint4 raw[kBatch][2];
+            float part[LAYOUT == 2 && KIND < 2 ? kBatch : 1][LAYOUT == 2 ? 16 : 1];
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int r = r0 + b * SLOTS;
-            if (r >= r_end) break;
-            const bool is_v = r >= a.Hq + a.Hkv;
-            float x[8];
-            unpack8(raw[b], x);
-            if (!is_v) {
-                float p[8];
-                if constexpr (LAYOUT == 0) {
-                    const int from = (tid & 31) / LPR * LPR + pl;
-                    uint4 w;
-                    w.x = __shfl_sync(gmask, raw[b].x, from);
-                    w.y = __shfl_sync(gmask, raw[b].y, from);
-                    w.z = __shfl_sync(gmask, raw[b].z, from);
-                    w.w = __shfl_sync(gmask, raw[b].w, from);
-                    unpack8(w, p);
-                } else {
+            for (int b = 0; b < kBatch; ++b) {
+                if (h + b * SLOTS >= end) break;
+                raw[b][0] = *reinterpret_cast<const uint4 *>(src + b * SLOTS * D + 8 * p0);
+                raw[b][1] = *reinterpret_cast<const uint4 *>(src + b * SLOTS * D + 8 * p1);
+                if constexpr (LAYOUT == 2 && KIND < 2) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) p[e] = LAYOUT == 1 ? x[e ^ 1] : part[LAYOUT == 2 ? b : 0][e];
-                }
-                float y[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = 8 * c + e < a.rot ? fmaf(p[e], sn[e], x[e] * cs[e]) : x[e];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = y[e];
-            }
-            // bf16 words that are not rotated keep their bits (NaN payloads among them)
-            uint4 word = raw[b];
-            if (!is_v) {
-                const uint4 y = pack8(x);
-                if (8 * c < a.rot) word.x = y.x;
-                if (8 * c + 2 < a.rot) word.y = y.y;
-                if (8 * c + 4 < a.rot) word.z = y.z;
-                if (8 * c + 6 < a.rot) word.w = y.w;
-            }
-            if (r < a.Hq) {
-                *reinterpret_cast<uint4 *>(a.q_out + (t * a.Hq + r) * D + 8 * c) = word;
-                continue;
-            }
-            const int h = is_v ? r - a.Hq - a.Hkv : r - a.Hq;
-            if (!is_v && a.k_out) *reinterpret_cast<uint4 *>(a.k_out + (t * a.Hkv + h) * D + 8 * c) = word;
-            if (!store) continue;
-            const int64_t row = (blk * a.Hkv + h) * a.bs + off;
-            void *cache = is_v ? a.v_cache : a.k_cache;
-            if constexpr (KV == PA_KV_BF16) {
-                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(cache) + row * D + 8 * c) = word;
-            } else {
-                float amax = 0.f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
-#pragma unroll
-                for (int o = LPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(gmask, amax, o));
-                const float scale = amax > 0.f ? __fdiv_rn(amax, KV == PA_KV_FP8 ? 448.f : 127.f) : 1.f;
-                uint32_t code[2] = {0u, 0u};
-#pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    const float u = __fdiv_rn(x[e], scale), w = __fdiv_rn(x[e + 1], scale);
-                    uint32_t two;
-                    if constexpr (KV == PA_KV_FP8) {
-                        two = __nv_cvt_float2_to_fp8x2(make_float2(u, w), __NV_SATFINITE, __NV_E4M3);
-                    } else {
-                        const int i0 = (int)fminf(fmaxf(rintf(u), -127.f), 127.f);
-                        const int i1 = (int)fminf(fmaxf(rintf(w), -127.f), 127.f);
-                        two = (i0 & 0xff) | ((uint32_t)(i1 & 0xff) << 8);
+                    for (int e = 0; e < 16; ++e) {
+                        const int i = 16 * c + e;
+                        part[b][e] = i < a.rot ? __uint_as_float((uint32_t)src[b * SLOTS * D + (i < half ? i + half : i - half)] << 16) : 0.f;
                     }
-                    code[e / 4] |= two << (8 * (e & 2));
                 }
-                *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(cache) + row * D + 8 * c) = make_uint2(code[0], code[1]);
-                if (c == 0) (is_v ? a.v_scale : a.k_scale)[row] = scale;
             }
+            // a row may be rotated in place: all its lanes have read it before one writes
+            if (LAYOUT == 2) __syncwarp(gmask);
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                if (h + b * SLOTS >= end) break;
+                float x[8], y[8];
+                uint4 w0 = raw[b][0], w1 = raw[b][1];
+                if constexpr (KIND < 2) {
+                    rotate(raw[b][0], raw[b][1], part[LAYOUT == 2 ? b : 0], x, y);
+                    w0 = keep(w0, pack8(x), words0);
+                    w1 = keep(w1, pack8(y), words1);
+                    if (KIND == 0 || out) {
+                        *reinterpret_cast<uint4 *>(out + b * SLOTS * D + 8 * p0) = w0;
+                        *reinterpret_cast<uint4 *>(out + b * SLOTS * D + 8 * p1) = w1;
+                    }
+                } else if constexpr (KV != PA_KV_BF16) {
+                    unpack8(w0, x);
+                    unpack8(w1, y);
+                }
+                if (KIND == 0 || !store) continue;
+                const int64_t at = (row + b * row_step) * D;
+                if constexpr (KV == PA_KV_BF16) {
+                    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(cache) + at + 8 * p0) = w0;
+                    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(cache) + at + 8 * p1) = w1;
+                } else {
+                    float amax = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fmaxf(fabsf(x[e]), fabsf(y[e])));
+#pragma unroll
+                    for (int o = LPR / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(gmask, amax, o));
+                    const float scale = amax > 0.f ? __fdiv_rn(amax, KV == PA_KV_FP8 ? 448.f : 127.f) : 1.f;
+                    *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(cache) + at + 8 * p0) = codes8<KV>(x, scale);
+                    *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(cache) + at + 8 * p1) = codes8<KV>(y, scale);
+                    if (c == 0) scales[row + b * row_step] = scale;
+                }
+            }
+            src += SLOTS * kBatch * D;
+            if (out) out += SLOTS * kBatch * D;
+            row += row_step * kBatch;
         }
-    }
+    };
+    const int lo = blockIdx.y * a.rows_per_cta, hi = min(a.rows, lo + a.rows_per_cta);
+    if (lo < a.Hq)
+        rows(std::integral_constant<int, 0>(), lo, min(hi, a.Hq), a.q + t * a.q_stride, a.q_out + t * a.Hq * D, nullptr, nullptr);
+    const int klo = max(lo - a.Hq, 0), khi = min(hi - a.Hq, a.Hkv);
+    if (klo < khi)
+        rows(std::integral_constant<int, 1>(), klo, khi, a.k + t * a.k_stride, a.k_out ? a.k_out + t * a.Hkv * D : nullptr, a.k_cache,
+             a.k_scale);
+    const int vlo = max(lo - a.Hq - a.Hkv, 0), vhi = hi - a.Hq - a.Hkv;
+    if (vlo < vhi && store)
+        rows(std::integral_constant<int, 2>(), vlo, vhi, a.v + t * a.v_stride, nullptr, a.v_cache, a.v_scale);
 }
 
 template <int D, int KV>
@@ -372,7 +438,7 @@ pa_status pa_rotary_and_cache(pa_bf16 *query_out, pa_bf16 *key_out, const pa_bf1
     a.rows = Hq + Hkv + (append ? Hkv : 0);
     // enough CTAs for one wave at two per SM, else all rows of a token in one CTA (its
     // cosines are computed once)
-    const int step = kThreadsPerToken / (D / 8);  // rows of a token at once
+    const int step = kThreadsPerToken / (D / 16);  // rows of a token at once
     const int groups = (T + kTokens - 1) / kTokens;
     const int most = (a.rows + step - 1) / step;
     const int split = std::min(most, std::max(1, 304 / groups));
