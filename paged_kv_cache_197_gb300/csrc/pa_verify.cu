@@ -27,9 +27,10 @@
 namespace pa {
 namespace {
 
-// 256 threads: four CTAs per SM at 64 registers, so 64 sequences' clusters are all resident.
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+// Threads of a CTA: 512 while two CTAs per SM hold the batch (a run is half as long, and so is
+// a pass), else 256: four CTAs per SM at 64 registers hold 76 sequences.
+constexpr int kFew = 512, kMany = 256;
+constexpr int kMaxWarps = kFew / 32;
 constexpr int kMaxCluster = 8;
 
 struct VerifyArgs {
@@ -75,6 +76,16 @@ __device__ __forceinline__ void unpack(const uint4 &w, float (&x)[8]) {
     }
 }
 
+// Four neighbouring entries (4 v aligned to them).
+__device__ __forceinline__ void quad(const float *p, float (&x)[4]) { unpack(__ldg(reinterpret_cast<const uint4 *>(p)), x); }
+__device__ __forceinline__ void quad(const uint16_t *p, float (&x)[4]) {
+    const uint2 w = __ldg(reinterpret_cast<const uint2 *>(p));
+    x[0] = fmaxf(__uint_as_float(w.x << 16), 0.f);
+    x[1] = fmaxf(__uint_as_float(w.x & 0xffff0000u), 0.f);
+    x[2] = fmaxf(__uint_as_float(w.y << 16), 0.f);
+    x[3] = fmaxf(__uint_as_float(w.y & 0xffff0000u), 0.f);
+}
+
 // An unevaluated sum of two fp32, |lo| <= ulp(hi) / 2 up to a few roundings.
 struct Pair {
     float hi, lo;
@@ -96,6 +107,13 @@ __device__ __forceinline__ Pair residual(float p, float q, Pair C) {
     lo = __fsub_rn(lo, __fsub_rn(hi, d));
     const bool pos = hi > 0.f;
     return {pos ? hi : 0.f, pos ? lo : 0.f};
+}
+
+// The same for C = 1, a node's first rejection: p - q and its rounding error.
+__device__ __forceinline__ Pair residual(float p, float q) {
+    const float d = __fsub_rn(p, q), b = __fsub_rn(p, d);
+    const float lo = __fsub_rn(__fsub_rn(p, __fadd_rn(d, b)), __fsub_rn(q, b));
+    return {d > 0.f ? d : 0.f, d > 0.f ? lo : 0.f};
 }
 
 __device__ __forceinline__ void add(Pair &s, Pair x) {
@@ -136,13 +154,14 @@ struct Task {
 
 struct Shared {
     Pair part[2][kMaxCluster];              // the CTAs' sums of a pass, by its parity
-    Pair run[kWarps];                       // the warps' sums of the last pass
+    Pair run[kMaxWarps];                    // the warps' sums of the last pass
     double from, target;                    // the draw: R's sum before the owner's run, and its place
     int owner_run;                          // the run of this CTA that holds it, or -1
     Task task;
     float tp[PA_TREE_MAX_NODES], tq[PA_TREE_MAX_NODES];  // p and q of each row's token at its parent
     int parent[PA_TREE_MAX_NODES], token[PA_TREE_MAX_NODES], place[PA_TREE_MAX_NODES];
     float u[PA_TREE_MAX_NODES];
+    int block[PA_TREE_MAX_NODES];           // block of the sequence's slot at each place
     int gone[PA_TREE_MAX_NODES];            // the current node's rejected tokens (no drafter)
 };
 
@@ -154,17 +173,20 @@ struct Residual {
     const int *gone;
     int n_gone;
 
-    __device__ __forceinline__ Pair operator()(int64_t v) const {
-        const float x = prob(p, v);
-        if (q) return residual(x, prob(q, v), c);
+    // R(v) from the entries x of p and y of q
+    __device__ __forceinline__ Pair weight(int64_t v, float x, float y) const {
+        if (q) return residual(x, y, c);
         for (int i = 0; i < n_gone; ++i)
             if (gone[i] == (int)v) return {0.f, 0.f};
         return {x, 0.f};
     }
+    __device__ __forceinline__ Pair operator()(int64_t v) const {
+        return weight(v, prob(p, v), q ? prob(q, v) : 0.f);
+    }
 };
 
-// The sum of R over a warp's run [begin, end).
-template <typename T, bool DRAFTED>
+// The sum of R over a warp's run [begin, end).  DRAFTED: 0 = p alone, 1 = p - q, 2 = p - C q.
+template <typename T, int DRAFTED>
 __device__ __forceinline__ Pair run_sum(const Residual<T> &R, int64_t begin, int64_t end, bool vector, int lane) {
     constexpr int N = kVec<T>;
     Pair s{0.f, 0.f};
@@ -190,7 +212,8 @@ __device__ __forceinline__ Pair run_sum(const Residual<T> &R, int64_t begin, int
                 unpack(a[i], x);
                 if (DRAFTED) unpack(b[i], y);
 #pragma unroll
-                for (int e = 0; e < N; ++e) add(s, DRAFTED ? residual(x[e], y[e], R.c) : Pair{x[e], 0.f});
+                for (int e = 0; e < N; ++e)
+                    add(s, DRAFTED == 2 ? residual(x[e], y[e], R.c) : DRAFTED == 1 ? residual(x[e], y[e]) : Pair{x[e], 0.f});
             }
         }
     }
@@ -204,7 +227,8 @@ __device__ __forceinline__ Pair run_sum(const Residual<T> &R, int64_t begin, int
                 if (DRAFTED) y[i] = prob(R.q, v + i * 32 + lane);
             }
 #pragma unroll
-            for (int i = 0; i < U; ++i) add(s, DRAFTED ? residual(x[i], y[i], R.c) : Pair{x[i], 0.f});
+            for (int i = 0; i < U; ++i)
+                add(s, DRAFTED == 2 ? residual(x[i], y[i], R.c) : DRAFTED == 1 ? residual(x[i], y[i]) : Pair{x[i], 0.f});
         }
     }
     for (v += lane; v < end; v += 32) add(s, R(v));
@@ -216,21 +240,37 @@ __device__ __forceinline__ Pair run_sum(const Residual<T> &R, int64_t begin, int
 // summed by the warp, four to a lane, lane g keeping the sum of group g; the group that
 // passes the target is scanned.
 template <typename T>
-__device__ __forceinline__ int run_find(const Residual<T> &R, int64_t begin, int64_t end, double at, double target, int lane) {
+__device__ __forceinline__ int run_find(const Residual<T> &R, int64_t begin, int64_t end, double at, double target, bool vector, int lane) {
     int64_t group = -1, last_group = -1;  // first entry of the group that passes; of the last with weight
     double last_at = at;
     for (int64_t v0 = begin; v0 < end && group < 0; v0 += 32 * 128) {
         Pair mine{0.f, 0.f};
-#pragma unroll 4
-        for (int g = 0; g < 32; ++g) {
-            const int64_t v = v0 + g * 128 + lane * 4;
-            if (v0 + g * 128 >= end) break;
-            Pair s{0.f, 0.f};
+        for (int g0 = 0; g0 < 32 && v0 + g0 * 128 < end; g0 += 4) {
+            // four groups' entries are loaded before the first is added up
+            float x[4][4], y[4][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (v + e < end) add(s, R(v + e));
-            s = lanes_sum(s, 32);
-            if (lane == g) mine = s;
+            for (int g = 0; g < 4; ++g) {
+                const int64_t v = v0 + (g0 + g) * 128 + lane * 4;
+                if (vector && v + 4 <= end) {
+                    quad(R.p + v, x[g]);
+                    if (R.q) quad(R.q + v, y[g]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        x[g][e] = v + e < end ? prob(R.p, v + e) : 0.f;
+                        y[g][e] = R.q && v + e < end ? prob(R.q, v + e) : 0.f;
+                    }
+                }
+            }
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int64_t v = v0 + (g0 + g) * 128 + lane * 4;
+                Pair s{0.f, 0.f};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) add(s, R.weight(v + e, x[g][e], y[g][e]));
+                s = lanes_sum(s, 32);
+                if (lane == g0 + g) mine = s;
+            }
         }
         const double w = value(mine), upto = warp_scan(w, lane);
         const unsigned hit = __ballot_sync(0xffffffffu, w > 0.0 && at + upto > target);
@@ -267,8 +307,9 @@ __device__ __forceinline__ int run_find(const Residual<T> &R, int64_t begin, int
     return (int)(last_group + from * 4 + e);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_constant__ VerifyArgs a) {
+template <typename T, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(const __grid_constant__ VerifyArgs a) {
+    constexpr int kWarps = kThreads / 32;
     __shared__ Shared sh;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -287,6 +328,10 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
             sh.token[j] = x;
             sh.place[j] = j ? -1 : 0;
             sh.u[j] = j ? a.u[r0 + j] : 0.f;
+            if (a.slots) {
+                const int64_t at = ((int64_t)max(a.context_lens[s], 0) + j) / a.bs;
+                sh.block[j] = at < a.M ? a.block_tables[(int64_t)s * a.M + at] : -1;
+            }
             // every test needs p and q at the row's token, at its parent
             float tp = 0.f, tq = 0.f;
             if (p >= 0 && p < j && x >= 0 && x < a.V) {
@@ -394,7 +439,9 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
         R.c = task.c;
         R.gone = sh.gone;
         R.n_gone = Q ? 0 : task.rejected;
-        const Pair d = R.q ? run_sum<T, true>(R, begin, end, a.vector != 0, lane) : run_sum<T, false>(R, begin, end, a.vector != 0, lane);
+        const Pair d = !R.q ? run_sum<T, 0>(R, begin, end, a.vector != 0, lane)
+                       : R.c.hi == 1.f && R.c.lo == 0.f ? run_sum<T, 1>(R, begin, end, a.vector != 0, lane)
+                                                        : run_sum<T, 2>(R, begin, end, a.vector != 0, lane);
         if (lane == 0) sh.run[warp] = d;
         __syncthreads();
         if (warp == 0) {
@@ -451,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
         R.c = task.c;
         R.gone = sh.gone;
         R.n_gone = Q ? 0 : task.rejected;
-        const int v = run_find(R, begin, end, sh.from, sh.target, lane);
+        const int v = run_find(R, begin, end, sh.from, sh.target, a.vector != 0, lane);
         if (lane == 0) tokens_out[n - 1] = v;
     }
     // ---- the branch
@@ -466,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
             if (place > 0) tokens_out[place - 1] = sh.token[j];
             if (a.slots) {
                 const int64_t pos = (int64_t)max(a.context_lens[s], 0) + place;
-                const int b = pos / a.bs < a.M ? a.block_tables[(int64_t)s * a.M + pos / a.bs] : -1;
+                const int b = sh.block[place];
                 if (b >= 0 && b < a.N)
                     slot = (int64_t)b * a.bs + pos % a.bs;
                 else
@@ -478,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
 }
 
 template <typename T>
-cudaError_t launch_verify(const VerifyArgs &a, int S, cudaStream_t stream) {
+cudaError_t launch_verify(const VerifyArgs &a, int S, int threads, cudaStream_t stream) {
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -487,11 +534,11 @@ cudaError_t launch_verify(const VerifyArgs &a, int S, cudaStream_t stream) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)S * a.cluster);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(threads);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, verify_kernel<T>, a);
+    return threads == kFew ? cudaLaunchKernelEx(&cfg, verify_kernel<T, kFew>, a) : cudaLaunchKernelEx(&cfg, verify_kernel<T, kMany>, a);
 }
 
 }  // namespace
@@ -555,12 +602,13 @@ extern "C" pa_status pa_verify_tree(int32_t *tokens_out, int32_t *path, int32_t 
     a.N = N;
     // small vocabularies: one CTA, whose sums need no cluster barrier
     a.cluster = V > 8192 ? kMaxCluster : 1;
-    const int64_t runs = (int64_t)a.cluster * kWarps;
+    const int threads = (int64_t)S * a.cluster <= 2 * device_sms() ? kFew : kMany;
+    const int64_t runs = (int64_t)a.cluster * (threads / 32);
     a.run = (int)align_up((size_t)((V + runs - 1) / runs), 8);
     const int64_t elem = prob_dtype == PA_PROB_F32 ? 4 : 2;
     auto rows16 = [&](const void *p, int64_t stride) { return aligned16(p) && stride * elem % 16 == 0; };
     a.vector = rows16(target_probs, target_stride) && (!draft_probs || rows16(draft_probs, draft_stride));
-    prob_dtype == PA_PROB_F32 ? launch_verify<float>(a, S, (cudaStream_t)stream)
-                              : launch_verify<uint16_t>(a, S, (cudaStream_t)stream);
+    prob_dtype == PA_PROB_F32 ? launch_verify<float>(a, S, threads, (cudaStream_t)stream)
+                              : launch_verify<uint16_t>(a, S, threads, (cudaStream_t)stream);
     return check_launch(fn);
 }
