@@ -130,12 +130,15 @@ size_t pa_tree_workspace_size(int S, int T, int Hq, int Hkv, int D, int bs, int 
  *   query_start        [S + 1] int32, device; parents [T] int32, device (see above; several
  *                      rows of a sequence may have parent -1).
  *   max_query_len      host bound of the rows of a sequence, 1 .. min(T, PA_TREE_MAX_NODES).
- *   workspace          pa_tree_workspace_size(...) bytes, 256-byte aligned (NULL when 0).
+ *   workspace          pa_tree_workspace_size(...) bytes, 256-byte aligned.
  * A sequence whose offsets are outside [0, T], decreasing or longer than max_query_len is
  * left out (PA_FLAG_QUERY_OUT_OF_RANGE), as is one with a parent that is neither -1 nor
  * below its row (PA_FLAG_TREE_PARENT): its rows of out are not written.  Other arguments,
  * cache types and device-side checks as in pa_multi_token_attention.  Scores, softmax
- * statistics and weighted sums are fp32; the result is rounded once to bf16.
+ * statistics and weighted sums are fp32, the weights of cached tokens bf16 (fp16 with 8-bit
+ * caches); the result is rounded once to bf16.  Entries of an 8-bit cache with D = 128 are
+ * taken as fp16(code * fp16(scale)), within 2^-10 of code * scale, or 2^-31 of the largest
+ * scale of the 128 tokens they are read with where that is more.
  */
 pa_status pa_tree_attention(pa_bf16 *out, const pa_bf16 *query, const pa_bf16 *key,
                             int64_t key_stride, const pa_bf16 *value, int64_t value_stride,
@@ -179,8 +182,8 @@ pa_status pa_tree_attention(pa_bf16 *out, const pa_bf16 *query, const pa_bf16 *k
  *                      entry is missing or outside [0, N) is -1 (PA_FLAG_BLOCK_OUT_OF_RANGE).
  *                      Ignored when NULL: block_tables, M, context_lens, bs, N.
  * A sequence with bad offsets or parents is left out as in pa_tree_attention.  Sums are
- * carried in pairs of fp32 (about 48 bits), borders decided in fp64; results do not
- * depend on the launch.  V <= 2^30, max_query_len <= min(T, PA_TREE_MAX_NODES).
+ * carried in pairs of fp32 (about 48 bits), borders decided in fp64, always in the
+ * same order for the same shapes.  V <= 2^30, max_query_len <= min(T, PA_TREE_MAX_NODES).
  */
 pa_status pa_verify_tree(int32_t *tokens_out, int32_t *path, int32_t *n_out, int64_t *slot_mapping,
                          const int32_t *draft_tokens, const void *target_probs,

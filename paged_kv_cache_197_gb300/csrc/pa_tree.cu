@@ -38,7 +38,10 @@ struct TreeArgs {
 };
 
 constexpr int kJoinWarps = 8;      // rows of a CTA
-constexpr int kStagedRows = 96;    // rows of a sequence kept in shared memory
+// Rows of a sequence kept in shared memory: of 512 bytes at head_dim 128, 45 KB with the
+// parents, four CTAs an SM, and below the 48 KB a launch may have unasked.
+constexpr int kStagedRows = 88;
+static_assert(kStagedRows * 512 + PA_TREE_MAX_NODES * 4 <= 48 * 1024, "shared memory of a join without an attribute");
 
 // The sums over the warp of HEADS values; lane i ends with that of value i % HEADS.  Halving
 // exchanges while there is more than one value to a lane, then plain sums: 6 shuffles for
@@ -309,7 +312,8 @@ pa_status check_tree_args(const char *fn, int S, int T, int Hq, int Hkv, int D, 
     if (max_query_len < 1 || max_query_len > T || max_query_len > PA_TREE_MAX_NODES)
         return fail(PA_ERR_INVALID_ARG, "%s: max_query_len = %d (1 .. min(T, %d))", fn, max_query_len, PA_TREE_MAX_NODES);
     const int64_t cb = ((int64_t)max_query_len * (Hq / Hkv) + multi_cols_per_cta() - 1) / multi_cols_per_cta();
-    if ((int64_t)Hkv * cb > 65535) return fail(PA_ERR_UNSUPPORTED, "%s: too many rows and heads", fn);
+    if ((int64_t)Hkv * cb > 65535 || (int64_t)Hkv * ((Hq / Hkv + 3) / 4) > 65535)
+        return fail(PA_ERR_UNSUPPORTED, "%s: too many rows and heads", fn);
     return PA_OK;
 }
 

@@ -22,8 +22,9 @@
 // Tensor memory: S of the lanes at columns 0 and 128 (overwritten by P as 16-bit pairs, the A
 // operand of P V), O at 256 and 384.
 // 8-bit caches: an entry is code x scale in fp16, in units of a power of two per tile (2^e,
-// the tile's largest scale below it), the scale rounded to fp16 and the product once more
-// (together within 2^-11; an entry 2^-24 below the tile's largest is lost); the query rows
+// the tile's largest scale below 2^7 of them, so entries below 448 x 128), the scale rounded
+// to fp16 and the product once more (2^-11 each; scales to 2^-20 of the tile's largest keep
+// all their bits, and what is below 2^-31 of it is lost); the query rows
 // are fp16 scaled by a power of two each (exact).  The columns take both powers into their
 // score factor, and keep the base m above the scores plus the values' e: a weight p 2^e
 // stays below 2^8 whatever the scales.  Scales in fp32 per element instead, on the scores and
@@ -226,6 +227,9 @@ __device__ __forceinline__ void scaled_f16(const uint4 &c, __half2 scale, uint4 
         }
     }
 }
+
+constexpr float kTiny = 1.17549435e-38f;  // least score factor: 0 times a masked -inf is a NaN
+constexpr int kScaleTop = 7;  // scales below 2^7 units: 448 x 2^7 is below fp16's 65504
 
 // Exponent e with |x| < 2^e for the bits of a positive x, kept in -100 .. 100.
 __device__ __forceinline__ int exponent_over(uint32_t bits) {
@@ -562,9 +566,9 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                 // the tile's power of two (scales behind the context may hold anything)
                 const float *scale = sh.raw_scale[rst];
                 const float4 s4 = reinterpret_cast<const float4 *>(scale)[lane];
-                const float top = fmaxf(fmaxf(4 * lane < left ? s4.x : 0.f, 4 * lane + 1 < left ? s4.y : 0.f),
-                                        fmaxf(4 * lane + 2 < left ? s4.z : 0.f, 4 * lane + 3 < left ? s4.w : 0.f));
-                const int e = exponent_over(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+                const float top = fmaxf(fmaxf(4 * lane < left ? fabsf(s4.x) : 0.f, 4 * lane + 1 < left ? fabsf(s4.y) : 0.f),
+                                        fmaxf(4 * lane + 2 < left ? fabsf(s4.z) : 0.f, 4 * lane + 3 < left ? fabsf(s4.w) : 0.f));
+                const int e = exponent_over(__reduce_max_sync(0xffffffffu, __float_as_uint(top))) - kScaleTop;
                 const float down = __uint_as_float((uint32_t)(127 - e) << 23);  // 2^-e
                 if (me == 0) {
                     // the lanes have read this slot's last tile
@@ -729,16 +733,17 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                 }
                 const int k0 = (u.t0 + t) * kTile;
                 if (!idle) {
+                    const int left = u.ctx - k0;  // tokens of the context from the tile on
                     float factor = rs, over = 0.f;  // of the scores; exponent of the values' unit
                     if constexpr (QUANT) {
                         const float2 unit = sh.unit[j % kScaleSlots];
                         factor = rs * __uint_as_float((uint32_t)(127 + (int)unit.x) << 23);
                         over = unit.y;
                     }
+                    if (left < kTile) factor = fmaxf(factor, kTiny);
                     // The scores are read twice, for the maximum and for the weights, 64 and 32 at a
                     // time, in loops that stay loops: all 128 in registers spilled, and code
                     // unrolled over the tile starved the roles of instructions.
-                    const int left = u.ctx - k0;  // tokens of the context from the tile on
                     float mx[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) mx[i] = -INFINITY;

@@ -26,15 +26,16 @@ def rotated(x, positions, inv_freq, interleaved, factor):
 
 
 # ------------------------------------------------------------------------------ tree
-def tree_attention(q, k, v, k_cache, v_cache, k_scale, v_scale, tables, lens, starts, parents, scale):
-    """(out, spread): the attention and sum_t w_t |v_t|, both [T][Hq][D] fp64 (NaN in rows of no
-    sequence)."""
+def tree_attention(q, k, v, k_cache, v_cache, k_scale, v_scale, tables, lens, starts, parents, scale, entries=0.0):
+    """(out, spread, taken): the attention, sum_t w_t |v_t|, and what cached keys and values off by
+    `entries` relative, or 2^-31 of the cache's largest scale, may change, all [T][Hq][D] fp64 (NaN in
+    rows of no sequence)."""
     q, k, v = (t.double().cpu() for t in (q, k, v))
     T, Hq, D = q.shape
     Hkv, bs = k_cache.shape[1], k_cache.shape[2]
     G = Hq // Hkv
     out = torch.full((T, Hq, D), float("nan"), dtype=torch.float64)
-    spread = out.clone()
+    spread, taken = out.clone(), torch.zeros_like(out)
     tables, k_cache, v_cache = tables.cpu(), k_cache.cpu(), v_cache.cpu()
 
     def context(cache, scales, s, n):
@@ -63,7 +64,29 @@ def tree_attention(q, k, v, k_cache, v_cache, k_scale, v_scale, tables, lens, st
             w = torch.softmax((q[a:b, h] @ kk[h // G].T * scale).masked_fill(~mask, -math.inf), -1)
             out[a:b, h] = w @ vv[h // G]
             spread[a:b, h] = w @ vv[h // G].abs()
-    return out, spread
+            if entries and n:
+                # Scores off by e_t change a weight's logarithm by at most e_t + log sum w exp(e), which
+                # is at most e_t + E' exp(E) with E' = sum w e, E = max e; so the weight by at most
+                # w_t (e_t + E') exp(4 E) while E is below 0.2.
+                kc, vc = (x[h // G][:n].abs() * entries + 2.0 ** -31 * float(top) for x, top in (
+                    (kk, _largest(k_scale, tables, lens)), (vv, _largest(v_scale, tables, lens))))
+                e = torch.zeros(L, n + L, dtype=torch.float64)
+                e[:, :n] = abs(scale) * (q[a:b, h].abs() @ kc.T)
+                assert e.max() < 0.2
+                mean, grow = (w * e).sum(-1, keepdim=True), torch.exp(4 * e.amax(-1, keepdim=True))
+                taken[a:b, h] = grow * ((w * (e + mean)) @ vv[h // G].abs() + w[:, :n] @ vc)
+    return out, spread, taken
+
+
+def _largest(scales, tables, lens):
+    """The largest scale of the sequences' cached tokens."""
+    top, bs = 0.0, scales.shape[2]
+    for s, n in enumerate(lens):
+        ids = tables[s, : -(-n // bs)].long()
+        if n:
+            x = scales.cpu()[ids].abs().permute(1, 0, 2).reshape(scales.shape[1], -1)[:, :n]
+            top = max(top, float(x.max()))
+    return top
 
 
 def random_parents(lens, gen, kind="tree"):

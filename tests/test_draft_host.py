@@ -154,7 +154,9 @@ def test_tree_refusals(pa):
     size = lambda **k: pa.pa_tree_workspace_size(**{**dict(  # noqa: E731
         S=2, T=8, Hq=8, Hkv=2, D=128, bs=16, kv_dtype=0, max_context_len=64, max_query_len=4), **k})
     assert size(D=80) == 0 and size(max_query_len=9) == 0 and size(kv_dtype=3) == 0
-    assert size(max_context_len=0) >= 0
+    assert size(max_context_len=0) > 0
+    # more groups of four query heads than a grid has rows
+    assert size(Hq=5 * 40000, Hkv=40000, max_query_len=1) == 0 and size(Hq=4 * 40000, Hkv=40000, max_query_len=1) > 0
 
 
 def test_verify_refusals(pa):

@@ -256,21 +256,27 @@ def _tree_call(pa, c, max_ctx=None, max_q=None, out=None, flag=None, workspace=N
 
 
 def _tree_reference(c):
+    return _tree_taken(c)[:2]
+
+
+def _tree_taken(c, entries=0.0):
     return ref.tree_attention(c["q"], c["k"], c["v"], c["cache"]["k_cache"], c["cache"]["v_cache"], c["cache"].get("k_scale"),
-                              c["cache"].get("v_scale"), c["tables"], c["lens"], c["starts"], c["parents"], c["scale"])
+                              c["cache"].get("v_scale"), c["tables"], c["lens"], c["starts"], c["parents"], c["scale"], entries)
 
 
 def _tree_check(out, c):
     """The output is rounded to bf16 once (2^-8 of it), and each softmax weight once, to bf16 or fp16,
     before its product with v (2^-8 of sum w |v|; the sum of the weights takes them unrounded).
     Scores, exponentials and sums in fp32: |score| below 2^5 here, off by a few 2^-24 of it, is below
-    2^-16 of a weight, ex2.approx 2^-22; together under 2^-12 of sum w |v|."""
-    want, spread = _tree_reference(c)
+    2^-16 of a weight, ex2.approx 2^-22; together under 2^-12 of sum w |v|.  8-bit caches, heads of
+    128: an entry is off by 2^-11 for its scale's rounding and 2^-11 for its own (fp16)."""
+    quant = "k_scale" in c["cache"] and c["q"].shape[2] == 128
+    want, spread, taken = _tree_taken(c, 2.0 ** -10 * (1 + 2.0 ** -11) if quant else 0.0)
     got = out.double().cpu()
     none = torch.isnan(want)
     assert torch.isnan(got[none]).all()  # rows of no sequence are not written
     off = (got - want).abs()[~none]
-    bound = (2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -12) * spread)[~none]
+    bound = (2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -12) * spread + taken)[~none]
     assert torch.isfinite(got[~none]).all()
     assert (off <= bound).all(), (off / bound).max().item()
 
@@ -314,6 +320,59 @@ def test_tree_large(pa, kind, L, kv):
 def test_tree_head_layouts(pa, Hq, Hkv, kv):
     """One head per kv head, twelve, and 64 (several column blocks of one row)."""
     c = _tree_case(kv, 128, 32, Hq, Hkv, [700, 90], [9, 40], Hq)
+    _tree_check(_tree_call(pa, c), c)
+
+
+@pytest.mark.parametrize("D", [128, 64])
+@pytest.mark.parametrize("L", [87, 88, 89, 94, 96, 97])
+def test_tree_rows_at_the_staging_limit(pa, L, D):
+    """Trees on both sides of the most rows whose own keys and values are kept on chip."""
+    c = _tree_case("bf16", D, 16, 8, 2, [50, 0], [L, 3], L)
+    _tree_check(_tree_call(pa, c), c)
+
+
+@pytest.mark.parametrize("D", [128, 64])
+@pytest.mark.parametrize("kv", ["bf16", "int8", "fp8"])
+def test_tree_softmax_scales(pa, kv, D):
+    """A negative scale, and 0: every token the same weight."""
+    c = _tree_case(kv, D, 16, 12, 4, [300, 70, 129], [9, 30, 40], 23)
+    for scale in (-(D ** -0.5), 0.0):
+        c["scale"] = scale
+        _tree_check(_tree_call(pa, c), c)
+
+
+@pytest.mark.parametrize("D", [128, 64])
+@pytest.mark.parametrize("kv", ["int8", "fp8"])
+def test_tree_scales_of_all_sizes(pa, kv, D):
+    """Scales of neighbouring tokens up to 2^18 apart, some of them 0 or negative."""
+    c = _tree_case(kv, D, 16, 8, 2, [300, 70, 129, 1000], [9, 30, 40, 2], 29)
+    g = _gen(1)
+    for name in ("k_scale", "v_scale"):
+        t = c["cache"][name]
+        t *= (2.0 ** torch.randint(-18, 1, t.shape, generator=g)).to(DEV)
+        t *= (torch.randint(0, 5, t.shape, generator=g) - 1).sign().to(DEV)
+    _tree_check(_tree_call(pa, c), c)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_tree_many_sequences(pa, kv):
+    """More sequences than threads in a block, most of them short, some empty, in one call."""
+    g = _gen(31)
+    lens = torch.randint(0, 200, (700,), generator=g).tolist()
+    nodes = torch.randint(0, 4, (700,), generator=g).tolist()
+    c = _tree_case(kv, 128, 16, 4, 2, lens, nodes, 32)
+    flag = _flag()
+    out = _tree_call(pa, c, flag=flag)
+    torch.cuda.synchronize()
+    assert flag.item() == 0
+    _tree_check(out, c)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "int8"])
+@pytest.mark.parametrize("L", [2, 70])
+def test_tree_long_shares(pa, kv, L):
+    """Dozens of tiles and several units to a block of threads, whatever the order of the lengths."""
+    c = _tree_case(kv, 128, 32, 16, 4, [30000, 5, 20001, 640, 30000, 0, 128], [L, 3, 1, L, 4, 2, L], 37)
     _tree_check(_tree_call(pa, c), c)
 
 
@@ -366,10 +425,10 @@ def test_tree_leaves_out_bad_sequences(pa, kv, D):
         if at is not None:
             good["parents"] = list(c["parents"])
             good["parents"][5 + at] = 0
-        want, spread = _tree_reference(good)
+        want, spread, taken = _tree_taken(good, 2.0 ** -10 * (1 + 2.0 ** -11) if kv != "bf16" else 0.0)
         rows = [*range(5), *range(13, 17)]
         off = (out.double().cpu() - want).abs()[rows]
-        assert (off <= (2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -12) * spread)[rows]).all()
+        assert (off <= (2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -12) * spread + taken)[rows]).all()
 
 
 @pytest.mark.parametrize("kv,D", [("bf16", 128), ("bf16", 64), ("int8", 128), ("fp8", 128)])
