@@ -181,9 +181,9 @@ pa_status pa_tree_attention(pa_bf16 *out, const pa_bf16 *query, const pa_bf16 *k
  *                      through block_tables [S][M]; -1 for the others.  A slot whose table
  *                      entry is missing or outside [0, N) is -1 (PA_FLAG_BLOCK_OUT_OF_RANGE).
  *                      Ignored when NULL: block_tables, M, context_lens, bs, N.
- * A sequence with bad offsets or parents is left out as in pa_tree_attention.  Sums are
- * carried in pairs of fp32 (about 48 bits), borders decided in fp64, always in the
- * same order for the same shapes.  V <= 2^30, max_query_len <= min(T, PA_TREE_MAX_NODES).
+ * A sequence with bad offsets or parents is left out as in pa_tree_attention.  Sums,
+ * products and the borders drawn at are carried in pairs of fp32 (about 48 bits), always in
+ * the same order for the same shapes.  V <= 2^30, max_query_len <= min(T, PA_TREE_MAX_NODES).
  */
 pa_status pa_verify_tree(int32_t *tokens_out, int32_t *path, int32_t *n_out, int64_t *slot_mapping,
                          const int32_t *draft_tokens, const void *target_probs,

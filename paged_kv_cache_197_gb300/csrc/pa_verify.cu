@@ -6,16 +6,17 @@
 //   max(max(p - C q, 0) - Z q, 0) = max(p - (C + Z) q, 0),
 // so the state of a node is one number C, a child's test needs p and q at its token alone,
 // and a rejection costs one pass over the vocabulary for Z = sum_v max(p - C q, 0).
-// The weights p - C q and their sums are carried as unevaluated pairs of fp32 (two-term
-// sums and products with their rounding errors): about 48 bits at fp32 rates, where GB300's
-// fp64 lanes (two per SM and clock) would take several times longer than the loads.
+// The weights p - C q, their sums and the borders they are compared with are carried as
+// unevaluated pairs of fp32 (two-term sums and products with their rounding errors): about 48
+// bits at fp32 rates.  GB300 has two fp64 lanes per SM and clock: a pass would take several
+// times longer than its loads, and one choice among 32 sums takes 1230 clocks in fp64.
 //
 // A cluster of CTAs serves a sequence, each CTA a slice of the vocabulary and each warp an
 // equal run of it.  All CTAs walk the tree alike, from the tests' probabilities gathered for
 // all rows at once, and meet only for the sum of a pass: every CTA writes its part into the
 // others' shared memory, one cluster barrier, and each adds the parts in the same order, so
-// all decide the same.  The draw needs no further pass: the run that holds the target's
-// place is scanned by its warp.
+// all decide the same.  The draw needs no further pass: the sums of the last one say which
+// run holds the target's place.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -77,8 +78,14 @@ __device__ __forceinline__ void unpack(const uint4 &w, float (&x)[8]) {
 }
 
 // Four neighbouring entries (4 v aligned to them).
-__device__ __forceinline__ void quad(const float *p, float (&x)[4]) { unpack(__ldg(reinterpret_cast<const uint4 *>(p)), x); }
-__device__ __forceinline__ void quad(const uint16_t *p, float (&x)[4]) {
+__device__ __forceinline__ void quad(const float *p, float *x) {
+    const float4 w = __ldg(reinterpret_cast<const float4 *>(p));
+    x[0] = fmaxf(w.x, 0.f);
+    x[1] = fmaxf(w.y, 0.f);
+    x[2] = fmaxf(w.z, 0.f);
+    x[3] = fmaxf(w.w, 0.f);
+}
+__device__ __forceinline__ void quad(const uint16_t *p, float *x) {
     const uint2 w = __ldg(reinterpret_cast<const uint2 *>(p));
     x[0] = fmaxf(__uint_as_float(w.x << 16), 0.f);
     x[1] = fmaxf(__uint_as_float(w.x & 0xffff0000u), 0.f);
@@ -90,11 +97,6 @@ __device__ __forceinline__ void quad(const uint16_t *p, float (&x)[4]) {
 struct Pair {
     float hi, lo;
 };
-
-__device__ __forceinline__ Pair split(double x) {
-    const float hi = (float)x;
-    return {hi, (float)(x - (double)hi)};
-}
 
 // max(p - C q, 0) as a pair.  C.hi q = h + e exactly (e the product's rounding error), p - h
 // is a two-term difference with its error; C.lo q is below ulp(h) / 2.
@@ -123,7 +125,18 @@ __device__ __forceinline__ void add(Pair &s, Pair x) {
     s.hi = t;
 }
 
-__device__ __forceinline__ double value(Pair x) { return (double)x.hi + (double)x.lo; }
+__device__ __forceinline__ Pair plus(Pair s, Pair x) {
+    add(s, x);
+    return s;
+}
+
+// x y for a single y, and whether a < b (the difference of the leading parts is exact where they
+// are close).
+__device__ __forceinline__ Pair times(Pair x, float y) {
+    const float h = __fmul_rn(x.hi, y);
+    return {h, __fmaf_rn(x.lo, y, __fmaf_rn(x.hi, y, -h))};
+}
+__device__ __forceinline__ bool less(Pair a, Pair b) { return __fadd_rn(__fsub_rn(a.hi, b.hi), __fsub_rn(a.lo, b.lo)) < 0.f; }
 
 // The sum over the first `lanes` (a power of two) lanes' pairs, in each of them.
 __device__ __forceinline__ Pair lanes_sum(Pair s, int lanes) {
@@ -135,13 +148,13 @@ __device__ __forceinline__ Pair lanes_sum(Pair s, int lanes) {
 }
 
 // Inclusive sums over the lanes.
-__device__ __forceinline__ double warp_scan(double x, int lane) {
+__device__ __forceinline__ Pair lanes_scan(Pair s, int lane) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+        const Pair x{__shfl_up_sync(0xffffffffu, s.hi, o), __shfl_up_sync(0xffffffffu, s.lo, o)};
+        if (lane >= o) add(s, x);
     }
-    return x;
+    return s;
 }
 
 // What the first warp asks of all: a pass over the node's residual, or nothing more.
@@ -155,8 +168,7 @@ struct Task {
 struct Shared {
     Pair part[2][kMaxCluster];              // the CTAs' sums of a pass, by its parity
     Pair run[kMaxWarps];                    // the warps' sums of the last pass
-    double from, target;                    // the draw: R's sum before the owner's run, and its place
-    int owner_run;                          // the run of this CTA that holds it, or -1
+    Pair piece[kMaxWarps];                  // the draw: the warps' sums of the run drawn from
     Task task;
     float tp[PA_TREE_MAX_NODES], tq[PA_TREE_MAX_NODES];  // p and q of each row's token at its parent
     int parent[PA_TREE_MAX_NODES], token[PA_TREE_MAX_NODES], place[PA_TREE_MAX_NODES];
@@ -235,76 +247,31 @@ __device__ __forceinline__ Pair run_sum(const Residual<T> &R, int64_t begin, int
     return lanes_sum(s, 32);
 }
 
-// The first v of a warp's run whose running sum, from `at`, exceeds the target; the last v
-// with weight where rounding leaves none; -1 if none has weight.  Groups of 128 entries are
-// summed by the warp, four to a lane, lane g keeping the sum of group g; the group that
-// passes the target is scanned.
+// The sum of R over one lane's [b, e), eight entries at a time; vector: 16-byte loads (b a multiple
+// of 4).
 template <typename T>
-__device__ __forceinline__ int run_find(const Residual<T> &R, int64_t begin, int64_t end, double at, double target, bool vector, int lane) {
-    int64_t group = -1, last_group = -1;  // first entry of the group that passes; of the last with weight
-    double last_at = at;
-    for (int64_t v0 = begin; v0 < end && group < 0; v0 += 32 * 128) {
-        Pair mine{0.f, 0.f};
-        for (int g0 = 0; g0 < 32 && v0 + g0 * 128 < end; g0 += 4) {
-            // four groups' entries are loaded before the first is added up
-            float x[4][4], y[4][4];
+__device__ __forceinline__ Pair piece_sum(const Residual<T> &R, int64_t b, int64_t e, bool vector) {
+    Pair s{0.f, 0.f};
+#pragma unroll 1
+    for (int64_t v = b; v < e; v += 8) {
+        float x[8], y[8];
+        if (vector && v + 8 <= e) {
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int64_t v = v0 + (g0 + g) * 128 + lane * 4;
-                if (vector && v + 4 <= end) {
-                    quad(R.p + v, x[g]);
-                    if (R.q) quad(R.q + v, y[g]);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        x[g][e] = v + e < end ? prob(R.p, v + e) : 0.f;
-                        y[g][e] = R.q && v + e < end ? prob(R.q, v + e) : 0.f;
-                    }
-                }
+            for (int i = 0; i < 8; i += 4) {
+                quad(R.p + v + i, x + i);
+                if (R.q) quad(R.q + v + i, y + i);
             }
+        } else {
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int64_t v = v0 + (g0 + g) * 128 + lane * 4;
-                Pair s{0.f, 0.f};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) add(s, R.weight(v + e, x[g][e], y[g][e]));
-                s = lanes_sum(s, 32);
-                if (lane == g0 + g) mine = s;
+            for (int i = 0; i < 8; ++i) {
+                x[i] = v + i < e ? prob(R.p, v + i) : 0.f;
+                y[i] = R.q && v + i < e ? prob(R.q, v + i) : 0.f;
             }
         }
-        const double w = value(mine), upto = warp_scan(w, lane);
-        const unsigned hit = __ballot_sync(0xffffffffu, w > 0.0 && at + upto > target);
-        const unsigned any = __ballot_sync(0xffffffffu, w > 0.0);
-        if (any) {
-            const int g = hit ? __ffs(hit) - 1 : 31 - __clz(any);
-            const double before = at + __shfl_sync(0xffffffffu, upto - w, g);
-            last_group = v0 + g * 128;
-            last_at = before;
-            if (hit) group = last_group;
-        }
-        at += __shfl_sync(0xffffffffu, upto, 31);
-    }
-    if (last_group < 0) return -1;
-    double w[4], sum = 0.0;
-    const int64_t v = last_group + lane * 4;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        w[e] = v + e < end ? value(R(v + e)) : 0.0;
-        sum += w[e];
+        for (int i = 0; i < 8; ++i) add(s, R.weight(v + i, x[i], y[i]));
     }
-    const double upto = warp_scan(sum, lane);
-    double run = last_at + (upto - sum);
-    int first = 4, last = -1;  // of this lane's entries: the first past the target, the last with weight
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        run += w[e];
-        if (w[e] > 0.0) last = e;
-        if (first == 4 && w[e] > 0.0 && run > target) first = e;
-    }
-    const unsigned hit = __ballot_sync(0xffffffffu, first < 4), any = __ballot_sync(0xffffffffu, last >= 0);
-    const int from = hit ? __ffs(hit) - 1 : 31 - __clz(any);
-    const int e = __shfl_sync(0xffffffffu, hit ? first : last, from);
-    return (int)(last_group + from * 4 + e);
+    return s;
 }
 
 template <typename T, int kThreads>
@@ -356,18 +323,22 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(const
         return;
     }
     const int64_t begin = min((int64_t)a.V, ((int64_t)rank * kWarps + warp) * a.run), end = min((int64_t)a.V, begin + a.run);
-    // ---- the walk, in the first warp (fp64 is scarce: two lanes per SM and clock); the other
-    // warps join it for the passes.  A row is tested after its parent and its older siblings.
+    // ---- the walk, in the first warp; the others join it for the passes.  A row is tested
+    // after its parent and its older siblings.
     int cur = 0, n = 1, rejected = 0, j = 1, pass = 0;
-    double C = 0.0, Z = 1.0, total = 0.0;
+    Pair C{0.f, 0.f}, Z{1.f, 0.f}, total{0.f, 0.f};
     bool fresh = false;  // `total` is of the current residual
     Task task;
+    auto left_at = [&](const Task &t) {
+        return Residual<T>{P + (r0 + t.cur) * a.p_stride, Q && t.rejected > 0 ? Q + (r0 + t.cur) * a.q_stride : nullptr, t.c,
+                           sh.gone, Q ? 0 : t.rejected};
+    };
     for (;;) {
         if (warp == 0) {
             bool need = false;
             if (pass > 0) {  // back from a pass
-                total = value(lanes_sum(lane < a.cluster ? sh.part[(pass - 1) & 1][lane] : Pair{0.f, 0.f}, kMaxCluster));
-                total = __shfl_sync(0xffffffffu, total, 0);
+                total = lanes_sum(lane < a.cluster ? sh.part[(pass - 1) & 1][lane] : Pair{0.f, 0.f}, kMaxCluster);
+                total = {__shfl_sync(0xffffffffu, total.hi, 0), __shfl_sync(0xffffffffu, total.lo, 0)};
                 if (rejected) Z = total;
                 fresh = true;
             }
@@ -385,60 +356,57 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(const
                 j = at + 1;
                 if (at >= L) break;
                 const int x = sh.token[at];
-                const double q = sh.tq[at];
-                double R = sh.tp[at];
+                const float q = sh.tq[at];
+                Pair R{sh.tp[at], 0.f};
                 bool again = false;  // no drafter: the token was rejected before
                 if (Q) {
-                    R = fmax(R - C * q, 0.0);
+                    if (rejected) R = residual(R.hi, q, C);
                 } else {
                     for (int i = 0; i < rejected; ++i) again |= sh.gone[i] == x;
-                    if (again) R = 0.0;
+                    if (again) R.hi = 0.f;
                 }
+                // u Z q: the product of u and q is a pair, so a first child's test is exact
+                const Pair uq = times(Pair{sh.u[at], 0.f}, q), uzq = plus(times(Z, uq.hi), Pair{__fmul_rn(Z.hi, uq.lo), 0.f});
                 const bool inside = x >= 0 && x < a.V;
                 if (!inside && rank == 0 && lane == 0) raise_flag(a.err_flag, PA_FLAG_TOKEN_OUT_OF_RANGE);
-                if (inside && (double)sh.u[at] * Z * q < R) {
+                if (inside && less(uzq, R)) {
                     cur = at;
-                    C = 0.0;
-                    Z = 1.0;
+                    C = {0.f, 0.f};
+                    Z = {1.f, 0.f};
                     rejected = 0;
                     fresh = false;
                     if (lane == 0) sh.place[at] = n;
                     ++n;
                     continue;
                 }
-                C += Z;
+                add(C, Z);
                 __syncwarp();
                 if (!Q && lane == 0) sh.gone[rejected] = x;
                 __syncwarp();
                 ++rejected;
                 // Without a drafter the mass after the first rejection falls by what is
                 // rejected: no pass while the difference keeps its digits.
-                const double less = Z - R;
-                if (!Q && rejected > 1 && less > 1e-6) {
-                    Z = less;
+                const Pair rest = plus(Z, Pair{-R.hi, 0.f});
+                if (!Q && rejected > 1 && rest.hi > 1e-6f) {
+                    Z = rest;
                     fresh = again && fresh;
                 } else {
                     need = true;
                 }
             }
             if (!need && !fresh) need = true;  // the draw needs the sums
-            if (!need && rejected && !(total > 0.0)) {
+            if (!need && rejected && !(total.hi > 0.f)) {
                 // nothing left: the target's own row
                 rejected = 0;
-                C = 0.0;
+                C = {0.f, 0.f};
                 need = true;
             }
-            if (lane == 0) sh.task = Task{cur, rejected, split(C), need, n};
+            if (lane == 0) sh.task = Task{cur, rejected, C, need, n};
         }
         __syncthreads();
         task = sh.task;
         if (!task.more) break;
-        Residual<T> R;
-        R.p = P + (r0 + task.cur) * a.p_stride;
-        R.q = Q && task.rejected > 0 ? Q + (r0 + task.cur) * a.q_stride : nullptr;
-        R.c = task.c;
-        R.gone = sh.gone;
-        R.n_gone = Q ? 0 : task.rejected;
+        const Residual<T> R = left_at(task);
         const Pair d = !R.q ? run_sum<T, 0>(R, begin, end, a.vector != 0, lane)
                        : R.c.hi == 1.f && R.c.lo == 0.f ? run_sum<T, 1>(R, begin, end, a.vector != 0, lane)
                                                         : run_sum<T, 2>(R, begin, end, a.vector != 0, lane);
@@ -458,48 +426,70 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(const
             __syncthreads();
         ++pass;
     }
-    // ---- the draw: the first v whose running sum of R exceeds u total
-    if (warp == 0) {
-        const bool drawn = total > 0.0 && total <= 1.7e308;
-        int owner_run = -1;
-        double from = 0.0, target = 0.0;
-        if (!drawn) {
-            if (rank == 0 && lane == 0) {
-                raise_flag(a.err_flag, PA_FLAG_PROBABILITY);
-                tokens_out[n - 1] = -1;
-            }
-        } else {
-            target = (double)a.u_final[s] * total;
-            // first of the CTAs' parts, then of this CTA's runs; past all of them (numbers of 1
-            // or more, rounding) the last with weight
-            const double w = lane < a.cluster ? value(sh.part[(pass - 1) & 1][lane]) : 0.0, upto = warp_scan(w, lane);
-            const unsigned hit = __ballot_sync(0xffffffffu, w > 0.0 && upto > target), any = __ballot_sync(0xffffffffu, w > 0.0);
-            const int owner = hit ? __ffs(hit) - 1 : 31 - __clz(any);
-            if (owner == rank) {
-                const double start = __shfl_sync(0xffffffffu, upto - w, owner);
-                const double r = lane < kWarps ? value(sh.run[lane]) : 0.0, to = start + warp_scan(r, lane);
-                const unsigned h = __ballot_sync(0xffffffffu, r > 0.0 && to > target), y = __ballot_sync(0xffffffffu, r > 0.0);
-                owner_run = h ? __ffs(h) - 1 : 31 - __clz(y);
-                from = __shfl_sync(0xffffffffu, to - r, owner_run);
-            }
-        }
-        if (lane == 0) {
-            sh.owner_run = owner_run;
-            sh.from = from;
-            sh.target = target;
-        }
-    }
-    __syncthreads();
+    // ---- the draw: the first v whose running sum of R exceeds u total; past all of them (numbers
+    // of 1 or more, rounding) the last with weight.  It is narrowed down to a CTA, one of its runs,
+    // a warp's and a lane's piece of that run (the CTA sums all of them at once), and parts of that
+    // piece.  (One loop: most of a draw is latency and fetching its instructions, met once a
+    // launch.  One warp that scanned the run, in fp64, took 12000 to 20000 clocks.)
     n = task.n;
-    if (warp == sh.owner_run) {
-        Residual<T> R;
-        R.p = P + (r0 + task.cur) * a.p_stride;
-        R.q = Q && task.rejected > 0 ? Q + (r0 + task.cur) * a.q_stride : nullptr;
-        R.c = task.c;
-        R.gone = sh.gone;
-        R.n_gone = Q ? 0 : task.rejected;
-        const int v = run_find(R, begin, end, sh.from, sh.target, a.vector != 0, lane);
-        if (lane == 0) tokens_out[n - 1] = v;
+    {
+        const Residual<T> R = left_at(task);
+        Pair before{0.f, 0.f}, target{0.f, 0.f}, own{0.f, 0.f};  // R's sum before what is left; its place; a thread's piece
+        int64_t lo = 0, hi = a.V, threads_piece = 0;
+#pragma unroll 1
+        for (int level = 0;; ++level) {
+            int64_t piece;
+            Pair mine{0.f, 0.f};
+            if (level == 0) {
+                piece = (int64_t)a.run * kWarps;
+                if (lane < a.cluster) mine = sh.part[(pass - 1) & 1][lane];
+            } else if (level == 1) {
+                piece = a.run;
+                if (lane < kWarps) mine = sh.run[lane];
+            } else if (level == 3) {
+                piece = threads_piece;
+                mine = own;
+            } else {
+                const int64_t len = hi - lo, parts = level == 2 ? kThreads : 32;
+                const bool quads = a.vector && len >= 4 * parts;  // (lo stays a multiple of 4)
+                piece = quads ? (len + 4 * parts - 1) / (4 * parts) * 4 : (len + parts - 1) / parts;
+                const int64_t b = min(hi, lo + (level == 2 ? tid : lane) * piece);
+                mine = piece_sum(R, b, min(hi, b + piece), quads);
+                if (level == 2) {
+                    own = mine;
+                    threads_piece = piece;
+                    piece *= 32;
+                    mine = lanes_sum(mine, 32);
+                    if (lane == 0) sh.piece[warp] = mine;
+                    __syncthreads();
+                    mine = lane < kWarps ? sh.piece[lane] : Pair{0.f, 0.f};
+                }
+            }
+            const Pair upto = lanes_scan(mine, lane);
+            if (level == 0) {
+                const float all = __shfl_sync(0xffffffffu, upto.hi, 31);
+                if (!(all > 0.f && all <= 3.402823466e38f)) {
+                    if (rank == 0 && tid == 0) {
+                        raise_flag(a.err_flag, PA_FLAG_PROBABILITY);
+                        tokens_out[n - 1] = -1;
+                    }
+                    break;
+                }
+                target = times(Pair{all, __shfl_sync(0xffffffffu, upto.lo, 31)}, a.u_final[s]);
+            }
+            const unsigned any = __ballot_sync(0xffffffffu, mine.hi > 0.f);
+            const unsigned hit = __ballot_sync(0xffffffffu, mine.hi > 0.f && less(target, plus(before, upto)));
+            const int at = hit ? __ffs(hit) - 1 : 31 - __clz(any);
+            if (at != (level == 0 ? rank : level == 2 ? warp : at)) break;
+            const Pair up{__shfl_sync(0xffffffffu, upto.hi, max(at - 1, 0)), __shfl_sync(0xffffffffu, upto.lo, max(at - 1, 0))};
+            if (at > 0) add(before, up);
+            lo += at * piece;
+            hi = min(hi, lo + piece);
+            if (hi - lo <= 1 && level != 1) {
+                if (lane == 0 && (level > 1 || warp == 0)) tokens_out[n - 1] = (int)lo;
+                break;
+            }
+        }
     }
     // ---- the branch
     if (rank != 0) return;
