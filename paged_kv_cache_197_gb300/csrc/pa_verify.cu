@@ -192,9 +192,6 @@ struct Residual {
             if (gone[i] == (int)v) return {0.f, 0.f};
         return {x, 0.f};
     }
-    __device__ __forceinline__ Pair operator()(int64_t v) const {
-        return weight(v, prob(p, v), q ? prob(q, v) : 0.f);
-    }
 };
 
 // The sum of R over a warp's run [begin, end).  DRAFTED: 0 = p alone, 1 = p - q, 2 = p - C q.
@@ -229,21 +226,30 @@ __device__ __forceinline__ Pair run_sum(const Residual<T> &R, int64_t begin, int
             }
         }
     }
-    if (plain) {
-        constexpr int U = 8;
-        for (; v + 32 * U <= end; v += 32 * U) {
-            float x[U], y[U];
+    // what is left of the run, or all of it; entries behind the run count as 0
+    constexpr int U = 8;
+    for (; v < end; v += 32 * U) {
+        float x[U], y[U];
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-                x[i] = prob(R.p, v + i * 32 + lane);
-                if (DRAFTED) y[i] = prob(R.q, v + i * 32 + lane);
-            }
+        for (int i = 0; i < U; ++i) {
+            const int64_t at = v + i * 32 + lane;
+            x[i] = at < end ? prob(R.p, at) : 0.f;
+            y[i] = DRAFTED && at < end ? prob(R.q, at) : 0.f;
+        }
+        if (plain) {
 #pragma unroll
             for (int i = 0; i < U; ++i)
                 add(s, DRAFTED == 2 ? residual(x[i], y[i], R.c) : DRAFTED == 1 ? residual(x[i], y[i]) : Pair{x[i], 0.f});
+        } else {
+#pragma unroll 1
+            for (int i = 0; i < U; ++i) {
+                float xi = x[0];
+#pragma unroll
+                for (int k = 1; k < U; ++k) xi = i == k ? x[k] : xi;
+                add(s, R.weight(v + i * 32 + lane, xi, 0.f));
+            }
         }
     }
-    for (v += lane; v < end; v += 32) add(s, R(v));
     return lanes_sum(s, 32);
 }
 
