@@ -148,13 +148,6 @@ __device__ __forceinline__ void tma_block(uint32_t dst, const CUtensorMap *map, 
         : "memory");
 }
 
-// Plain bytes, 16-byte aligned on both sides.
-__device__ __forceinline__ void bulk_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(src), "r"(bytes), "r"(bar)
-                 : "memory");
-}
-
 // Eight floats, one 32-byte sector.
 __device__ __forceinline__ void store8(float *p, const float *v) {
     asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
@@ -255,7 +248,7 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
     if (warp == 1) {
         for (int i = lane; i < kFull; i += 32) mbar_init_n(tc_smem(&sh.full[i]), QUANT ? 128 : 1);
         for (int i = lane; i < kFull; i += 32) mbar_init_n(tc_smem(&sh.free[i]), SPLIT ? 1 : 2);  // lanes that read a stage
-        for (int i = lane; i < G::kRawFull; i += 32) mbar_init(tc_smem(&sh.raw_full[i]));
+        for (int i = lane; i < G::kRawFull; i += 32) mbar_init_n(tc_smem(&sh.raw_full[i]), 33);  // codes, each lane's scales
         for (int i = lane; i < G::kRaw; i += 32) mbar_init_n(tc_smem(&sh.raw_free[i]), 128);
         if (QUANT && lane < 2 * kScaleSlots) mbar_init_n(tc_smem(&sh.units[lane]), 2);
         if (QUANT && lane < kScaleSlots) mbar_init_n(tc_smem(&sh.units_free[lane]), SPLIT ? kLaneCols : 2 * kLaneCols);
@@ -373,17 +366,16 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
             const CUtensorMap *map = is_k ? &kmap : &vmap;
             if constexpr (QUANT) {
                 const uint32_t bar = tc_smem(&sh.raw_full[issued % (QUANT ? G::kRawFull : 1)]);
-                const bool scaled = lane < kBlocks && b >= 0;
-                const int blocks = __popc(__ballot_sync(0xffffffffu, scaled));
-                float *slot = sh.raw_scale[st] + (lane < kBlocks ? lane : 0) * BS;
-                if (lane < kBlocks && b < 0)
-#pragma unroll
-                    for (int i = 0; i < BS; i += 4) *reinterpret_cast<float4 *>(slot + i) = make_float4(0.f, 0.f, 0.f, 0.f);
-                __syncwarp();
-                if (lane == 0) mbar_expect(bar, kRawBytes + blocks * BS * 4);
+                if (lane == 0) mbar_expect(bar, kRawBytes);
                 __syncwarp();
                 if (lane < kBlocks) tma_load(box + st * kRawBytes, map, 0, y, bar);
-                if (scaled) bulk_copy(tc_smem(slot), (is_k ? a.k_scale : a.v_scale) + ((int64_t)b * a.Hkv + u.kvh) * BS, BS * 4, bar);
+                __syncwarp();
+                // the scales, four tokens a lane in one instruction (a bulk copy per block:
+                // 128.1 instead of 127.5 us for the fp8 batch)
+                const int from = __shfl_sync(0xffffffffu, b, 4 * lane / BS);
+                const float *scale = (is_k ? a.k_scale : a.v_scale) + ((int64_t)max(from, 0) * a.Hkv + u.kvh) * BS + 4 * lane % BS;
+                tiled::cp_async16(tc_smem(sh.raw_scale[st] + 4 * lane), scale, from >= 0 ? 16 : 0);
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
             } else {
                 const uint32_t bar = tc_smem(&sh.full[issued % kFull]);
                 if (lane == 0) mbar_expect(bar, kTileBytes);
