@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 32 / kJoinWarps) tree_join_ke
         const int64_t tiles = (ctx + kTreeTile - 1) / kTreeTile, total = c.prefix[a.S];
         n = 0;
         if (tiles > 0) {
-            const int64_t first = c.prefix[s] + kvh * tree_unit_len(tiles) + kTreePad, groups = min((int64_t)c.groups, total);
+            const int64_t first = c.prefix[s] + kvh * tree_unit_len(tiles, c.cols) + tree_pad(c.cols), groups = min((int64_t)c.groups, total);
             const int64_t g0 = tree_group_of(first, total, groups), g1 = tree_group_of(first + tiles - 1, total, groups);
             n = (int)(g1 - g0) + 1;
             if (n == 1) {

@@ -163,7 +163,8 @@ struct Unit {
     int s, kvh, t0, n, tiles, ctx, r0, ncols;
 };
 
-// The units of a CTA's share, in order.
+// The units of a CTA's share, in order; COLS columns to a CTA.
+template <int COLS>
 struct Walk {
     int64_t pos, end, before;  // positions: here, end of the share, before sequence s
     int s, tiles;              // sequence and its tiles per kv head (-1: not read yet)
@@ -179,7 +180,7 @@ struct Walk {
                 ncols = L * a.G;
                 tiles = r0 >= 0 && r1 <= a.T && L >= 1 && L <= a.max_query_len ? (ctx + kTile - 1) / kTile : 0;
             }
-            const int64_t len = tree_unit_len(tiles);
+            const int64_t len = tree_unit_len(tiles, COLS);
             if (pos >= before + len * a.Hkv) {
                 before += len * a.Hkv;
                 ++s;
@@ -195,8 +196,8 @@ struct Walk {
             const int64_t step = min(len - off, end - pos);
             pos += step;
             u.s = s;
-            u.t0 = max(0, off - kTreePad);
-            u.n = (int)(off + step) - kTreePad - u.t0;
+            u.t0 = max(0, off - tree_pad(COLS));
+            u.n = (int)(off + step) - tree_pad(COLS) - u.t0;
             u.tiles = tiles;
             u.ctx = ctx;
             u.r0 = r0;
@@ -235,6 +236,7 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                const __grid_constant__ CUtensorMap vmap) {
     using G = Geo<KV, SPLIT>;
     constexpr bool QUANT = G::kQuant;
+    constexpr int kCols = SPLIT ? kLaneCols : 2 * kLaneCols;
     constexpr int kThreads = G::kThreads, kStages = G::kStages, kFull = G::kFull;
     static_assert(G::kOffShared + sizeof(Shared<G>) <= 232448, "shared memory of one CTA per SM");
     extern __shared__ __align__(1024) unsigned char smem[];
@@ -284,7 +286,7 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
         const bool ok = r0 >= 0 && r1 <= a.T && L >= 0 && L <= a.max_query_len;
         if (report && (ctx < 0 || ctx > lim)) raise_flag(a.err_flag, PA_FLAG_CONTEXT_OUT_OF_RANGE);
         if (report && !ok) raise_flag(a.err_flag, PA_FLAG_QUERY_OUT_OF_RANGE);
-        return ok && L > 0 ? (int)tree_unit_len((min(max(ctx, 0), lim) + kTile - 1) / kTile) : 0;
+        return ok && L > 0 ? (int)tree_unit_len((min(max(ctx, 0), lim) + kTile - 1) / kTile, kCols) : 0;
     };
     const int n_first = tid < a.S ? len_of(tid, blockIdx.x == 0) : 0;
     int64_t sum = n_first;
@@ -327,7 +329,7 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.taddr;
-    Walk w{begin, end, sh.first_tile, sh.first_seq, -1, 0, 0, 0};
+    Walk<kCols> w{begin, end, sh.first_tile, sh.first_seq, -1, 0, 0, 0};
     int *abort = &sh.abort;
 
     // lane 1 has work: its half of the columns, or (lanes on the same columns) a second tile
