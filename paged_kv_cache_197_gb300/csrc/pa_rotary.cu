@@ -19,7 +19,7 @@
 namespace pa {
 namespace {
 
-// Tokens per CTA, and rows a thread has in flight: 8192 tokens take 56.3 us (4 tokens 59.4, 8
+// Tokens per CTA; a thread has kBatch rows in flight, four or (layout 2) one: 8192 tokens take 56.3 us (4 tokens 59.4, 8
 // tokens 69.8; 1 token 56.4; two rows in flight 56.8).
 constexpr int kTokens = 2;
 constexpr int kThreadsPerToken = 64;
@@ -70,9 +70,10 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], float scale) {
         if constexpr (KV == PA_KV_FP8) {
             two = __nv_cvt_float2_to_fp8x2(make_float2(u, w), __NV_SATFINITE, __NV_E4M3);
         } else {
-            const int i0 = (int)fminf(fmaxf(rintf(u), -127.f), 127.f);
-            const int i1 = (int)fminf(fmaxf(rintf(w), -127.f), 127.f);
-            two = (i0 & 0xff) | ((uint32_t)(i1 & 0xff) << 8);
+            // The sum with 1.5 x 2^23 rounds to an integer, ties to even, and leaves it in the low
+            // bits (float-to-int conversions took 2.4 us more for 6000 tokens).
+            const float i0 = __fadd_rn(fminf(fmaxf(u, -127.f), 127.f), 12582912.f), i1 = __fadd_rn(fminf(fmaxf(w, -127.f), 127.f), 12582912.f);
+            two = (__float_as_uint(i0) & 0xffu) | ((__float_as_uint(i1) & 0xffu) << 8);
         }
         code[e / 4] |= two << (8 * (e & 2));
     }
@@ -84,15 +85,17 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], float scale) {
 // sines serve all the rows it visits.
 // LAYOUT: 0 = half (rot_dim / 2 a multiple of 8: pieces c and c + rot_dim / 16, the rest of
 // the head in the other lanes), 1 = interleaved (neighbouring pieces), 2 = half with any
-// other rot_dim (neighbouring pieces, partners read one by one).
+// other rot_dim (neighbouring pieces, partners read again from L1, by words where they align).
 // Bounds: HBM beyond a few hundred tokens.  8192 tokens of 64 + 8 + 8 heads, 336 MB, 56.3 us:
 // 5.97 TB/s, 0.88 of the measured copy rate.  (66.5 us with one piece a lane and partners
-// through shuffles, when the instructions were most of the time.)
+// through shuffles, when the instructions were most of the time.)  Layout 2 is bound by its
+// partners' loads: 6000 tokens of these heads with rot_dim 20 take 60.1 us, interleaved 41.5 (two
+// bytes at a time and two rows in flight, in more registers, 97.6).
 template <int D, int KV, int LAYOUT>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryArgs a) {
     constexpr int LPR = D / 16;                      // lanes per row
     constexpr int SLOTS = kThreadsPerToken / LPR;    // rows of a token at once
-    constexpr int kBatch = LAYOUT == 2 ? 2 : 4;      // rows a thread has in flight
+    constexpr int kBatch = LAYOUT == 2 ? 1 : 4;
     __shared__ float2 s_cs[kTokens][D / 2];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -215,6 +218,16 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
                 raw[b][0] = *reinterpret_cast<const uint4 *>(src + b * SLOTS * D + 8 * p0);
                 raw[b][1] = *reinterpret_cast<const uint4 *>(src + b * SLOTS * D + 8 * p1);
                 if constexpr (LAYOUT == 2 && KIND < 2) {
+                    if (half % 2 == 0) {  // two partners to a word
+#pragma unroll
+                        for (int e = 0; e < 16; e += 2) {
+                            const int i = 16 * c + e;
+                            const uint32_t w = i < a.rot ? *reinterpret_cast<const uint32_t *>(src + b * SLOTS * D + (i < half ? i + half : i - half)) : 0u;
+                            part[b][e] = __uint_as_float(w << 16);
+                            part[b][e + 1] = __uint_as_float(w & 0xffff0000u);
+                        }
+                        continue;
+                    }
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const int i = 16 * c + e;
