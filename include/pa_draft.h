@@ -136,7 +136,7 @@ size_t pa_tree_workspace_size(int S, int T, int Hq, int Hkv, int D, int bs, int 
  * below its row (PA_FLAG_TREE_PARENT): its rows of out are not written.  Other arguments,
  * cache types and device-side checks as in pa_multi_token_attention.  Scores, softmax
  * statistics and weighted sums are fp32, the weights of cached tokens bf16 (fp16 with 8-bit
- * caches); the result is rounded once to bf16.  Entries of an 8-bit cache with D = 128 are
+ * caches); the result is rounded once to bf16.  Values of an 8-bit cache with D = 128 are
  * taken as fp16(code * fp16(scale)), within 2^-10 of code * scale, or 2^-31 of the largest
  * scale of the 128 tokens they are read with where that is more.
  */

@@ -21,15 +21,14 @@
 //     turn those of K, warps 16-19 those of V into fp16 in the stages the products read.
 // Tensor memory: S of the lanes at columns 0 and 128 (overwritten by P as 16-bit pairs, the A
 // operand of P V), O at 256 and 384.
-// 8-bit caches: an entry is code x scale in fp16, in units of a power of two per tile (2^e,
-// the tile's largest scale below 2^7 of them, so entries below 448 x 128), the scale rounded
-// to fp16 and the product once more (2^-11 each; scales to 2^-20 of the tile's largest keep
-// all their bits, and what is below 2^-31 of it is lost); the query rows
-// are fp16 scaled by a power of two each (exact).  The columns take both powers into their
-// score factor, and keep the base m above the scores plus the values' e: a weight p 2^e
-// stays below 2^8 whatever the scales.  Scales in fp32 per element instead, on the scores and
-// on the weights, were slower: 261 us for the fp8 batch of 64 sequences of 128 to 4096
-// tokens and 9 to 16 rows, bound by the columns' reads of the scales.
+// 8-bit caches: K's codes are exact in fp16, and a score is multiplied by its token's scale in
+// fp32 (fp16 of code x scale would put scores of a few hundred off by a tenth and more; it
+// saved 14 us of 142 for the fp8 batch).  A value is code x scale in fp16, in units of a power of two per tile (2^e, the
+// tile's largest scale below 2^7 of them, so entries below 448 x 128), the scale rounded to
+// fp16 and the product once more (2^-11 each; scales to 2^-20 of the tile's largest keep all
+// their bits, and what is below 2^-31 of it is lost).  The query rows are fp16 scaled by a power
+// of two each (exact), which the columns take into their score factor; and they keep the base m
+// above the scores plus the values' e: a weight p 2^e stays below 2^8 whatever the scales.
 // Bounds: up to 128 columns, or 256 shared ones, the 64 KB of a bf16 K and V tile take 2800 SM
 // clocks at the measured HBM rate and the products 1024 / 2048, so HBM bounds; more columns
 // reread the tiles through L2 and the products bound.
@@ -92,11 +91,12 @@ template <typename G>
 struct Shared {
     float2 ml[2][kLaneCols];                    // lanes joined: each one's (base, sum) per column
     float raw_scale[G::kQuant ? G::kRaw : 1][G::kQuant ? kTile : 4];  // scales of the codes' stages
-    float2 unit[kScaleSlots];                   // tiles' powers of two, as exponents: K's and V's
+    float unit[kScaleSlots];                    // tiles' powers of two for V, as exponents
+    float k_scale[G::kQuant ? kScaleSlots : 1][G::kQuant ? kTile : 4];  // tiles' scales of K
     float rs[2][G::kQuant ? kLaneCols : 1];     // columns' score factors, by query buffer
     uint64_t full[G::kFull], free[G::kFull];    // ring positions landed / consumed
     uint64_t raw_full[G::kQuant ? G::kRawFull : 1], raw_free[G::kQuant ? G::kRaw : 1];
-    uint64_t units[2 * kScaleSlots], units_free[kScaleSlots];  // of the powers: both in / read
+    uint64_t units[2 * kScaleSlots], units_free[kScaleSlots];  // of unit and k_scale: both in / read
     uint64_t sfull[2], pfull[2], odone[2];      // per lane: S written, P written, P V done
     uint64_t qfull[2];                          // query buffers staged
     uint64_t mlready, oread;                    // lanes joined: both (base, sum) and O in / read
@@ -208,11 +208,12 @@ struct Walk {
     }
 };
 
-// Sixteen codes of one row times a scale, as sixteen fp16 (two 16-byte words).
+// Sixteen codes of one row, times a scale if scaled, as sixteen fp16 (two 16-byte words).
 template <typename KV>
-__device__ __forceinline__ void scaled_f16(const uint4 &c, __half2 scale, uint4 &lo, uint4 &hi) {
+__device__ __forceinline__ void scaled_f16(const uint4 &c, bool scaled, __half2 scale, uint4 &lo, uint4 &hi) {
     if constexpr (sizeof(KV) == 1) {
         tiled::codes_to_f16_exact<KV>(c, lo, hi);
+        if (!scaled) return;
         uint32_t *w[8] = {&lo.x, &lo.y, &lo.z, &lo.w, &hi.x, &hi.y, &hi.z, &hi.w};
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -252,7 +253,7 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
         for (int i = lane; i < kFull; i += 32) mbar_init_n(tc_smem(&sh.free[i]), SPLIT ? 1 : 2);  // lanes that read a stage
         for (int i = lane; i < G::kRawFull; i += 32) mbar_init_n(tc_smem(&sh.raw_full[i]), 33);  // codes, each lane's scales
         for (int i = lane; i < G::kRaw; i += 32) mbar_init_n(tc_smem(&sh.raw_free[i]), 128);
-        if (QUANT && lane < 2 * kScaleSlots) mbar_init_n(tc_smem(&sh.units[lane]), 2);
+        if (QUANT && lane < 2 * kScaleSlots) mbar_init_n(tc_smem(&sh.units[lane]), 129);  // K's group, V's first thread
         if (QUANT && lane < kScaleSlots) mbar_init_n(tc_smem(&sh.units_free[lane]), SPLIT ? kLaneCols : 2 * kLaneCols);
         if (lane < 2) {
             mbar_init(tc_smem(&sh.sfull[lane]));
@@ -563,13 +564,17 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                 const float top = fmaxf(fmaxf(4 * lane < left ? fabsf(s4.x) : 0.f, 4 * lane + 1 < left ? fabsf(s4.y) : 0.f),
                                         fmaxf(4 * lane + 2 < left ? fabsf(s4.z) : 0.f, 4 * lane + 3 < left ? fabsf(s4.w) : 0.f));
                 const int e = exponent_over(__reduce_max_sync(0xffffffffu, __float_as_uint(top))) - kScaleTop;
-                const float down = __uint_as_float((uint32_t)(127 - e) << 23);  // 2^-e
-                if (me == 0) {
+                const float down = is_k ? 1.f : __uint_as_float((uint32_t)(127 - e) << 23);  // 2^-e
+                if (is_k || me == 0) {
                     // the lanes have read this slot's last tile
                     if (j >= kScaleSlots) ok = wait_for(&sh.units_free[j % kScaleSlots], (j / kScaleSlots - 1) & 1, abort);
-                    (is_k ? sh.unit[j % kScaleSlots].x : sh.unit[j % kScaleSlots].y) = (float)e;
+                    if (is_k)
+                        sh.k_scale[j % kScaleSlots][me] = scale[me];
+                    else
+                        sh.unit[j % kScaleSlots] = (float)e;
                     mbar_arrive(tc_smem(&sh.units[j % (2 * kScaleSlots)]));
                 }
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 // this thread's piece c of rows r0, r0 + 16, ..: two 8-value chunks each.  Eight
                 // lanes take the same half of rows r and r ^ 5: both tiles are swizzled by the
                 // row's low three bits, codes in pieces (the two rows' halves then lie apart: bit
@@ -600,7 +605,7 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                     }
 #pragma unroll
                     for (int k = 0; k < kAtOnce; ++k) {
-                        scaled_f16<KV>(code[k], __float2half2_rn(sc[k]), lo, hi);
+                        scaled_f16<KV>(code[k], !is_k, __float2half2_rn(sc[k]), lo, hi);
                         *reinterpret_cast<uint4 *>(to0 + k * 2 * kGroup) = lo;
                         *reinterpret_cast<uint4 *>(to1 + k * 2 * kGroup) = hi;
                     }
@@ -729,11 +734,21 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                 if (!idle) {
                     const int left = u.ctx - k0;  // tokens of the context from the tile on
                     float factor = rs, over = 0.f;  // of the scores; exponent of the values' unit
-                    if constexpr (QUANT) {
-                        const float2 unit = sh.unit[j % kScaleSlots];
-                        factor = rs * __uint_as_float((uint32_t)(127 + (int)unit.x) << 23);
-                        over = unit.y;
-                    }
+                    if constexpr (QUANT) over = sh.unit[j % kScaleSlots];
+                    // 8-bit caches: 32 scores of codes times their tokens' scales
+                    auto scaled = [&](float (&x)[32], int q) {
+                        if constexpr (QUANT) {
+                            const float4 *ks = reinterpret_cast<const float4 *>(sh.k_scale[j % kScaleSlots]) + 8 * q;
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const float4 w = ks[k];
+                                x[4 * k] *= w.x;
+                                x[4 * k + 1] *= w.y;
+                                x[4 * k + 2] *= w.z;
+                                x[4 * k + 3] *= w.w;
+                            }
+                        }
+                    };
                     if (left < kTile) factor = fmaxf(factor, kTiny);
                     // The scores are read twice, for the maximum and for the weights, 64 and 32 at a
                     // time, in loops that stay loops: all 128 in registers spilled, and code
@@ -746,6 +761,7 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                         float sv[32];
                         tmem_ld32(t_s + 32 * h, sv);
                         tmem_wait_ld();
+                        scaled(sv, h);
                         if (left < kTile) {
 #pragma unroll
                             for (int k = 0; k < 32; ++k)
@@ -812,6 +828,7 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                         float x[32];
                         tmem_ld32(t_s + 32 * q, x);
                         tmem_wait_ld();
+                        scaled(x, q);
                         weigh(x, q);
                     }
                     const float sum = (ls[0] + ls[1]) + (ls[2] + ls[3]);

@@ -26,10 +26,11 @@ def rotated(x, positions, inv_freq, interleaved, factor):
 
 
 # ------------------------------------------------------------------------------ tree
-def tree_attention(q, k, v, k_cache, v_cache, k_scale, v_scale, tables, lens, starts, parents, scale, entries=0.0):
-    """(out, spread, taken): the attention, sum_t w_t |v_t|, and what cached keys and values off by
-    `entries` relative, or 2^-31 of the cache's largest scale, may change, all [T][Hq][D] fp64 (NaN in
-    rows of no sequence)."""
+def tree_attention(q, k, v, k_cache, v_cache, k_scale, v_scale, tables, lens, starts, parents, scale, values=0.0, sums=0.0,
+                   small=0.0):
+    """(out, spread, taken): the attention, sum_t w_t |v_t|, and what cached values off by `values`
+    relative, or 2^-31 of the cache's largest scale, scores off by `sums` times scale * sum |q||k|, and
+    weights of cached tokens off by `small`, or lost, may change, all [T][Hq][D] fp64 (NaN in rows of no sequence)."""
     q, k, v = (t.double().cpu() for t in (q, k, v))
     T, Hq, D = q.shape
     Hkv, bs = k_cache.shape[1], k_cache.shape[2]
@@ -64,17 +65,18 @@ def tree_attention(q, k, v, k_cache, v_cache, k_scale, v_scale, tables, lens, st
             w = torch.softmax((q[a:b, h] @ kk[h // G].T * scale).masked_fill(~mask, -math.inf), -1)
             out[a:b, h] = w @ vv[h // G]
             spread[a:b, h] = w @ vv[h // G].abs()
-            if entries and n:
+            if values and n:
+                vc = vv[h // G][:n].abs() * values + 2.0 ** -31 * _largest(v_scale, tables, lens)
+                taken[a:b, h] += w[:, :n] @ vc
+            taken[a:b, h] += w[:, :n].clamp(max=small) @ vv[h // G][:n].abs()
+            if sums:
                 # Scores off by e_t change a weight's logarithm by at most e_t + log sum w exp(e), which
                 # is at most e_t + E' exp(E) with E' = sum w e, E = max e; so the weight by at most
                 # w_t (e_t + E') exp(4 E) while E is below 0.2.
-                kc, vc = (x[h // G][:n].abs() * entries + 2.0 ** -31 * float(top) for x, top in (
-                    (kk, _largest(k_scale, tables, lens)), (vv, _largest(v_scale, tables, lens))))
-                e = torch.zeros(L, n + L, dtype=torch.float64)
-                e[:, :n] = abs(scale) * (q[a:b, h].abs() @ kc.T)
+                e = sums * abs(scale) * (q[a:b, h].abs() @ kk[h // G].abs().T)
                 assert e.max() < 0.2
                 mean, grow = (w * e).sum(-1, keepdim=True), torch.exp(4 * e.amax(-1, keepdim=True))
-                taken[a:b, h] = grow * ((w * (e + mean)) @ vv[h // G].abs() + w[:, :n] @ vc)
+                taken[a:b, h] += grow * ((w * (e + mean)) @ vv[h // G].abs())
     return out, spread, taken
 
 

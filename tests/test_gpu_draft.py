@@ -259,19 +259,21 @@ def _tree_reference(c):
     return _tree_taken(c)[:2]
 
 
-def _tree_taken(c, entries=0.0):
+def _tree_taken(c, values=0.0, sums=0.0, small=0.0):
     return ref.tree_attention(c["q"], c["k"], c["v"], c["cache"]["k_cache"], c["cache"]["v_cache"], c["cache"].get("k_scale"),
-                              c["cache"].get("v_scale"), c["tables"], c["lens"], c["starts"], c["parents"], c["scale"], entries)
+                              c["cache"].get("v_scale"), c["tables"], c["lens"], c["starts"], c["parents"], c["scale"], values, sums, small)
 
 
-def _tree_check(out, c):
+def _tree_check(out, c, sums=0.0, small=0.0):
     """The output is rounded to bf16 once (2^-8 of it), and each softmax weight once, to bf16 or fp16,
     before its product with v (2^-8 of sum w |v|; the sum of the weights takes them unrounded).
     Scores, exponentials and sums in fp32: |score| below 2^5 here, off by a few 2^-24 of it, is below
     2^-16 of a weight, ex2.approx 2^-22; together under 2^-12 of sum w |v|.  8-bit caches, heads of
-    128: an entry is off by 2^-11 for its scale's rounding and 2^-11 for its own (fp16)."""
+    128: a value is off by 2^-11 for its scale's rounding and 2^-11 for its own (fp16).  sums: for larger
+    scores, their error in units of scale * sum |q||k|, and small:
+    what fp16 weights far below the largest are off by."""
     quant = "k_scale" in c["cache"] and c["q"].shape[2] == 128
-    want, spread, taken = _tree_taken(c, 2.0 ** -10 * (1 + 2.0 ** -11) if quant else 0.0)
+    want, spread, taken = _tree_taken(c, 2.0 ** -10 * (1 + 2.0 ** -11) if quant else 0.0, sums, small)
     got = out.double().cpu()
     none = torch.isnan(want)
     assert torch.isnan(got[none]).all()  # rows of no sequence are not written
@@ -352,6 +354,21 @@ def test_tree_scales_of_all_sizes(pa, kv, D):
         t *= (2.0 ** torch.randint(-18, 1, t.shape, generator=g)).to(DEV)
         t *= (torch.randint(0, 5, t.shape, generator=g) - 1).sign().to(DEV)
     _tree_check(_tree_call(pa, c), c)
+
+
+@pytest.mark.parametrize("D", [128, 64])
+@pytest.mark.parametrize("kv", ["int8", "fp8"])
+def test_tree_scores_of_hundreds(pa, kv, D):
+    """Keys up to 64 times as large as usual, token by token: scores of a few hundred, whose rounding shows
+    in the weights.  A score is a sum of D products in fp32, in any order, D 2^-24 of sum |q||k|, and
+    four more roundings (its token's scale, the row's factor, the exponent, and the key's own in the plain
+    row); a rounding of the keys to 11 bits, 2^-12 at a time, would be ten times that.  fp16 weights below
+    2^-14 have steps of 2^-24, so are off by 2^-25 of the largest, times at most 4 as they come in units
+    of the tile's value scale (within a factor of four here)."""
+    c = _tree_case(kv, D, 16, 8, 2, [300, 70, 1000], [9, 30, 2], 41)
+    t = c["cache"]["k_scale"]
+    t *= (2.0 ** torch.randint(0, 7, t.shape, generator=_gen(2))).to(DEV)
+    _tree_check(_tree_call(pa, c), c, sums=(D + 4) * 2.0 ** -24, small=2.0 ** -23)
 
 
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
