@@ -23,7 +23,7 @@
 // operand of P V), O at 256 and 384.
 // 8-bit caches: K's codes are exact in fp16, and a score is multiplied by its token's scale in
 // fp32 (fp16 of code x scale would put scores of a few hundred off by a tenth and more; it
-// saved 14 us of 142 for the fp8 batch).  A value is code x scale in fp16, in units of a power of two per tile (2^e, the
+// saved 5 us of 132 for the fp8 batch).  A value is code x scale in fp16, in units of a power of two per tile (2^e, the
 // tile's largest scale below 2^7 of them, so entries below 448 x 128), the scale rounded to
 // fp16 and the product once more (2^-11 each; scales to 2^-20 of the tile's largest keep all
 // their bits, and what is below 2^-31 of it is lost).  The query rows are fp16 scaled by a power
@@ -225,6 +225,25 @@ __device__ __forceinline__ void scaled_f16(const uint4 &c, bool scaled, __half2 
 
 constexpr float kTiny = 1.17549435e-38f;  // least score factor: 0 times a masked -inf is a NaN
 constexpr int kScaleTop = 7;  // scales below 2^7 units: 448 x 2^7 is below fp16's 65504
+
+// Two fp32 operations in one instruction (one at a time: 141.6 instead of 132.5 us for the fp8
+// batch, 90.7 instead of 89.7 for the ragged one).
+__device__ __forceinline__ void mul2(float &x, float &y, float a, float b) {
+    asm("{\n.reg .b64 p, q;\nmov.b64 p, {%0, %1};\nmov.b64 q, {%2, %3};\nmul.rn.f32x2 p, p, q;\nmov.b64 {%0, %1}, p;\n}\n"
+        : "+f"(x), "+f"(y)
+        : "f"(a), "f"(b));
+}
+__device__ __forceinline__ void fma2(float &x, float &y, float a, float c) {
+    asm("{\n.reg .b64 p, q, r;\nmov.b64 p, {%0, %1};\nmov.b64 q, {%2, %2};\nmov.b64 r, {%3, %3};\nfma.rn.f32x2 p, p, q, r;\n"
+        "mov.b64 {%0, %1}, p;\n}\n"
+        : "+f"(x), "+f"(y)
+        : "f"(a), "f"(c));
+}
+__device__ __forceinline__ void add2(float &x, float &y, float a, float b) {
+    asm("{\n.reg .b64 p, q;\nmov.b64 p, {%0, %1};\nmov.b64 q, {%2, %3};\nadd.rn.f32x2 p, p, q;\nmov.b64 {%0, %1}, p;\n}\n"
+        : "+f"(x), "+f"(y)
+        : "f"(a), "f"(b));
+}
 
 // Exponent e with |x| < 2^e for the bits of a positive x, kept in -100 .. 100.
 __device__ __forceinline__ int exponent_over(uint32_t bits) {
@@ -742,10 +761,8 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
 #pragma unroll
                             for (int k = 0; k < 8; ++k) {
                                 const float4 w = ks[k];
-                                x[4 * k] *= w.x;
-                                x[4 * k + 1] *= w.y;
-                                x[4 * k + 2] *= w.z;
-                                x[4 * k + 3] *= w.w;
+                                mul2(x[4 * k], x[4 * k + 1], w.x, w.y);
+                                mul2(x[4 * k + 2], x[4 * k + 3], w.z, w.w);
                             }
                         }
                     };
@@ -809,9 +826,11 @@ tree_tc_kernel(const __grid_constant__ TreeContext a, const __grid_constant__ CU
                         for (int i = 0; i < 16; i += 2) {
                             float p[4];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                p[e] = tc_exp2(fmaf(x[2 * i + e], factor, -base));
-                                ls[e] += p[e];
+                            for (int e = 0; e < 4; e += 2) {
+                                fma2(x[2 * i + e], x[2 * i + e + 1], factor, -base);
+                                p[e] = tc_exp2(x[2 * i + e]);
+                                p[e + 1] = tc_exp2(x[2 * i + e + 1]);
+                                add2(ls[e], ls[e + 1], p[e], p[e + 1]);
                             }
                             if constexpr (QUANT) {
                                 pw[i] = __uint_as_float(tiled::f16x2(p[0], p[1]));
