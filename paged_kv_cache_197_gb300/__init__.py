@@ -1,4 +1,4 @@
-"""Paged KV-cache decode on GB300: Python binding of the C ABI in include/pa.h.
+"""Paged KV-cache decode on GB300: Python binding of the C ABI in include/pa.h and pa_draft.h.
 
 Every function here only marshals arguments (torch tensors -> pointers and sizes)
 and calls the function of the same name in libpa.so; all of the work runs in the
@@ -7,9 +7,14 @@ its call fails, an exception is raised.
 
 Layouts (see include/pa.h):
   query, out        [S][Hq][D] bf16
-  k_cache, v_cache  [N][Hkv][bs][D] bf16 or int8
-  k_scale, v_scale  [N][Hkv][bs] fp32 (int8 caches)
+  k_cache, v_cache  [N][Hkv][bs][D] bf16, int8, or uint8 (e4m3 codes)
+  k_scale, v_scale  [N][Hkv][bs] fp32 (8-bit caches)
   block_tables      [S][M] int32, context_lens [S] int32, slot_mapping [T] int64
+
+A step of speculative decoding over the cache (see include/pa_draft.h) is
+pa_rotary_and_cache, pa_tree_attention and pa_verify_tree; rows are [T], sequence s has rows
+query_start[s] .. query_start[s + 1] - 1, and parents [T] holds each row's parent in its
+sequence (-1: the root).
 """
 from __future__ import annotations
 

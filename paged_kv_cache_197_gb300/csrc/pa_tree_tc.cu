@@ -23,15 +23,19 @@
 // operand of P V), O at 256 and 384.
 // 8-bit caches: K's codes are exact in fp16, and a score is multiplied by its token's scale in
 // fp32 (fp16 of code x scale would put scores of a few hundred off by a tenth and more; it
-// saved 5 us of 132 for the fp8 batch).  A value is code x scale in fp16, in units of a power of two per tile (2^e, the
-// tile's largest scale below 2^7 of them, so entries below 448 x 128), the scale rounded to
-// fp16 and the product once more (2^-11 each; scales to 2^-20 of the tile's largest keep all
-// their bits, and what is below 2^-31 of it is lost).  The query rows are fp16 scaled by a power
-// of two each (exact), which the columns take into their score factor; and they keep the base m
-// above the scores plus the values' e: a weight p 2^e stays below 2^8 whatever the scales.
+// saved 5 us of 132 for the fp8 batch).  A value is code x scale in fp16, in units of a power
+// of two per tile (2^e, the tile's largest scale below 2^7 of them, so entries below 448 x 128),
+// the scale rounded to fp16 and the product once more (2^-11 each; scales to 2^-20 of the tile's
+// largest keep all their bits, and what is below 2^-31 of it is lost).  The query rows are fp16
+// scaled by a power of two each (exact), which the columns take into their score factor; and
+// they keep the base m above the scores plus the values' e: a weight p 2^e stays below 2^8
+// whatever the scales.
 // Bounds: up to 128 columns, or 256 shared ones, the 64 KB of a bf16 K and V tile take 2800 SM
 // clocks at the measured HBM rate and the products 1024 / 2048, so HBM bounds; more columns
-// reread the tiles through L2 and the products bound.
+// reread the tiles through L2.  Measured with the join: 20 trees of 16 nodes over 8000 tokens
+// (64/8 heads, 668 MB) 122.5 us, 5.5 TB/s; 16 trees of 33 to 64 nodes over 700 to 8191 tokens (512
+// columns) 89.7 us, of which the copies alone are 74; 64 trees of 9 to 16 nodes over 128 to 4096
+// tokens of an fp8 cache 132.5 us, the copies and changes of unit 93, the conversion 12.
 // Every wait is bounded; a wait that gives up stops the CTA (PA_FLAG_TIMEOUT).
 #include <cuda_fp16.h>
 #include <math.h>

@@ -17,6 +17,10 @@
 // others' shared memory, one cluster barrier, and each adds the parts in the same order, so
 // all decide the same.  The draw needs no further pass: the sums of the last one say which
 // run holds the target's place.
+// Bounds: the latency of steps that depend on one another.  64 chains over 131072 entries, 67 MB,
+// take 19.3 us with the launch: 1.4 for the gather, 0.7 for the tests, 2 for the pass (4 where
+// HBM is shared), 1.1 for the exchange, 3.4 for the draw.  (One CTA a sequence: 429 us; 256
+// threads a CTA and the draw one warp's in fp64: 31.5.)
 #include <cuda_bf16.h>
 #include <math.h>
 
