@@ -130,7 +130,9 @@ size_t pa_tree_workspace_size(int S, int T, int Hq, int Hkv, int D, int bs, int 
  *   query_start        [S + 1] int32, device; parents [T] int32, device (see above; several
  *                      rows of a sequence may have parent -1).
  *   max_query_len      host bound of the rows of a sequence, 1 .. min(T, PA_TREE_MAX_NODES).
- *   workspace          pa_tree_workspace_size(...) bytes, 256-byte aligned.
+ *   workspace          pa_tree_workspace_size(...) bytes, 256-byte aligned; nothing in it is kept from
+ *                      one call to the next, but calls that may run at the same time (streams,
+ *                      replayed graphs) need one each.
  * A sequence whose offsets are outside [0, T], decreasing or longer than max_query_len is
  * left out (PA_FLAG_QUERY_OUT_OF_RANGE), as is one with a parent that is neither -1 nor
  * below its row (PA_FLAG_TREE_PARENT): its rows of out are not written.  Other arguments,

@@ -539,6 +539,38 @@ def test_tree_graph_and_streams(pa, kv, D):
     assert torch.equal(outs[0], eager[1]) and torch.equal(outs[1], eager[1])
 
 
+def test_tree_graphs_that_share_a_workspace(pa):
+    """Two captured calls of other shapes and cache types with one workspace, replayed in turn on one stream."""
+    cases = [_tree_case("bf16", 128, 16, 8, 2, [700, 33], [40, 3], 43), _tree_case("fp8", 128, 32, 16, 4, [64, 0, 2100], [2, 9, 30], 44),
+             _tree_case("int8", 64, 16, 8, 2, [500], [12], 45)]
+    want = [_tree_call(pa, c) for c in cases]
+    sizes = [pa.pa_tree_workspace_size(len(c["lens"]), len(c["parents"]), c["q"].shape[1], c["k"].shape[1], c["q"].shape[2],
+                                       c["cache"]["k_cache"].shape[2], pa.kv_dtype_of(c["cache"]["k_cache"]), max(c["lens"]),
+                                       max(c["nodes"])) for c in cases]
+    ws = torch.full((max(sizes),), 0xff, dtype=torch.uint8, device=DEV)
+    graphs, outs, held = [], [], []
+    for c in cases:
+        args = dict(out=torch.empty_like(c["q"]), query=c["q"], key=c["k"], value=c["v"], k_cache=c["cache"]["k_cache"],
+                    v_cache=c["cache"]["v_cache"], block_tables=c["tables"], context_lens=_i32(c["lens"]), query_start=_i32(c["starts"]),
+                    parents=_i32(c["parents"]), scale=c["scale"], max_context_len=max(c["lens"]), max_query_len=max(c["nodes"]),
+                    workspace=ws, k_scale=c["cache"].get("k_scale"), v_scale=c["cache"].get("v_scale"))
+        pa.pa_tree_attention(**args)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            pa.pa_tree_attention(**args)
+        graphs.append(graph)
+        outs.append(args["out"])
+        held.append(args)
+    for out in outs:
+        out.zero_()
+    for i in (0, 1, 2, 1, 0, 2, 0):
+        graphs[i].replay()
+    torch.cuda.synchronize()
+    for out, eager in zip(outs, want):
+        assert torch.equal(out, eager)
+
+
 # ------------------------------------------------------------------------------ verify
 def _verify_case(S, V, nodes, seed, kind="tree", drafter=True, probs="fp32", pad=0, sharp=2.0, near=0.7, before=0, behind=0):
     g = _gen(seed)
