@@ -32,8 +32,9 @@ constexpr int kTreeTile = 128;  // cached tokens per tile
 // Each unit is laid out with a head start of positions before its tiles, about what changing over
 // to it costs in tiles, so that shares of many short units are smaller: 3 where the lanes share
 // their tiles, and a tile takes the products of both, else 4.  Batches of 128 to 8191 tokens a
-// sequence, 2 / 3 / 4 / 5 positions: shared bf16 92.7 / 90.9 / 92.6 / 93.2 us, shared fp8 130.0 /
-// 125.5 / 127.8, up to 128 columns fp8 142.6 / 134.7 / 127.5 / 129.3, bf16 113.4 / 110.0 / 110.3.
+// sequence, 2 / 3 / 4 / 5 positions: shared bf16 101.1 / 98.0 / 98.9 / 100.0 us, shared fp8 133.4 /
+// 128.9 / 130.9 / 131.7; 3 / 4 / 5 / 6: up to 128 columns fp8 141.9 / 133.3 / 134.4 / -, bf16 110.0 /
+// 110.7 / 111.1 / 112.6.
 __host__ __device__ constexpr int tree_pad(int cols) { return cols > 128 ? 3 : 4; }
 __host__ __device__ inline int64_t tree_unit_len(int64_t tiles, int cols) { return tiles > 0 ? tiles + tree_pad(cols) : 0; }
 
