@@ -626,7 +626,7 @@ def _verify_check(o, c):
 
 @pytest.mark.parametrize("probs", ["fp32", "bf16"])
 @pytest.mark.parametrize("drafter", [True, False])
-@pytest.mark.parametrize("V,pad", [(1, 0), (2, 0), (7, 1), (129, 0), (1000, 24), (5003, 0), (32000, 0), (33333, 3)])
+@pytest.mark.parametrize("V,pad", [(1, 0), (2, 0), (7, 1), (129, 0), (1000, 24), (5003, 0), (6007, 1), (32000, 0), (33333, 3)])
 def test_verify_trees(pa, V, pad, drafter, probs):
     """Trees and chains of one row up, rows of no sequence, vocabularies on both sides of a vector and of
     a CTA's share, rows with padding behind the vocabulary (NaN there)."""
