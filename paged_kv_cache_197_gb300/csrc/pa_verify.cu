@@ -15,8 +15,10 @@
 // equal run of it.  All CTAs walk the tree alike, from the tests' probabilities gathered for
 // all rows at once, and meet only for the sum of a pass: every CTA writes its part into the
 // others' shared memory, one cluster barrier, and each adds the parts in the same order, so
-// all decide the same.  The draw needs no further pass: the sums of the last one say which
-// run holds the target's place.
+// all decide the same.  (Another CTA's shared memory may be written once that CTA runs: all
+// arrive at a cluster barrier on entry and wait for it behind the first pass, so its latency
+// lies behind the gather and the loads.)  The draw needs no further pass: the sums of the last
+// one say which run holds the target's place.
 // Bounds: the latency of steps that depend on one another.  64 chains over 131072 entries, 67 MB,
 // take 19.3 us with the launch: 1.4 for the gather, 0.7 for the tests, 2 for the pass (4 where
 // HBM is shared), 1.1 for the exchange, 3.4 for the draw.  (One CTA a sequence: 429 us; 256
@@ -289,6 +291,10 @@ template <typename T, int kThreads>
 __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(const __grid_constant__ VerifyArgs a) {
     constexpr int kWarps = kThreads / 32;
     __shared__ Shared sh;
+    if (a.cluster > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    auto cluster_runs = [&] {  // every CTA of the cluster has started
+        if (a.cluster > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    };
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int s = blockIdx.x / a.cluster, rank = blockIdx.x % a.cluster;
@@ -321,6 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(const
         }
     bad = __syncthreads_or(bad);
     if (!offsets || bad || L == 0) {  // every CTA of the cluster alike
+        cluster_runs();
         if (rank == 0) {
             for (int j = tid; j < a.W; j += kThreads) tokens_out[j] = path[j] = -1;
             if (offsets && a.slots)
@@ -423,6 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(const
                                                         : run_sum<T, 2>(R, begin, end, a.vector != 0, lane);
         if (lane == 0) sh.run[warp] = d;
         __syncthreads();
+        if (pass == 0) cluster_runs();
         if (warp == 0) {
             const Pair mine = lanes_sum(lane < kWarps ? sh.run[lane] : Pair{0.f, 0.f}, kWarps);
             if (lane < a.cluster) {

@@ -657,6 +657,31 @@ def test_verify_large_vocabulary(pa):
         _verify_check(_verify_call(pa, c), c)
 
 
+@pytest.mark.parametrize("probs", ["fp32", "bf16"])
+@pytest.mark.parametrize("drafter", [True, False])
+def test_verify_serving_batches_of_clusters(pa, drafter, probs):
+    """More sequences than one wave of large blocks holds, each served by several blocks of threads: short and
+    empty trees over vocabularies just above the smallest that is split, where one block's part of a
+    sum is ready soonest; several rejections a sequence, some sequences refused."""
+    for V, kind, pad in ((6001, "star", 0), (6016, "tree", 0), (9001, "chain", 7)):
+        nodes = [(0, 1, 2, 4, 7, 12)[s % 6] for s in range(64)]
+        c = _verify_case(64, V, nodes, V, kind=kind, drafter=drafter, probs=probs, pad=pad, near=1.5)
+        c["u"][1::3] = 1 - (1 - c["u"][1::3]) * 1e-3  # hard to accept
+        for _ in range(8):
+            _verify_check(_verify_call(pa, c), c)
+        bad = dict(c, parents=list(c["parents"]))
+        refused = [s for s in range(64) if nodes[s] > 1 and s % 4 == 0]
+        for s in refused:
+            bad["parents"][c["starts"][s] + 1] = 1
+        flag, good = _flag(), _verify_call(pa, c)
+        o = _verify_call(pa, bad, flag=flag)
+        assert flag.item() == pa.PA_FLAG_TREE_PARENT
+        kept = [s for s in range(64) if s not in refused]
+        assert (o["n_out"][refused] == 0).all() and (o["tokens_out"][refused] == -1).all()
+        for name in ("tokens_out", "path", "n_out"):
+            assert torch.equal(o[name][kept], good[name][kept])
+
+
 def test_verify_one_hot_targets(pa):
     """Greedy targets: a draft is kept exactly where it is the target's token."""
     c = _verify_case(4, 300, [9, 9, 9, 9], 8, kind="chain", drafter=False)
