@@ -14,8 +14,8 @@
 // A cluster of CTAs serves a sequence, each CTA a slice of the vocabulary and each warp an
 // equal run of it.  All CTAs walk the tree alike, from the tests' probabilities gathered for
 // all rows at once, and meet only for the sum of a pass: every CTA writes its part into the
-// others' shared memory, one cluster barrier, and each adds the parts in the same order, so
-// all decide the same.  (Another CTA's shared memory may be written once that CTA runs: all
+// others' shared memory (the same number to each), one cluster barrier, and each adds the parts
+// in the same order, so all decide the same.  (Another CTA's shared memory may be written once that CTA runs: all
 // arrive at a cluster barrier on entry and wait for it behind the first pass, so its latency
 // lies behind the gather and the loads.)  The draw needs no further pass: the sums of the last
 // one say which run holds the target's place.
@@ -145,7 +145,8 @@ __device__ __forceinline__ Pair times(Pair x, float y) {
 }
 __device__ __forceinline__ bool less(Pair a, Pair b) { return __fadd_rn(__fsub_rn(a.hi, b.hi), __fsub_rn(a.lo, b.lo)) < 0.f; }
 
-// The sum over the first `lanes` (a power of two) lanes' pairs, in each of them.
+// The sum over the first `lanes` (a power of two) lanes' pairs, in each of them: the same hi, but lo
+// differs between lanes by its roundings (add does not round alike with its operands exchanged).
 __device__ __forceinline__ Pair lanes_sum(Pair s, int lanes) {
     for (int o = lanes / 2; o > 0; o >>= 1) {
         const Pair x{__shfl_xor_sync(0xffffffffu, s.hi, o), __shfl_xor_sync(0xffffffffu, s.lo, o)};
@@ -432,7 +433,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_kernel(const
         __syncthreads();
         if (pass == 0) cluster_runs();
         if (warp == 0) {
-            const Pair mine = lanes_sum(lane < kWarps ? sh.run[lane] : Pair{0.f, 0.f}, kWarps);
+            Pair mine = lanes_sum(lane < kWarps ? sh.run[lane] : Pair{0.f, 0.f}, kWarps);
+            // lane 0's, so that every CTA gets the same number
+            mine = {__shfl_sync(0xffffffffu, mine.hi, 0), __shfl_sync(0xffffffffu, mine.lo, 0)};
             if (lane < a.cluster) {
                 uint32_t to = (uint32_t)__cvta_generic_to_shared(&sh.part[pass & 1][rank]);
                 asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(to) : "r"(lane));

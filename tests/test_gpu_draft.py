@@ -682,6 +682,27 @@ def test_verify_serving_batches_of_clusters(pa, drafter, probs):
             assert torch.equal(o[name][kept], good[name][kept])
 
 
+def test_verify_draws_at_the_border_of_two_shares(pa):
+    """Rows whose halves hold the same entries in another order, drawn at one half of their sum: the border of two
+    blocks' shares exactly, so that the last bit of their sums decides.  The blocks of a sequence agree: one of
+    the two neighbours is drawn, the same one every time.  (Eight blocks that each added the others' parts
+    with roundings of their own left 3 of 38 such rows without a token.)"""
+    g, S, half = _gen(50), 38, 4096
+    for probs in (torch.float32, torch.bfloat16):
+        a = torch.softmax(torch.randn((S, half), generator=g, dtype=torch.float64) * 4, -1).to(probs)
+        p = torch.cat((a, torch.stack([row[torch.randperm(half, generator=g)] for row in a])), 1).to(DEV)
+        assert (p > 0).all()
+        said = []
+        for _ in range(10):
+            o = torch.full((S, 1), 99, dtype=torch.int32, device=DEV), torch.full((S, 1), 99, dtype=torch.int32, device=DEV)
+            n = torch.empty(S, dtype=torch.int32, device=DEV)
+            pa.pa_verify_tree(o[0], o[1], n, _i32([0] * S), p, _i32(range(S + 1)), _i32([-1] * S), torch.zeros(S, device=DEV),
+                              torch.full((S,), 0.5, device=DEV))
+            said.append(o[0][:, 0].tolist())
+        assert all(x in (half - 1, half) for x in said[0]), said[0]
+        assert all(x == said[0] for x in said)
+
+
 def test_verify_one_hot_targets(pa):
     """Greedy targets: a draft is kept exactly where it is the target's token."""
     c = _verify_case(4, 300, [9, 9, 9, 9], 8, kind="chain", drafter=False)
