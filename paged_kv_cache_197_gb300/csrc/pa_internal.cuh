@@ -152,7 +152,8 @@ cudaError_t launch_dequant_blocks(const MultiArgs &a, int bs, int kv_dtype, int 
 
 // Launch `kernel` as a programmatic dependent of the kernel before it on `stream`: it
 // may be scheduled while that kernel drains, and must execute griddepcontrol.wait
-// before it reads or writes anything that kernel may touch.
+// before it reads or writes anything that kernel may touch, and in one block at least
+// whatever the inputs: the kernel after it waits for this one's end alone.
 template <typename... Params, typename... Args>
 cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
                              cudaStream_t stream, Args &&...args) {

@@ -71,7 +71,9 @@ __device__ __forceinline__ float sums(float (&x)[HEADS], int lane) {
 // ancestors, from the row up, in fp32, the sequence's keys and values for the kv head
 // staged in shared memory (longer trees read them from L2); then the context's partials.
 // Launched as a programmatic dependent: the first part, which the context's kernel does not
-// touch, runs before the wait.
+// touch, runs before the wait.  The first CTA waits even where it has nothing to join (a sequence
+// left out): the context's kernel has then ended when this one has, and what comes next on
+// the stream, another call with this workspace perhaps, waits for this one alone.
 template <int D, int HEADS, bool STAGED>
 __global__ void __launch_bounds__(kJoinWarps * 32, 32 / kJoinWarps) tree_join_kernel(const __grid_constant__ TreeArgs a) {
     constexpr int PER = D / 32;
@@ -81,7 +83,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 32 / kJoinWarps) tree_join_ke
     const int kvh = blockIdx.y / a.chunks, h0 = blockIdx.y % a.chunks * HEADS;
     const int i = blockIdx.x * kJoinWarps + (tid >> 5);
     const int r0 = a.query_start[s], r1 = a.query_start[s + 1], L = r1 - r0;
-    if (!(r0 >= 0 && r1 <= a.T && L >= 0 && L <= a.max_query_len)) return;  // flagged by the context's kernel
+    auto depart = [] {
+        if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+    };
+    if (!(r0 >= 0 && r1 <= a.T && L >= 0 && L <= a.max_query_len)) return depart();  // flagged by the context's kernel
     const int top = min(L, ((int)blockIdx.x + 1) * kJoinWarps);  // ancestors are above their rows
     if ((int)blockIdx.x * kJoinWarps >= L && blockIdx.x > 0) return;
     if constexpr (STAGED) {
@@ -121,9 +126,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 32 / kJoinWarps) tree_join_ke
     if constexpr (STAGED) tiled::cp_async_wait<0>();
     if (__syncthreads_or(bad)) {
         if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0 && a.err_flag) atomicOr(a.err_flag, PA_FLAG_TREE_PARENT);
-        return;
+        return depart();
     }
-    if (i >= L) return;
+    if (i >= L) return depart();
     const int mine = lane % HEADS;  // the head whose scalars this lane keeps
     // acc = acc f + w x, with head h's f and w from the lane that keeps them
     auto add = [&](float f, float w, auto row) {

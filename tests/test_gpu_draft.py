@@ -571,6 +571,31 @@ def test_tree_graphs_that_share_a_workspace(pa):
         assert torch.equal(out, eager)
 
 
+@pytest.mark.parametrize("kv,D", [("bf16", 128), ("bf16", 64), ("int8", 64), ("fp8", 128)])
+def test_tree_refused_then_valid_on_one_workspace(pa, kv, D):
+    """A call all of whose sequences are left out (a bad parent behind a long context, no rows, too many
+    rows), and at once a valid one with the same workspace: the bits that call gives alone."""
+    good = _tree_case(kv, D, 16, 8, 2, [70, 700, 33], [9, 30, 16], 51)
+    late = _tree_case(kv, D, 16, 8, 2, [40000], [30], 52)
+    late["parents"][3] = 3
+    none = _tree_case(kv, D, 16, 8, 2, [40000], [0], 53, behind=30)
+    long = _tree_case(kv, D, 16, 8, 2, [40000], [31], 54)
+    code = pa.kv_dtype_of(good["cache"]["k_cache"])
+    n = max(pa.pa_tree_workspace_size(3, 55, 8, 2, D, 16, code, 700, 30), pa.pa_tree_workspace_size(1, 31, 8, 2, D, 16, code, 40000, 30))
+    ws = torch.full((n,), 0xff, dtype=torch.uint8, device=DEV)
+    alone = _tree_call(pa, good, workspace=ws)
+    _tree_check(alone, good)
+    for bad, flagged in ((late, pa.PA_FLAG_TREE_PARENT), (none, 0), (long, pa.PA_FLAG_QUERY_OUT_OF_RANGE)):
+        outs, held = [], torch.full_like(bad["q"], float("nan"))
+        flag = _flag()
+        for _ in range(20):
+            _tree_call(pa, bad, out=held, max_q=30, flag=flag, workspace=ws)
+            outs.append(_tree_call(pa, good, workspace=ws))
+        torch.cuda.synchronize()
+        assert flag.item() == flagged and torch.isnan(held.float()).all()
+        assert all(torch.equal(out, alone) for out in outs)
+
+
 # ------------------------------------------------------------------------------ verify
 def _verify_case(S, V, nodes, seed, kind="tree", drafter=True, probs="fp32", pad=0, sharp=2.0, near=0.7, before=0, behind=0):
     g = _gen(seed)
