@@ -157,6 +157,20 @@ def _stream(stream, device) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _workspace(n: int, device, stream) -> torch.Tensor | None:
+    """n bytes of scratch for one call on `stream`, None for none.  They are allocated on that stream:
+    when the call returns they are given back, and may be used again at once by what is queued
+    behind it there, but not by another stream before it has run."""
+    if n == 0:
+        return None
+    if stream is None:
+        return torch.empty(n, dtype=torch.uint8, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream, device), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(n, dtype=torch.uint8, device=device)
+
+
 def _flag(err_flag):
     if err_flag is not None:
         _cuda(err_flag, "err_flag", torch.int32)
@@ -383,7 +397,7 @@ def pa_decode_shared_prefix(out, query, k_cache, v_cache, block_tables, context_
     if workspace is None:
         n = pa_decode_shared_prefix_workspace_size(S, Hq, Hkv, D, bs, kv_dtype, max_context_len,
                                                    max_group_size, max_prefix_len)
-        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=query.device)
+        workspace = _workspace(max(n, 1), query.device, stream)
     _cuda(workspace, "workspace", workspace.dtype)
     ws_bytes = workspace.numel() * workspace.element_size()
     lib = load_library()
@@ -443,7 +457,7 @@ def pa_multi_token_attention(out, query, k_cache, v_cache, block_tables, context
             n = pa_multi_token_workspace_size_for_tokens(S, T, Hq, Hkv, D, bs, kv_dtype,
                                                          max_context_len, max_query_len,
                                                          total_context_tokens)
-        workspace = torch.empty(n, dtype=torch.uint8, device=query.device) if n else None
+        workspace = _workspace(n, query.device, stream)
     ws_bytes = 0
     if workspace is not None:
         _cuda(workspace, "workspace", workspace.dtype)
@@ -629,7 +643,7 @@ def pa_tree_attention(out, query, key, value, k_cache, v_cache, block_tables, co
         raise ValueError("pa_tree_attention: shape mismatch")
     if workspace is None:
         n = pa_tree_workspace_size(S, T, Hq, Hkv, D, bs, kv_dtype, max_context_len, max_query_len)
-        workspace = torch.empty(n, dtype=torch.uint8, device=query.device) if n else None
+        workspace = _workspace(n, query.device, stream)
     ws, ws_bytes = None, 0
     if workspace is not None:
         ws = _need(workspace, "workspace", workspace.dtype, workspace.dim(), dev)

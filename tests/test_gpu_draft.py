@@ -596,6 +596,77 @@ def test_tree_refused_then_valid_on_one_workspace(pa, kv, D):
         assert all(torch.equal(out, alone) for out in outs)
 
 
+class _Recorder:
+    """The library with one call replaced: it notes its arguments and runs nothing."""
+
+    def __init__(self, lib, name):
+        self._lib, self._name, self.args = lib, name, None
+
+    def __getattr__(self, name):
+        if name != self._name:
+            return getattr(self._lib, name)
+
+        def call(*args):
+            self.args = args
+            return 0
+        return call
+
+
+@pytest.mark.parametrize("handle", [False, True])
+@pytest.mark.parametrize("name", ["pa_tree_attention", "pa_multi_token_attention", "pa_decode_shared_prefix"])
+def test_default_workspace_belongs_to_the_calls_stream(pa, monkeypatch, name, handle):
+    """A workspace allocated for a call on another stream than the current one is not given to the current
+    stream's next allocation while that call may still run."""
+    c = _tree_case("bf16", 128, 16, 8, 2, [6000, 700], [9, 30], 55)
+    lib = pa.load_library()
+    recorder, side, fresh = _Recorder(lib, name), torch.cuda.Stream(), torch.empty_like(c["q"])
+    stream = side.cuda_stream if handle else side
+    cache = (c["cache"]["k_cache"], c["cache"]["v_cache"], c["tables"], _i32(c["lens"]))
+    q2 = torch.empty((2, 8, 128), dtype=torch.bfloat16, device=DEV)
+    starts, parents, one, prefix = _i32(c["starts"]), _i32(c["parents"]), _i32([0, 2]), _i32([16])
+    if name == "pa_tree_attention":
+        n, at = pa.pa_tree_workspace_size(2, 39, 8, 2, 128, 16, 0, 6000, 30), -4
+    elif name == "pa_multi_token_attention":
+        n, at = pa.pa_multi_token_workspace_size(2, 39, 8, 2, 128, 16, 0, 6000, 30), -4
+    else:
+        n, at = pa.pa_decode_shared_prefix_workspace_size(2, 8, 2, 128, 16, 0, 6000, 2, 16), -4
+    assert n > 0
+    monkeypatch.setattr(pa, "_LIB", recorder)
+    if name == "pa_tree_attention":
+        pa.pa_tree_attention(fresh, c["q"], c["k"], c["v"], *cache, starts, parents, 0.1, 6000, 30, stream=stream)
+    elif name == "pa_multi_token_attention":
+        pa.pa_multi_token_attention(fresh, c["q"], *cache, starts, 0.1, 6000, 30, stream=stream)
+    else:
+        pa.pa_decode_shared_prefix(q2, q2, *cache, 0.1, 6000, one, prefix, 2, 16, stream=stream)
+    monkeypatch.undo()
+    start, size = recorder.args[at], recorder.args[at + 1]
+    assert size >= n and recorder.args[-1] == side.cuda_stream
+    others = [torch.empty(n, dtype=torch.uint8, device=DEV) for _ in range(4)]
+    assert all(t.data_ptr() + n <= start or start + size <= t.data_ptr() for t in others)
+
+
+def test_default_workspace_on_a_side_stream(pa):
+    """Calls that allocate their own workspace on a side stream, behind work there, while the main stream allocates
+    and overwrites as much memory: the bits of a call on the main stream."""
+    c = _tree_case("bf16", 128, 16, 8, 2, [9000, 700, 33], [9, 30, 16], 56)
+    want, side = _tree_call(pa, c), torch.cuda.Stream()
+    n = pa.pa_tree_workspace_size(3, 55, 8, 2, 128, 16, 0, 9000, 30)
+    outs = [torch.full_like(c["q"], float("nan")) for _ in range(10)]
+    lists = [_i32(c[x]) for x in ("lens", "starts", "parents")]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(2_000_000)
+    for out in outs:
+        pa.pa_tree_attention(out, c["q"], c["k"], c["v"], c["cache"]["k_cache"], c["cache"]["v_cache"], c["tables"], *lists, c["scale"],
+                             9000, 30, stream=side)
+        for _ in range(4):
+            torch.empty(n, dtype=torch.uint8, device=DEV).fill_(0xff)
+    for _ in range(200):
+        torch.empty(n, dtype=torch.uint8, device=DEV).fill_(0xff)
+    torch.cuda.synchronize()
+    assert all(torch.equal(out, want) for out in outs)
+
+
 # ------------------------------------------------------------------------------ verify
 def _verify_case(S, V, nodes, seed, kind="tree", drafter=True, probs="fp32", pad=0, sharp=2.0, near=0.7, before=0, behind=0):
     g = _gen(seed)
