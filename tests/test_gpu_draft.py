@@ -498,6 +498,54 @@ def test_tree_of_a_chain_is_multi_token_attention(pa, kv):
     assert ((a.double() - b.double()).abs().cpu() <= bound).all()
 
 
+@pytest.mark.parametrize("kv", ["int8", "fp8"])
+def test_tree_of_a_chain_is_multi_token_attention_8bit(pa, kv):
+    """The same on 8-bit caches whose rows lose nothing: codes times a power of two, the largest code among
+    each row's, so that the chain's appended rows are the rows the tree saw.  Both results are
+    then within the bounds of a bf16 cache."""
+    g = _gen(57)
+    top, step = (127.0, 2.0 ** -5) if kv == "int8" else (448.0, 2.0 ** -7)
+
+    def rows(*shape):
+        x = (torch.randn(shape, generator=g) * top / 3).clamp(-top, top)
+        x = x.round() if kv == "int8" else x.to(torch.float8_e4m3fn).float()
+        x[..., 5] = top
+        return x
+
+    c = _tree_case(kv, 128, 16, 16, 4, [130, 64], [6, 20], 58, kind="chain", spare=8)
+    cache, N = c["cache"], c["cache"]["k_cache"].shape[0]
+    for name in ("k", "v"):
+        codes = rows(N, 4, 16, 128)
+        cache[name + "_cache"].copy_(codes.to(torch.int8) if kv == "int8" else codes.to(torch.float8_e4m3fn).view(torch.uint8))
+        cache[name + "_scale"].fill_(step)
+        c[name] = (rows(26, 4, 128) * step).to(torch.bfloat16).to(DEV)
+    a = _tree_call(pa, c)
+    _tree_check(a, c)
+    taken = set(c["tables"][c["tables"] < 2 ** 30].tolist())
+    free = [b for b in range(N) if b not in taken]
+    wide = torch.full((2, 16), 2 ** 30, dtype=torch.int32)
+    wide[:, : c["tables"].shape[1]] = c["tables"].cpu()
+    slots, lens = [], []
+    for s, n in enumerate(c["lens"]):
+        for t in range(n, n + c["nodes"][s]):
+            if wide[s, t // 16] == 2 ** 30:
+                wide[s, t // 16] = free.pop()
+            slots.append(int(wide[s, t // 16]) * 16 + t % 16)
+        lens.append(n + c["nodes"][s])
+    at = torch.tensor(slots, device=DEV)
+    (pa.pa_quantize_kv if kv == "int8" else pa.pa_quantize_kv_fp8)(c["k"], c["v"], *cache.values(), at)
+    block, off = (at // 16).cpu().numpy(), (at % 16).cpu().numpy()
+    for name in ("k", "v"):  # appended without loss
+        held = _values(cache[name + "_cache"])[block, :, off] * cache[name + "_scale"].cpu().double().numpy()[block, :, off][..., None]
+        assert (held == c[name].double().cpu().numpy()).all()
+    b = torch.empty_like(a)
+    pa.pa_multi_token_attention(b, c["q"], cache["k_cache"], cache["v_cache"], wide.to(DEV), _i32(lens), _i32(c["starts"]), c["scale"],
+                                max(lens), 20, k_scale=cache["k_scale"], v_scale=cache["v_scale"])
+    want, spread = _tree_reference(c)
+    bound = 2 * (2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -12) * spread)
+    assert ((a.double() - b.double()).abs().cpu() <= bound).all()
+
+
 @pytest.mark.parametrize("kv,D", [("bf16", 128), ("int8", 64), ("fp8", 128)])
 def test_tree_graph_and_streams(pa, kv, D):
     """Captured and replayed on other inputs of the same shapes, and run on two side streams at once with a
