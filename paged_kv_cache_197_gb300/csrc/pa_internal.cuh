@@ -121,7 +121,7 @@ struct MultiArgs {
 int multi_cols_per_cta();
 cudaError_t launch_multi_token(const MultiArgs &a, int D, int bs, int kv_dtype, cudaStream_t stream);
 // The mma.sync kernel over the whole context for every column (no causal limit, contexts
-// apart from the new tokens): partials only, ceil(context / part_tokens) per column.
+// apart from the new tokens), head_dim 64: partials only, ceil(context / part_tokens) per column.
 cudaError_t launch_multi_context(const MultiArgs &a, int D, int bs, int kv_dtype, cudaStream_t stream);
 // The log-sum-exp merge of multi-token partials (a programmatic dependent launch).
 cudaError_t launch_multi_merge(const MultiArgs &a, int D, int bs, cudaStream_t stream);

@@ -766,18 +766,24 @@ cudaError_t launch_multi_merge(const MultiArgs &a, int D, int bs, cudaStream_t s
     return bs == 16 ? launch_merge_typed<64, 16>(a, stream) : launch_merge_typed<64, 32>(a, stream);
 }
 
-template <typename KV, bool ALL = false>
+template <typename KV>
 cudaError_t launch_multi_kv(const MultiArgs &a, int D, int bs, cudaStream_t stream) {
     if (D == 128)
-        return bs == 16 ? launch_multi_typed<KV, 128, 16, ALL>(a, stream) : launch_multi_typed<KV, 128, 32, ALL>(a, stream);
-    return bs == 16 ? launch_multi_typed<KV, 64, 16, ALL>(a, stream) : launch_multi_typed<KV, 64, 32, ALL>(a, stream);
+        return bs == 16 ? launch_multi_typed<KV, 128, 16, false>(a, stream) : launch_multi_typed<KV, 128, 32, false>(a, stream);
+    return bs == 16 ? launch_multi_typed<KV, 64, 16, false>(a, stream) : launch_multi_typed<KV, 64, 32, false>(a, stream);
+}
+
+// head_dim 64 alone: the contexts of 128 have a kernel of their own.
+template <typename KV>
+cudaError_t launch_context_kv(const MultiArgs &a, int bs, cudaStream_t stream) {
+    return bs == 16 ? launch_multi_typed<KV, 64, 16, true>(a, stream) : launch_multi_typed<KV, 64, 32, true>(a, stream);
 }
 
 cudaError_t launch_multi_context(const MultiArgs &a, int D, int bs, int kv_dtype, cudaStream_t stream) {
-    if (!a.ws_acc || !a.ws_ml) return cudaErrorInvalidValue;
-    if (kv_dtype == PA_KV_INT8) return launch_multi_kv<int8_t, true>(a, D, bs, stream);
-    if (kv_dtype == PA_KV_FP8) return launch_multi_kv<e4m3_tag, true>(a, D, bs, stream);
-    return launch_multi_kv<uint16_t, true>(a, D, bs, stream);
+    if (!a.ws_acc || !a.ws_ml || D != 64) return cudaErrorInvalidValue;
+    if (kv_dtype == PA_KV_INT8) return launch_context_kv<int8_t>(a, bs, stream);
+    if (kv_dtype == PA_KV_FP8) return launch_context_kv<e4m3_tag>(a, bs, stream);
+    return launch_context_kv<uint16_t>(a, bs, stream);
 }
 
 bool multi_per_token_eligible(int D, int kv_dtype, int G, int max_query_len) {
