@@ -633,7 +633,6 @@ def pa_tree_attention(out, query, key, value, k_cache, v_cache, block_tables, co
     lens = _need(context_lens, "context_lens", torch.int32, 1, dev)
     starts = _need(query_start, "query_start", torch.int32, 1, dev)
     up = _need(parents, "parents", torch.int32, 1, dev)
-    max_context_len, max_query_len = int(max_context_len), int(max_query_len)
     shape, cache_shape = query.shape, k_cache.shape
     T, Hq, D = shape
     N, Hkv, bs, D2 = cache_shape
@@ -716,7 +715,7 @@ def pa_verify_tree(tokens_out, path, n_out, draft_tokens, target_probs, query_st
     flag = None if err_flag is None else _need(err_flag, "err_flag", torch.int32, err_flag.dim(), dev)
     _call(load_library().pa_verify_tree, dev, stream, said, way, count, slots, tokens, target_probs.data_ptr(), p_stride,
           qp, q_stride, PA_PROB_F32 if dtype is torch.float32 else PA_PROB_BF16, starts, up, u, u_final, S, T, V, W,
-          tables, M, lens, int(block_size), int(num_blocks), flag)
+          tables, M, lens, block_size, num_blocks, flag)
 
 
 # ------------------------------------------------------------------ block manager

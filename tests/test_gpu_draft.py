@@ -1057,16 +1057,6 @@ def test_speculative_step(pa, kv):
             assert torch.equal(cache[name].view(bits), other[name].view(bits)), name
 
 
-def test_sizes_given_as_array_scalars(pa):
-    """Bounds and sizes taken from an array (a NumPy integer, a one-element tensor) are numbers like any other."""
-    c = _tree_case("bf16", 128, 16, 8, 2, [70, 33], [9, 4], 59)
-    want = _tree_call(pa, c)
-    for number in (np.int64, torch.tensor):
-        assert torch.equal(_tree_call(pa, c, max_ctx=number(70), max_q=number(9)), want)
-    v = _verify_case(2, 64, [3, 3], 60)
-    _verify_check(_verify_call(pa, dict(v, bs=np.int32(16), N=np.int64(v["tables"].numel()))), v)
-
-
 def test_other_streams_and_devices(pa):
     """Calls on a side stream run there; tensors of another device than the first are refused."""
     c = _verify_case(2, 64, [3, 3], 40)
