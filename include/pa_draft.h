@@ -98,8 +98,9 @@ pa_status pa_rotary_table(const double *inv_freq, int n, uint64_t *table);
  *                      dense.  Outputs must not overlap inputs in any other way.
  *   k_cache, v_cache   the paged cache, or both NULL: no append, and value, slot_mapping and
  *                      the scales are ignored (then key_out must be given).  Layouts,
- *                      kv_dtype, scales and slot_mapping (negative: not appended) as in
- *                      pa_reshape_and_cache and pa_quantize_kv(_fp8).
+ *                      kv_dtype, scales and slot_mapping (negative: not appended; the
+ *                      others of a call must differ) as in pa_reshape_and_cache and
+ *                      pa_quantize_kv(_fp8).
  * Products and sums are fp32 with one rounding to bf16.  An 8-bit cache quantises the
  * rotated fp32 key by pa_quantize_kv(_fp8)'s rule directly, without rounding it to bf16
  * first; value rows are bit-identical to those calls.  D in {64, 128}, bs in {16, 32}.

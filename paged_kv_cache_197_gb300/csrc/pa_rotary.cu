@@ -87,10 +87,12 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], float scale) {
 // the head in the other lanes), 1 = interleaved (neighbouring pieces), 2 = half with any
 // other rot_dim (neighbouring pieces, partners read again from L1, by words where they align).
 // Bounds: HBM beyond a few hundred tokens.  8192 tokens of 64 + 8 + 8 heads, 336 MB, 56.3 us:
-// 5.97 TB/s, 0.88 of the measured copy rate.  (66.5 us with one piece a lane and partners
-// through shuffles, when the instructions were most of the time.)  Layout 2 is bound by its
-// partners' loads: 6000 tokens of these heads with rot_dim 20 take 60.1 us, interleaved 41.5 (two
-// bytes at a time and two rows in flight, in more registers, 97.6).
+// 5.97 TB/s, 0.88 of the measured copy rate; drafted rows, without a cache: 302 MB, 48.2 us.  (66.5 us
+// with one piece a lane and partners through shuffles, when the instructions were most of the
+// time.)  An fp8 cache takes longer for fewer bytes, 319 MB, 65.3 us, and the more so the more rows
+// are quantised: 32 + 32 + 32 heads, 338 MB, 87.7 us.  Layout 2 is bound by its partners' loads:
+// 6000 tokens of the first heads with rot_dim 20 take 59.4 us, interleaved 41.5 (two bytes at a time
+// and two rows in flight, in more registers, 97.6).
 template <int D, int KV, int LAYOUT>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryArgs a) {
     constexpr int LPR = D / 16;                      // lanes per row

@@ -30,12 +30,18 @@
 // scaled by a power of two each (exact), which the columns take into their score factor; and
 // they keep the base m above the scores plus the values' e: a weight p 2^e stays below 2^8
 // whatever the scales.
-// Bounds: up to 128 columns, or 256 shared ones, the 64 KB of a bf16 K and V tile take 2800 SM
-// clocks at the measured HBM rate and the products 1024 / 2048, so HBM bounds; more columns
-// reread the tiles through L2.  Measured with the join: 20 trees of 16 nodes over 8000 tokens
-// (64/8 heads, 668 MB) 122.5 us, 5.5 TB/s; 16 trees of 33 to 64 nodes over 700 to 8191 tokens (512
-// columns) 89.7 us, of which the copies alone are 74; 64 trees of 9 to 16 nodes over 128 to 4096
-// tokens of an fp8 cache 132.5 us, the copies and changes of unit 93, the conversion 12.
+// Weights are rounded to V's 16-bit type, as the two operands of a product have one type; their
+// sum l takes them unrounded.  Against 64 bits the bf16 outputs are off by 0.0023 relative,
+// where fp32 weights leave the output's own rounding, 0.0017; with fp16 weights it is 0.0017 too.
+// Bounds: with up to 128 columns the 64 KB of a bf16 K and V tile take 2800 SM clocks at the
+// measured HBM rate and the products 1024, so HBM bounds.  129 to 256 columns take 2048 clocks of
+// products, and a lane's chain of S, exponentials, P V and the next S 3700 to 3800 by clock
+// stamps, which bounds them, although every tile is fetched once for all the columns.  More
+// columns reread the tiles through L2, a CTA for every 256.  Measured with the join: 20 trees of 16
+// nodes over 8000 tokens (64/8 heads, 668 MB) 121 us, 5.5 TB/s; 16 trees of 33 to 64 nodes over 700
+// to 8191 tokens (32/8 heads: 132 to 256 columns) 89.9 us, with the copies alone 74; 64 trees of 9
+// to 16 nodes over 128 to 4096 tokens of an fp8 cache 133 us, the copies and changes of unit 93, the
+// conversion 12 (int8 132).
 // Every wait is bounded; a wait that gives up stops the CTA (PA_FLAG_TIMEOUT).
 #include <cuda_fp16.h>
 #include <math.h>

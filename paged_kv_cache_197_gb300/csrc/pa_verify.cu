@@ -613,7 +613,8 @@ extern "C" pa_status pa_verify_tree(int32_t *tokens_out, int32_t *path, int32_t 
     a.bs = bs;
     a.N = N;
     // small vocabularies: one CTA, whose sums need no cluster barrier (16 trees of 20 to 48 rows, one
-    // CTA / eight: 13.5 / 14.8 us at 4000 entries, 15.0 / 14.0 at 8000, 51.3 / 17.2 at 50021)
+    // CTA / eight: 13.5 / 14.8 us at 4000 entries, 15.0 / 14.0 at 8000, 51.3 / 17.2 at 50021; other counts
+    // between one and eight, and batches that take several waves of clusters, are not measured)
     a.cluster = V > 6000 ? kMaxCluster : 1;
     const int threads = (int64_t)S * a.cluster <= 2 * device_sms() ? kFew : kMany;
     const int64_t runs = (int64_t)a.cluster * (threads / 32);
