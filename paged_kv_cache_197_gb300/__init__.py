@@ -166,7 +166,8 @@ def _workspace(n: int, device, stream) -> torch.Tensor | None:
     if stream is None:
         return torch.empty(n, dtype=torch.uint8, device=device)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_stream(stream, device), device=device)
+        handle = _stream(stream, device)  # (an ExternalStream of 0 would be a new stream)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
     with torch.cuda.stream(stream):
         return torch.empty(n, dtype=torch.uint8, device=device)
 

@@ -693,6 +693,24 @@ def test_default_workspace_belongs_to_the_calls_stream(pa, monkeypatch, name, ha
     assert all(t.data_ptr() + n <= start or start + size <= t.data_ptr() for t in others)
 
 
+def test_default_workspace_on_the_default_stream(pa, monkeypatch):
+    """The default stream by its handle, 0, while another stream is current: the workspace is the default
+    stream's, given back to it and to no other."""
+    c = _tree_case("bf16", 128, 16, 8, 2, [6000, 700], [9, 30], 61)
+    want, n = _tree_call(pa, c), pa.pa_tree_workspace_size(2, 39, 8, 2, 128, 16, 0, 6000, 30)
+    torch.cuda.synchronize()
+    recorder, out, side = _Recorder(pa.load_library(), "pa_tree_attention"), torch.empty_like(c["q"]), torch.cuda.Stream()
+    with monkeypatch.context() as m, torch.cuda.stream(side):
+        m.setattr(pa, "_LIB", recorder)
+        _tree_call(pa, c, out=out, stream=0)
+        start, size = recorder.args[-4], recorder.args[-3]
+        others = [torch.empty(n, dtype=torch.uint8, device=DEV) for _ in range(4)]
+        assert all(t.data_ptr() + n <= start or start + size <= t.data_ptr() for t in others)
+    assert recorder.args[-1] in (0, None)
+    assert torch.empty(size, dtype=torch.uint8, device=DEV).data_ptr() == start  # (the current stream is the default one again)
+    assert torch.equal(_tree_call(pa, c, out=out, stream=0), want)
+
+
 def test_default_workspace_on_a_side_stream(pa):
     """Calls that allocate their own workspace on a side stream, behind work there, while the main stream allocates
     and overwrites as much memory: the bits of a call on the main stream."""
