@@ -89,6 +89,8 @@ enum {
                                          never accepted                                    */
     PA_FLAG_PROBABILITY = 1024,       /* pa_verify_tree: a row of probabilities to draw from
                                          has no finite, positive sum: token -1             */
+    PA_FLAG_SAMPLING = 2048,          /* pa_sample.h: a row with a temperature that is negative or
+                                         not finite, or a NaN top_p or min_p                 */
     PA_FLAG_WORKSPACE_SHORT = 128     /* pa_multi_token_attention, 8-bit cache, prefill-
                                          shaped call: the workspace's dequantised pool could
                                          not hold every attended block; the blocks beyond
@@ -157,6 +159,27 @@ pa_status pa_quantize_kv_fp8(const pa_bf16 *key, const pa_bf16 *value, uint8_t *
                              uint8_t *v_cache, float *k_scale, float *v_scale,
                              const int64_t *slot_mapping, int T, int Hkv, int D, int bs, int N,
                              int *err_flag, void *stream);
+
+/*
+ * Read cached rows back into dense ones: the inverse of the append, for rows that are handed
+ * on (to a cache of another type or pool through pa_quantize_kv(_fp8), to host memory, to an
+ * attention over dense keys).
+ *   key_out, value_out  [T][Hkv][D] bf16, device: the heads of a token dense, tokens
+ *                       key_stride / value_stride elements apart (multiples of 8, at least
+ *                       Hkv * D).  Row t receives the cache's row at slot_mapping[t]: its bits
+ *                       (bf16 cache), or code * scale rounded to bf16 (int8, fp8).  Must not
+ *                       overlap the cache.
+ *   slot_mapping        [T] int64, device, as in pa_reshape_and_cache, but several tokens may
+ *                       name one slot.  A token with a negative slot, or one >= N * bs
+ *                       (PA_FLAG_SLOT_OUT_OF_RANGE), leaves its rows as they were.
+ *   k_scale, v_scale    [N][Hkv][bs] fp32 for int8 and fp8; ignored (may be NULL) for bf16.
+ * D in {64, 128}, bs in {16, 32}.
+ */
+pa_status pa_gather_cache(pa_bf16 *key_out, int64_t key_stride, pa_bf16 *value_out,
+                          int64_t value_stride, const void *k_cache, const void *v_cache,
+                          const float *k_scale, const float *v_scale, int kv_dtype,
+                          const int64_t *slot_mapping, int T, int Hkv, int D, int bs, int N,
+                          int *err_flag, void *stream);
 
 /*
  * Copy-on-write block copy (gotburnout.io section 3.01): for each pair

@@ -114,6 +114,26 @@ pa_status pa_rotary_and_cache(pa_bf16 *query_out, pa_bf16 *key_out, const pa_bf1
                               float attention_factor, int T, int Hq, int Hkv, int D, int bs, int N,
                               int *err_flag, void *stream);
 
+/*
+ * The same with norms of the heads before the rotation, as models that normalise queries and
+ * keys need it: every query head x [D] and key head becomes
+ *   x / sqrt(mean_d x_d^2 + eps) * weight,
+ * in fp32, and is rotated (and, for an 8-bit cache, quantised) without being rounded to bf16 in
+ * between; elements from rot_dim on are normalised alone.  Values are not touched.
+ *   query_weight, key_weight   [D] fp32, device, one for all heads; NULL: 1.
+ *   eps                        positive.
+ * Other arguments as in pa_rotary_and_cache.
+ */
+pa_status pa_norm_rotary_and_cache(pa_bf16 *query_out, pa_bf16 *key_out, const pa_bf16 *query,
+                                   int64_t query_stride, const pa_bf16 *key, int64_t key_stride,
+                                   const pa_bf16 *value, int64_t value_stride, void *k_cache,
+                                   void *v_cache, float *k_scale, float *v_scale, int kv_dtype,
+                                   const int64_t *slot_mapping, const int64_t *positions,
+                                   const uint64_t *table, int rot_dim, int interleaved,
+                                   float attention_factor, const float *query_weight,
+                                   const float *key_weight, float eps, int T, int Hq, int Hkv, int D,
+                                   int bs, int N, int *err_flag, void *stream);
+
 /* Bytes of device workspace pa_tree_attention needs (0 for invalid arguments as well). */
 size_t pa_tree_workspace_size(int S, int T, int Hq, int Hkv, int D, int bs, int kv_dtype,
                               int max_context_len, int max_query_len);

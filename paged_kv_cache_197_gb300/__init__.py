@@ -1,4 +1,4 @@
-"""Paged KV-cache decode on GB300: Python binding of the C ABI in include/pa.h and pa_draft.h.
+"""Paged KV-cache decode on GB300: Python binding of the C ABI in include/pa.h, pa_draft.h and pa_sample.h.
 
 Every function here only marshals arguments (torch tensors -> pointers and sizes)
 and calls the function of the same name in libpa.so; all of the work runs in the
@@ -14,7 +14,9 @@ Layouts (see include/pa.h):
 A step of speculative decoding over the cache (see include/pa_draft.h) is
 pa_rotary_and_cache, pa_tree_attention and pa_verify_tree; rows are [T], sequence s has rows
 query_start[s] .. query_start[s + 1] - 1, and parents [T] holds each row's parent in its
-sequence (-1: the root).
+sequence (-1: the root).  pa_norm_rotary_and_cache is the first of them for models that
+normalise the heads of queries and keys; pa_sampling_probs makes the distributions that the
+last reads, and pa_sample_tokens draws tokens without drafts (see include/pa_sample.h).
 """
 from __future__ import annotations
 
@@ -39,8 +41,10 @@ PA_FLAG_WORKSPACE_SHORT = 128
 PA_FLAG_TREE_PARENT = 256
 PA_FLAG_TOKEN_OUT_OF_RANGE = 512
 PA_FLAG_PROBABILITY = 1024
+PA_FLAG_SAMPLING = 2048
 PA_TREE_MAX_NODES = 256
 PA_PROB_F32, PA_PROB_BF16 = 0, 1
+PA_SAMPLE_MAX_VOCABULARY = 1 << 20
 PA_ROTARY_PLAIN, PA_ROTARY_LINEAR, PA_ROTARY_BASE, PA_ROTARY_RAMP, PA_ROTARY_WAVELENGTH = range(5)
 
 EXPORTED = ["pa_version", "pa_status_string", "pa_last_error_string", "pa_reshape_and_cache",
@@ -48,7 +52,8 @@ EXPORTED = ["pa_version", "pa_status_string", "pa_last_error_string", "pa_reshap
             "pa_decode_noalloc", "pa_decode_shared_prefix_workspace_size", "pa_decode_shared_prefix",
             "pa_multi_token_workspace_size", "pa_multi_token_workspace_size_for_tokens",
             "pa_multi_token_attention", "pa_rotary_frequencies", "pa_rotary_table", "pa_rotary_and_cache",
-            "pa_tree_workspace_size", "pa_tree_attention", "pa_verify_tree"]
+            "pa_tree_workspace_size", "pa_tree_attention", "pa_verify_tree", "pa_norm_rotary_and_cache",
+            "pa_gather_cache", "pa_sample_tokens", "pa_sampling_probs"]
 PA_NOALLOC_SCRATCH_BYTES = 16 << 20
 
 
@@ -123,6 +128,15 @@ def load_library(path: Path | str | None = None) -> ctypes.CDLL:
     lib.pa_verify_tree.argtypes = [vp, vp, vp, vp, vp, vp, i64, vp, i64, i32, vp, vp, vp, vp, i32, i32, i32,
                                    i32, vp, i32, vp, i32, i32, vp, vp]
     lib.pa_verify_tree.restype = i32
+    lib.pa_norm_rotary_and_cache.argtypes = [vp, vp, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, i32, vp, vp, vp,
+                                             i32, i32, f32, vp, vp, f32, i32, i32, i32, i32, i32, i32, vp, vp]
+    lib.pa_norm_rotary_and_cache.restype = i32
+    lib.pa_gather_cache.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, vp, vp]
+    lib.pa_gather_cache.restype = i32
+    lib.pa_sample_tokens.argtypes = [vp, vp, vp, i64, i32, vp, vp, vp, vp, vp, i32, i32, vp, vp]
+    lib.pa_sample_tokens.restype = i32
+    lib.pa_sampling_probs.argtypes = [vp, i64, i32, vp, i64, i32, vp, vp, vp, vp, i32, i32, vp, vp]
+    lib.pa_sampling_probs.restype = i32
     if path is None:
         _LIB = lib
     return lib
@@ -571,13 +585,9 @@ def pa_rotary_table(inv_freq, device=None) -> torch.Tensor:
     return table if device is None else table.to(device)
 
 
-def pa_rotary_and_cache(query_out, query, key, positions, table, interleaved: bool = False,
-                        attention_factor: float = 1.0, key_out=None, value=None, k_cache=None, v_cache=None,
-                        slot_mapping=None, k_scale=None, v_scale=None, err_flag=None, stream=None) -> None:
-    """Rotate query [T][Hq][D] and key [T][Hkv][D] to positions [T] (int64), the first
-    2 * len(table) elements of each head; write query_out, key_out if given, and append the
-    rotated keys and the values if a cache is given.  query, key and value may be slices of
-    one tensor (dense heads, any token stride that is a multiple of 8)."""
+def _rotary_call(fn: str, norms, query_out, query, key, positions, table, interleaved, attention_factor, key_out, value,
+                 k_cache, v_cache, slot_mapping, k_scale, v_scale, err_flag, stream) -> None:
+    """pa_rotary_and_cache (norms None) and pa_norm_rotary_and_cache (query_weight, key_weight, eps)."""
     dev = _first_device(query, "query")
     q_stride, k_stride = _heads(query, "query", dev), _heads(key, "key", dev)
     T, Hq, D = query.shape
@@ -586,12 +596,12 @@ def pa_rotary_and_cache(query_out, query, key, positions, table, interleaved: bo
     pos = _need(positions, "positions", torch.int64, 1, dev)
     tab = _need(table, "table", torch.int64, 1, dev)
     if query_out.shape != query.shape or T2 != T or D2 != D or positions.shape[0] != T:
-        raise ValueError("pa_rotary_and_cache: shape mismatch")
+        raise ValueError(f"{fn}: shape mismatch")
     ko = None
     if key_out is not None:
         ko = _need(key_out, "key_out", torch.bfloat16, 3, dev)
         if key_out.shape != key.shape:
-            raise ValueError("pa_rotary_and_cache: shape mismatch")
+            raise ValueError(f"{fn}: shape mismatch")
     v_stride, kv_dtype, bs, N = 0, PA_KV_BF16, 16, 1
     vp = kc = vc = ks = vs = slots = None
     if k_cache is not None or v_cache is not None:
@@ -604,12 +614,62 @@ def pa_rotary_and_cache(query_out, query, key, positions, table, interleaved: bo
         shape = k_cache.shape
         N, heads, bs, D2 = shape
         if value.shape != key.shape or v_cache.shape != shape or heads != Hkv or D2 != D or slot_mapping.shape[0] != T:
-            raise ValueError("pa_rotary_and_cache: shape mismatch")
-        ks, vs = _scales(k_scale, v_scale, N, Hkv, bs, kv_dtype, dev, "pa_rotary_and_cache")
+            raise ValueError(f"{fn}: shape mismatch")
+        ks, vs = _scales(k_scale, v_scale, N, Hkv, bs, kv_dtype, dev, fn)
+    more = ()
+    if norms is not None:
+        weights = []
+        for w, name in ((norms[0], "query_weight"), (norms[1], "key_weight")):
+            weights.append(None if w is None else _need(w, name, torch.float32, 1, dev))
+            if w is not None and w.shape[0] != D:
+                raise ValueError(f"{fn}: {name} must have head_dim entries")
+        more = (*weights, norms[2])
     flag = None if err_flag is None else _need(err_flag, "err_flag", torch.int32, err_flag.dim(), dev)
-    _call(load_library().pa_rotary_and_cache, dev, stream, qo, ko, query.data_ptr(), q_stride, key.data_ptr(), k_stride,
-          vp, v_stride, kc, vc, ks, vs, kv_dtype, slots, pos, tab, 2 * table.shape[0], 1 if interleaved else 0,
-          attention_factor, T, Hq, Hkv, D, bs, N, flag)
+    _call(getattr(load_library(), fn), dev, stream, qo, ko, query.data_ptr(), q_stride, key.data_ptr(), k_stride, vp, v_stride,
+          kc, vc, ks, vs, kv_dtype, slots, pos, tab, 2 * table.shape[0], 1 if interleaved else 0, attention_factor, *more, T, Hq,
+          Hkv, D, bs, N, flag)
+
+
+def pa_rotary_and_cache(query_out, query, key, positions, table, interleaved: bool = False,
+                        attention_factor: float = 1.0, key_out=None, value=None, k_cache=None, v_cache=None,
+                        slot_mapping=None, k_scale=None, v_scale=None, err_flag=None, stream=None) -> None:
+    """Rotate query [T][Hq][D] and key [T][Hkv][D] to positions [T] (int64), the first
+    2 * len(table) elements of each head; write query_out, key_out if given, and append the
+    rotated keys and the values if a cache is given.  query, key and value may be slices of
+    one tensor (dense heads, any token stride that is a multiple of 8)."""
+    _rotary_call("pa_rotary_and_cache", None, query_out, query, key, positions, table, interleaved, attention_factor, key_out,
+                 value, k_cache, v_cache, slot_mapping, k_scale, v_scale, err_flag, stream)
+
+
+def pa_norm_rotary_and_cache(query_out, query, key, positions, table, eps: float, query_weight=None, key_weight=None,
+                             interleaved: bool = False, attention_factor: float = 1.0, key_out=None, value=None,
+                             k_cache=None, v_cache=None, slot_mapping=None, k_scale=None, v_scale=None, err_flag=None,
+                             stream=None) -> None:
+    """pa_rotary_and_cache of heads that are first divided by their root mean square (with eps
+    under the root) and multiplied by query_weight / key_weight [D] (fp32; None: 1)."""
+    _rotary_call("pa_norm_rotary_and_cache", (query_weight, key_weight, eps), query_out, query, key, positions, table,
+                 interleaved, attention_factor, key_out, value, k_cache, v_cache, slot_mapping, k_scale, v_scale, err_flag,
+                 stream)
+
+
+def pa_gather_cache(key_out, value_out, k_cache, v_cache, slot_mapping, k_scale=None, v_scale=None, err_flag=None,
+                    stream=None) -> None:
+    """Read the cached rows at slot_mapping [T] back into key_out / value_out [T][Hkv][D] bf16
+    (dense heads, any token stride that is a multiple of 8); negative slots leave theirs as
+    they were."""
+    dev = _first_device(k_cache, "k_cache")
+    k_stride, v_stride, kv_dtype = _heads(key_out, "key_out", dev), _heads(value_out, "value_out", dev), kv_dtype_of(k_cache)
+    kc = _need(k_cache, "k_cache", k_cache.dtype, 4, dev)
+    vc = _need(v_cache, "v_cache", k_cache.dtype, 4, dev)
+    slots = _need(slot_mapping, "slot_mapping", torch.int64, 1, dev)
+    N, Hkv, bs, D = k_cache.shape
+    T = slot_mapping.shape[0]
+    if v_cache.shape != k_cache.shape or key_out.shape != (T, Hkv, D) or value_out.shape != key_out.shape:
+        raise ValueError("pa_gather_cache: shape mismatch")
+    ks, vs = _scales(k_scale, v_scale, N, Hkv, bs, kv_dtype, dev, "pa_gather_cache")
+    flag = None if err_flag is None else _need(err_flag, "err_flag", torch.int32, err_flag.dim(), dev)
+    _call(load_library().pa_gather_cache, dev, stream, key_out.data_ptr(), k_stride, value_out.data_ptr(), v_stride, kc, vc, ks,
+          vs, kv_dtype, slots, T, Hkv, D, bs, N, flag)
 
 
 def pa_tree_workspace_size(S: int, T: int, Hq: int, Hkv: int, D: int, bs: int, kv_dtype: int,
@@ -717,6 +777,65 @@ def pa_verify_tree(tokens_out, path, n_out, draft_tokens, target_probs, query_st
     _call(load_library().pa_verify_tree, dev, stream, said, way, count, slots, tokens, target_probs.data_ptr(), p_stride,
           qp, q_stride, PA_PROB_F32 if dtype is torch.float32 else PA_PROB_BF16, starts, up, u, u_final, S, T, V, W,
           tables, M, lens, block_size, num_blocks, flag)
+
+
+# --------------------------------------------------------------- sampling (include/pa_sample.h)
+def _logit_rows(t, name: str, index: int):
+    """(rows, entries, row stride, PA_PROB_* code) of a 2-D fp32 or bf16 tensor with dense rows on device `index`."""
+    if t.dtype is not torch.float32 and t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name}: expected float32 or bfloat16")
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected 2 dimensions")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must live on the CUDA device of the other tensors")
+    R, V = t.shape
+    by_row, by_entry = t.stride()
+    if V > 1 and by_entry != 1:
+        raise ValueError(f"{name}: the entries of a row must be dense")
+    return R, V, by_row if R > 1 else V, PA_PROB_F32 if t.dtype is torch.float32 else PA_PROB_BF16
+
+
+def _filters(temperature, top_k, top_p, min_p, R: int, index: int):
+    """Addresses of the rows' parameters (None where one is not given)."""
+    out = []
+    for t, name, dtype in ((temperature, "temperature", torch.float32), (top_k, "top_k", torch.int32),
+                           (top_p, "top_p", torch.float32), (min_p, "min_p", torch.float32)):
+        out.append(None if t is None else _need(t, name, dtype, 1, index))
+        if t is not None and t.shape[0] != R:
+            raise ValueError(f"{name}: expected one entry a row")
+    return out
+
+
+def pa_sample_tokens(tokens_out, logits, uniforms, temperature=None, top_k=None, top_p=None, min_p=None, probs_out=None,
+                     err_flag=None, stream=None) -> None:
+    """Draw a token from each row of logits [R][V] (fp32 or bf16; dense rows, any stride), filtered
+    by temperature, top_k (int32), top_p and min_p ([R] tensors; None: 1, and off), with the
+    given uniform numbers [R]: tokens_out [R] int32 and, if given, its probability in probs_out [R]."""
+    dev = _first_device(logits, "logits")
+    R, V, stride, dtype = _logit_rows(logits, "logits", dev)
+    tokens = _need(tokens_out, "tokens_out", torch.int32, 1, dev)
+    u = _need(uniforms, "uniforms", torch.float32, 1, dev)
+    probs = None if probs_out is None else _need(probs_out, "probs_out", torch.float32, 1, dev)
+    if tokens_out.shape[0] != R or uniforms.shape[0] != R or (probs_out is not None and probs_out.shape[0] != R):
+        raise ValueError("pa_sample_tokens: shape mismatch")
+    filters = _filters(temperature, top_k, top_p, min_p, R, dev)
+    flag = None if err_flag is None else _need(err_flag, "err_flag", torch.int32, err_flag.dim(), dev)
+    _call(load_library().pa_sample_tokens, dev, stream, tokens, probs, logits.data_ptr(), stride, dtype, *filters, u, R, V, flag)
+
+
+def pa_sampling_probs(probs_out, logits, temperature=None, top_k=None, top_p=None, min_p=None, err_flag=None,
+                      stream=None) -> None:
+    """The distributions that pa_sample_tokens draws from, as rows of probabilities: probs_out [R][V]
+    (fp32 or bf16), ready for pa_verify_tree."""
+    dev = _first_device(logits, "logits")
+    R, V, stride, dtype = _logit_rows(logits, "logits", dev)
+    if not isinstance(probs_out, torch.Tensor) or probs_out.shape != logits.shape:
+        raise ValueError("pa_sampling_probs: shape mismatch")
+    _, _, out_stride, out_dtype = _logit_rows(probs_out, "probs_out", dev)
+    filters = _filters(temperature, top_k, top_p, min_p, R, dev)
+    flag = None if err_flag is None else _need(err_flag, "err_flag", torch.int32, err_flag.dim(), dev)
+    _call(load_library().pa_sampling_probs, dev, stream, probs_out.data_ptr(), out_stride, out_dtype, logits.data_ptr(), stride,
+          dtype, *filters, R, V, flag)
 
 
 # ------------------------------------------------------------------ block manager

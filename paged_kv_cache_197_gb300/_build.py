@@ -20,7 +20,7 @@ INCLUDE = ROOT / "include"
 BUILD = ROOT / "_build"
 LIBRARY = PKG / "libpa.so"
 SOURCES = ["pa_api.cu", "pa_cache.cu", "pa_decode.cu", "pa_prefix.cu", "pa_multi.cu", "pa_multi_tc.cu", "pa_noalloc.cu", "pa_blocks.cpp",
-           "pa_rotary.cu", "pa_tree.cu", "pa_tree_tc.cu", "pa_verify.cu"]
+           "pa_rotary.cu", "pa_tree.cu", "pa_tree_tc.cu", "pa_verify.cu", "pa_sample.cu", "pa_gather.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,4 +1,4 @@
-// Rotary positions fused with the cache append (pa_draft.h).
+// Rotary positions fused with the cache append, and with norms of the heads before them (pa_draft.h).
 //
 // A pair (x, x') of a head at position p is a complex number turned by the angle p f_j:
 //   y = x cos - x' sin,  y' = x' cos + x sin.
@@ -35,6 +35,8 @@ struct RotaryArgs {
     const uint64_t *table;
     int *err_flag;
     float factor;
+    const float *q_weight, *k_weight;  // norms: [D], or null for 1
+    float eps;
     int rot, T, Hq, Hkv, bs, N;
     int rows;           // Hq + Hkv, + Hkv value rows when appending
     int rows_per_cta;   // a multiple of the rows a CTA takes at once
@@ -93,7 +95,11 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], float scale) {
 // are quantised: 32 + 32 + 32 heads, 338 MB, 87.7 us.  Layout 2 is bound by its partners' loads:
 // 6000 tokens of the first heads with rot_dim 20 take 59.4 us, interleaved 41.5 (two bytes at a time
 // and two rows in flight, in more registers, 97.6).
-template <int D, int KV, int LAYOUT>
+//
+// NORM: query and key rows are normalised first, y = x / sqrt(mean x^2 + eps) w, in fp32.  A row lies in
+// its lanes' registers anyway, so the norm costs its sum of squares (log2 of the lanes' number shuffles)
+// and two products an element, but no byte more.
+template <int D, int KV, int LAYOUT, bool NORM>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryArgs a) {
     constexpr int LPR = D / 16;                      // lanes per row
     constexpr int SLOTS = kThreadsPerToken / LPR;    // rows of a token at once
@@ -157,15 +163,14 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
     // their bits, NaN payloads among them)
     const int words0 = LAYOUT == 0 ? (paired ? 4 : 0) : min(max((a.rot - 8 * p0) / 2, 0), 4);
     const int words1 = LAYOUT == 0 ? (paired ? 4 : 0) : min(max((a.rot - 8 * p1) / 2, 0), 4);
+    constexpr int kPartners = LAYOUT == 2 ? 16 : 1;
     const bool store = slot >= 0 && slot < (int64_t)a.N * a.bs;
     if (append && blockIdx.y == 0 && in == 0 && slot >= (int64_t)a.N * a.bs && a.err_flag)
         atomicOr(a.err_flag, PA_FLAG_SLOT_OUT_OF_RANGE);
     const int64_t blk = store ? slot / a.bs : 0;
     const int off = store ? (int)(slot % a.bs) : 0;
 
-    auto rotate = [&](const uint4 &r0, const uint4 &r1, const float (&part)[LAYOUT == 2 ? 16 : 1], float (&x)[8], float (&y)[8]) {
-        unpack8(r0, x);
-        unpack8(r1, y);
+    auto rotate = [&](const float (&part)[kPartners], float (&x)[8], float (&y)[8]) {
         if constexpr (LAYOUT == 0) {
             if (paired) {
 #pragma unroll
@@ -204,6 +209,36 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
         if (words < 4) w.w = raw.w;
         return w;
     };
+    // The row in x and y (and the partners of its elements) over its root mean square, times w.
+    auto normalise = [&](const float (&w)[16 + kPartners], float (&part)[kPartners], float (&x)[8], float (&y)[8]) {
+        auto squares = [&] {
+            float s = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s = fmaf(x[e], x[e], fmaf(y[e], y[e], s));
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(gmask, s, o);
+            return s * (1.f / D);
+        };
+        float mean = squares();
+        if (!(mean <= 3.402823466e38f)) {  // beyond fp32: the row 2^-80 times as large (eps is nothing to it)
+            constexpr float k = 8.2718061255302767e-25f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                x[e] *= k;
+                y[e] *= k;
+            }
+            for (int e = 0; e < (LAYOUT == 2 ? 16 : 0); ++e) part[e] *= k;
+            mean = squares();
+        }
+        const float over = rsqrtf(mean + a.eps);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            x[e] *= over * w[e];
+            y[e] *= over * w[8 + e];
+        }
+#pragma unroll
+        for (int e = 0; e < (LAYOUT == 2 ? 16 : 0); ++e) part[e] *= over * w[16 + e];
+    };
     // KIND 0: query rows, 1: key rows, 2: value rows; head h of this token at src + h D
     auto rows = [&](auto kind, int begin, int end, const uint16_t *src, uint16_t *out, void *cache, float *scales) {
         constexpr int KIND = decltype(kind)::value;
@@ -211,6 +246,24 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
         if (out) out += (int64_t)(begin + slot0) * D;
         int64_t row = (blk * a.Hkv + begin + slot0) * a.bs + off;
         const int64_t row_step = (int64_t)SLOTS * a.bs;
+        // the lane's weights, and those of its elements' partners
+        float weights[NORM && KIND < 2 ? 16 + kPartners : 1];
+        if constexpr (NORM && KIND < 2) {
+            const float *w = KIND == 0 ? a.q_weight : a.k_weight;
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+                const float4 four = w ? __ldg(reinterpret_cast<const float4 *>(w + 8 * (e < 8 ? p0 : p1) + e % 8)) : make_float4(1.f, 1.f, 1.f, 1.f);
+                weights[e] = four.x;
+                weights[e + 1] = four.y;
+                weights[e + 2] = four.z;
+                weights[e + 3] = four.w;
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int i = 16 * c + e;
+                if (LAYOUT == 2) weights[16 + e % kPartners] = w && i < a.rot ? w[i < half ? i + half : i - half] : 1.f;
+            }
+        }
         for (int h = begin + slot0; h < end; h += SLOTS * kBatch) {
             uint4 raw[kBatch][2];
             float part[LAYOUT == 2 && KIND < 2 ? kBatch : 1][LAYOUT == 2 ? 16 : 1];
@@ -245,9 +298,12 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
                 float x[8], y[8];
                 uint4 w0 = raw[b][0], w1 = raw[b][1];
                 if constexpr (KIND < 2) {
-                    rotate(raw[b][0], raw[b][1], part[LAYOUT == 2 ? b : 0], x, y);
-                    w0 = keep(w0, pack8(x), words0);
-                    w1 = keep(w1, pack8(y), words1);
+                    unpack8(w0, x);
+                    unpack8(w1, y);
+                    if constexpr (NORM) normalise(weights, part[LAYOUT == 2 ? b : 0], x, y);
+                    rotate(part[LAYOUT == 2 ? b : 0], x, y);
+                    w0 = NORM ? pack8(x) : keep(w0, pack8(x), words0);
+                    w1 = NORM ? pack8(y) : keep(w1, pack8(y), words1);
                     if (KIND == 0 || out) {
                         *reinterpret_cast<uint4 *>(out + b * SLOTS * D + 8 * p0) = w0;
                         *reinterpret_cast<uint4 *>(out + b * SLOTS * D + 8 * p1) = w1;
@@ -290,23 +346,128 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
         rows(std::integral_constant<int, 2>(), vlo, vhi, a.v + t * a.v_stride, nullptr, a.v_cache, a.v_scale);
 }
 
-template <int D, int KV>
+template <int D, int KV, bool NORM>
 cudaError_t launch_rotary_typed(const RotaryArgs &a, int layout, dim3 grid, cudaStream_t stream) {
-    auto *k = layout == 0 ? rotary_kernel<D, KV, 0> : layout == 1 ? rotary_kernel<D, KV, 1> : rotary_kernel<D, KV, 2>;
+    auto *k = layout == 0   ? rotary_kernel<D, KV, 0, NORM>
+              : layout == 1 ? rotary_kernel<D, KV, 1, NORM>
+                            : rotary_kernel<D, KV, 2, NORM>;
     return launch_dependent(k, grid, dim3(kThreads), 0, stream, a);
 }
 
-template <int D>
+template <int D, bool NORM>
 cudaError_t launch_rotary(const RotaryArgs &a, int kv_dtype, int layout, dim3 grid, cudaStream_t stream) {
-    if (kv_dtype == PA_KV_INT8) return launch_rotary_typed<D, PA_KV_INT8>(a, layout, grid, stream);
-    if (kv_dtype == PA_KV_FP8) return launch_rotary_typed<D, PA_KV_FP8>(a, layout, grid, stream);
-    return launch_rotary_typed<D, PA_KV_BF16>(a, layout, grid, stream);
+    if (kv_dtype == PA_KV_INT8) return launch_rotary_typed<D, PA_KV_INT8, NORM>(a, layout, grid, stream);
+    if (kv_dtype == PA_KV_FP8) return launch_rotary_typed<D, PA_KV_FP8, NORM>(a, layout, grid, stream);
+    return launch_rotary_typed<D, PA_KV_BF16, NORM>(a, layout, grid, stream);
 }
 
 // Whether [a, a + n) and [b, b + m) bytes overlap.
 bool overlap(const void *a, int64_t n, const void *b, int64_t m) {
     const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
     return a && b && x < y + (uintptr_t)m && y < x + (uintptr_t)n;
+}
+
+struct Norms {
+    bool wanted;
+    const float *query_weight, *key_weight;
+    float eps;
+};
+
+// What the calls with and without norms share: checks, plan and launch.
+pa_status rotary_call(const char *fn, const Norms &norms, pa_bf16 *query_out, pa_bf16 *key_out, const pa_bf16 *query,
+                      int64_t query_stride, const pa_bf16 *key, int64_t key_stride, const pa_bf16 *value, int64_t value_stride,
+                      void *k_cache, void *v_cache, float *k_scale, float *v_scale, int kv_dtype, const int64_t *slot_mapping,
+                      const int64_t *positions, const uint64_t *table, int rot_dim, int interleaved, float attention_factor,
+                      int T, int Hq, int Hkv, int D, int bs, int N, int *err_flag, void *stream) {
+    clear_error();
+    const bool append = k_cache != nullptr || v_cache != nullptr;
+    if (T < 0) return fail(PA_ERR_INVALID_ARG, "%s: T = %d is negative", fn, T);
+    if (Hq <= 0 || Hkv <= 0) return fail(PA_ERR_INVALID_ARG, "%s: Hq = %d, Hkv = %d", fn, Hq, Hkv);
+    if (D != 64 && D != 128) return fail(PA_ERR_UNSUPPORTED, "%s: head_dim %d not supported (64 or 128)", fn, D);
+    if (Hq > 65536 || Hkv > 65536) return fail(PA_ERR_UNSUPPORTED, "%s: too many heads", fn);
+    if (rot_dim < 2 || rot_dim > D || rot_dim % 2 != 0)
+        return fail(PA_ERR_INVALID_ARG, "%s: rot_dim = %d (even, 2 .. head_dim)", fn, rot_dim);
+    if (!std::isfinite(attention_factor)) return fail(PA_ERR_INVALID_ARG, "%s: attention_factor must be finite", fn);
+    if (norms.wanted && !(norms.eps > 0.f && std::isfinite(norms.eps)))
+        return fail(PA_ERR_INVALID_ARG, "%s: eps must be positive and finite", fn);
+    if (append) {
+        pa_status st = check_cache_shape(fn, Hkv, D, bs, N);
+        if (st != PA_OK) return st;
+        if (kv_dtype != PA_KV_BF16 && kv_dtype != PA_KV_INT8 && kv_dtype != PA_KV_FP8)
+            return fail(PA_ERR_UNSUPPORTED, "%s: kv dtype %d not supported", fn, kv_dtype);
+    }
+    const int64_t qw = (int64_t)Hq * D, kw = (int64_t)Hkv * D;
+    constexpr int64_t kMost = (int64_t)1 << 40;
+    if (query_stride < qw || key_stride < kw || query_stride % 8 != 0 || key_stride % 8 != 0 || query_stride > kMost ||
+        key_stride > kMost)
+        return fail(PA_ERR_INVALID_ARG, "%s: token strides must be multiples of 8, at least heads * head_dim", fn);
+    if (append && (value_stride < kw || value_stride % 8 != 0 || value_stride > kMost))
+        return fail(PA_ERR_INVALID_ARG, "%s: token strides must be multiples of 8, at least heads * head_dim", fn);
+    if (T == 0) return PA_OK;
+    if (!query_out || !query || !key || !positions || !table || (!append && !key_out))
+        return fail(PA_ERR_INVALID_ARG, "%s: null pointer", fn);
+    if (append && (!k_cache || !v_cache || !value || !slot_mapping || (kv_dtype != PA_KV_BF16 && (!k_scale || !v_scale))))
+        return fail(PA_ERR_INVALID_ARG, "%s: null pointer (appending)", fn);
+    if (!aligned16(query_out) || !aligned16(key_out) || !aligned16(query) || !aligned16(key))
+        return fail(PA_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", fn);
+    if (append && (!aligned16(value) || !aligned16(k_cache) || !aligned16(v_cache) ||
+                   (kv_dtype != PA_KV_BF16 && (!aligned16(k_scale) || !aligned16(v_scale)))))
+        return fail(PA_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", fn);
+    if (!aligned16(norms.query_weight) || !aligned16(norms.key_weight))
+        return fail(PA_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", fn);
+    // an output may be its own dense input; any other overlap would be read after it is written
+    const int64_t qo = 2 * (int64_t)T * qw, ko = 2 * (int64_t)T * kw;
+    const int64_t qi = 2 * ((T - 1) * query_stride + qw), ki = 2 * ((T - 1) * key_stride + kw);
+    const int64_t vi = append ? 2 * ((T - 1) * value_stride + kw) : 0;
+    const bool q_same = query_out == query && query_stride == qw, k_same = key_out == key && key_stride == kw;
+    if ((!q_same && overlap(query_out, qo, query, qi)) || overlap(query_out, qo, key, ki) ||
+        (!k_same && overlap(key_out, ko, key, ki)) || overlap(key_out, ko, query, qi) || overlap(query_out, qo, key_out, ko) ||
+        (append && (overlap(query_out, qo, value, vi) || overlap(key_out, ko, value, vi))))
+        return fail(PA_ERR_INVALID_ARG, "%s: an output overlaps an input (only whole dense tensors may be rotated in place)", fn);
+    RotaryArgs a{};
+    a.q_out = query_out;
+    a.k_out = key_out;
+    a.q = query;
+    a.k = key;
+    a.v = value;
+    a.q_stride = query_stride;
+    a.k_stride = key_stride;
+    a.v_stride = value_stride;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.slots = slot_mapping;
+    a.positions = positions;
+    a.table = table;
+    a.err_flag = err_flag;
+    a.factor = attention_factor;
+    a.q_weight = norms.query_weight;
+    a.k_weight = norms.key_weight;
+    a.eps = norms.eps;
+    a.rot = rot_dim;
+    a.T = T;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.bs = bs;
+    a.N = N;
+    a.rows = Hq + Hkv + (append ? Hkv : 0);
+    // enough CTAs for one wave at two per SM, else all rows of a token in one CTA (its
+    // cosines are computed once)
+    const int step = kThreadsPerToken / (D / 16);  // rows of a token at once
+    const int groups = (T + kTokens - 1) / kTokens;
+    const int most = (a.rows + step - 1) / step;
+    const int split = std::min(most, std::max(1, 304 / groups));
+    a.rows_per_cta = (most + split - 1) / split * step;
+    const dim3 grid(groups, (a.rows + a.rows_per_cta - 1) / a.rows_per_cta);
+    const int layout = interleaved ? 1 : (rot_dim / 2) % 8 == 0 ? 0 : 2;
+    if (!append) kv_dtype = PA_KV_BF16;
+    const cudaStream_t st = (cudaStream_t)stream;
+    if (norms.wanted)
+        D == 128 ? launch_rotary<128, true>(a, kv_dtype, layout, grid, st) : launch_rotary<64, true>(a, kv_dtype, layout, grid, st);
+    else
+        D == 128 ? launch_rotary<128, false>(a, kv_dtype, layout, grid, st) : launch_rotary<64, false>(a, kv_dtype, layout, grid, st);
+    return check_launch(fn);
 }
 
 }  // namespace
@@ -386,86 +547,22 @@ pa_status pa_rotary_and_cache(pa_bf16 *query_out, pa_bf16 *key_out, const pa_bf1
                               const int64_t *slot_mapping, const int64_t *positions, const uint64_t *table,
                               int rot_dim, int interleaved, float attention_factor, int T, int Hq, int Hkv, int D,
                               int bs, int N, int *err_flag, void *stream) {
-    const char *fn = "pa_rotary_and_cache";
-    clear_error();
-    const bool append = k_cache != nullptr || v_cache != nullptr;
-    if (T < 0) return fail(PA_ERR_INVALID_ARG, "%s: T = %d is negative", fn, T);
-    if (Hq <= 0 || Hkv <= 0) return fail(PA_ERR_INVALID_ARG, "%s: Hq = %d, Hkv = %d", fn, Hq, Hkv);
-    if (D != 64 && D != 128) return fail(PA_ERR_UNSUPPORTED, "%s: head_dim %d not supported (64 or 128)", fn, D);
-    if (Hq > 65536 || Hkv > 65536) return fail(PA_ERR_UNSUPPORTED, "%s: too many heads", fn);
-    if (rot_dim < 2 || rot_dim > D || rot_dim % 2 != 0)
-        return fail(PA_ERR_INVALID_ARG, "%s: rot_dim = %d (even, 2 .. head_dim)", fn, rot_dim);
-    if (!std::isfinite(attention_factor)) return fail(PA_ERR_INVALID_ARG, "%s: attention_factor must be finite", fn);
-    if (append) {
-        pa_status st = check_cache_shape(fn, Hkv, D, bs, N);
-        if (st != PA_OK) return st;
-        if (kv_dtype != PA_KV_BF16 && kv_dtype != PA_KV_INT8 && kv_dtype != PA_KV_FP8)
-            return fail(PA_ERR_UNSUPPORTED, "%s: kv dtype %d not supported", fn, kv_dtype);
-    }
-    const int64_t qw = (int64_t)Hq * D, kw = (int64_t)Hkv * D;
-    constexpr int64_t kMost = (int64_t)1 << 40;
-    if (query_stride < qw || key_stride < kw || query_stride % 8 != 0 || key_stride % 8 != 0 || query_stride > kMost ||
-        key_stride > kMost)
-        return fail(PA_ERR_INVALID_ARG, "%s: token strides must be multiples of 8, at least heads * head_dim", fn);
-    if (append && (value_stride < kw || value_stride % 8 != 0 || value_stride > kMost))
-        return fail(PA_ERR_INVALID_ARG, "%s: token strides must be multiples of 8, at least heads * head_dim", fn);
-    if (T == 0) return PA_OK;
-    if (!query_out || !query || !key || !positions || !table || (!append && !key_out))
-        return fail(PA_ERR_INVALID_ARG, "%s: null pointer", fn);
-    if (append && (!k_cache || !v_cache || !value || !slot_mapping || (kv_dtype != PA_KV_BF16 && (!k_scale || !v_scale))))
-        return fail(PA_ERR_INVALID_ARG, "%s: null pointer (appending)", fn);
-    if (!aligned16(query_out) || !aligned16(key_out) || !aligned16(query) || !aligned16(key))
-        return fail(PA_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", fn);
-    if (append && (!aligned16(value) || !aligned16(k_cache) || !aligned16(v_cache) ||
-                   (kv_dtype != PA_KV_BF16 && (!aligned16(k_scale) || !aligned16(v_scale)))))
-        return fail(PA_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", fn);
-    // an output may be its own dense input; any other overlap would be read after it is written
-    const int64_t qo = 2 * (int64_t)T * qw, ko = 2 * (int64_t)T * kw;
-    const int64_t qi = 2 * ((T - 1) * query_stride + qw), ki = 2 * ((T - 1) * key_stride + kw);
-    const int64_t vi = append ? 2 * ((T - 1) * value_stride + kw) : 0;
-    const bool q_same = query_out == query && query_stride == qw, k_same = key_out == key && key_stride == kw;
-    if ((!q_same && overlap(query_out, qo, query, qi)) || overlap(query_out, qo, key, ki) ||
-        (!k_same && overlap(key_out, ko, key, ki)) || overlap(key_out, ko, query, qi) || overlap(query_out, qo, key_out, ko) ||
-        (append && (overlap(query_out, qo, value, vi) || overlap(key_out, ko, value, vi))))
-        return fail(PA_ERR_INVALID_ARG, "%s: an output overlaps an input (only whole dense tensors may be rotated in place)", fn);
-    RotaryArgs a{};
-    a.q_out = query_out;
-    a.k_out = key_out;
-    a.q = query;
-    a.k = key;
-    a.v = value;
-    a.q_stride = query_stride;
-    a.k_stride = key_stride;
-    a.v_stride = value_stride;
-    a.k_cache = k_cache;
-    a.v_cache = v_cache;
-    a.k_scale = k_scale;
-    a.v_scale = v_scale;
-    a.slots = slot_mapping;
-    a.positions = positions;
-    a.table = table;
-    a.err_flag = err_flag;
-    a.factor = attention_factor;
-    a.rot = rot_dim;
-    a.T = T;
-    a.Hq = Hq;
-    a.Hkv = Hkv;
-    a.bs = bs;
-    a.N = N;
-    a.rows = Hq + Hkv + (append ? Hkv : 0);
-    // enough CTAs for one wave at two per SM, else all rows of a token in one CTA (its
-    // cosines are computed once)
-    const int step = kThreadsPerToken / (D / 16);  // rows of a token at once
-    const int groups = (T + kTokens - 1) / kTokens;
-    const int most = (a.rows + step - 1) / step;
-    const int split = std::min(most, std::max(1, 304 / groups));
-    a.rows_per_cta = (most + split - 1) / split * step;
-    const dim3 grid(groups, (a.rows + a.rows_per_cta - 1) / a.rows_per_cta);
-    const int layout = interleaved ? 1 : (rot_dim / 2) % 8 == 0 ? 0 : 2;
-    if (!append) kv_dtype = PA_KV_BF16;
-    D == 128 ? launch_rotary<128>(a, kv_dtype, layout, grid, (cudaStream_t)stream)
-             : launch_rotary<64>(a, kv_dtype, layout, grid, (cudaStream_t)stream);
-    return check_launch(fn);
+    return rotary_call("pa_rotary_and_cache", Norms{}, query_out, key_out, query, query_stride, key, key_stride, value,
+                       value_stride, k_cache, v_cache, k_scale, v_scale, kv_dtype, slot_mapping, positions, table, rot_dim,
+                       interleaved, attention_factor, T, Hq, Hkv, D, bs, N, err_flag, stream);
+}
+
+pa_status pa_norm_rotary_and_cache(pa_bf16 *query_out, pa_bf16 *key_out, const pa_bf16 *query, int64_t query_stride,
+                                   const pa_bf16 *key, int64_t key_stride, const pa_bf16 *value, int64_t value_stride,
+                                   void *k_cache, void *v_cache, float *k_scale, float *v_scale, int kv_dtype,
+                                   const int64_t *slot_mapping, const int64_t *positions, const uint64_t *table,
+                                   int rot_dim, int interleaved, float attention_factor, const float *query_weight,
+                                   const float *key_weight, float eps, int T, int Hq, int Hkv, int D, int bs, int N,
+                                   int *err_flag, void *stream) {
+    return rotary_call("pa_norm_rotary_and_cache", Norms{true, query_weight, key_weight, eps}, query_out, key_out, query,
+                       query_stride, key, key_stride, value, value_stride, k_cache, v_cache, k_scale, v_scale, kv_dtype,
+                       slot_mapping, positions, table, rot_dim, interleaved, attention_factor, T, Hq, Hkv, D, bs, N, err_flag,
+                       stream);
 }
 
 }  // extern "C"
