@@ -1,19 +1,23 @@
 // From logits to tokens or to filtered probabilities (pa_sample.h).
 //
-// Nothing is sorted.  The tokens that top-k and top-p leave are those down to a border in the
-// order (falling logit, rising index), and the border is searched: the tokens are counted, and
-// their weights summed, in 1024 bins over the logits; the bin that the border falls into is known
-// exactly, and it is split further (over its logits, and over the indices of equal logits)
-// until at most kList tokens are in question, which are gathered and sorted.  Then a token
-// is drawn by sums over runs of the vocabulary, narrowed down to the run, a thread's piece of it
-// and an entry; or the row is written.
+// No row is sorted.  The tokens that top-k and top-p leave are those down to a border in the
+// order (falling logit, rising index), and the border is searched: the tokens are counted in
+// cells of a grid over the logits, which gives the cell of the border (exactly for top-k; for
+// top-p as far as cells' mean weights tell); a second pass sums the weights before that cell and
+// gathers the cell's tokens, whose sorted list has the border.  Cells with more than kList tokens
+// are split on, over their logits and over the indices of equal logits.  A token is then
+// drawn by the sums of runs of the vocabulary, which the same pass left, narrowed down to a run, a
+// thread's piece of it and an entry; or the row is written.
 //
-// Weights are whole numbers: 2^45 exp((x - m) / T), rounded.  Their sums are exact and do not
-// depend on the order, so every CTA of a row's cluster decides alike, bins may be filled by
-// atomics, and a border is where it is in exact arithmetic unless two numbers agree to about
-// 2^-36.  (fp32 weights carry 2^-23 each: with the vocabulary's tens of thousands of small
-// weights near a border, one row in a hundred would be cut elsewhere.  GB300 has two fp64 lanes
-// per SM and clock, so fp64 weights would take several times longer than the loads.)
+// Weights and sums.  A logit is a grid point and a part of a cell, x = x_k + y, exactly;
+// its weight exp(x / T) is exp(x_k / T), one of 2047 entries of a table in whole numbers of 2^-44
+// made once a row to 2^-35, plus a correction of at most a 63rd of it, w (1 - exp(-y / T)), which
+// fp32 and the hardware's exp2 give to 2^-28 of w.  The whole numbers are summed exactly, the
+// corrections of a lane in fp32.  So a border or draw comes out as it does in 64 bits unless
+// two numbers agree to about 2^-28 of a single weight and 2^-36 of the sum.  (fp32 weights and sums
+// carry 2^-21: beside a vocabulary's tens of thousands of small weights, one row in a few hundred would
+// be cut or drawn elsewhere.  Weights as pairs of fp32 took 45 instructions each, three times as many;
+// GB300 has two fp64 lanes per SM and clock.)
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -28,11 +32,10 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kBins = 1024;
-constexpr int kBinsPerOctave = 32;  // of the first split: weights of a bin within 2.2 %
-constexpr int kList = 512;          // tokens that are sorted (at most one a thread)
-constexpr int kUnit = 45;           // a weight of 1 is 2^45
-constexpr int kSteps = 1024;        // table steps an octave
+constexpr int kCells = 2048;  // of the grid; the last one holds all logits whose weight is 0
+constexpr int kSplit = 512;   // bins of a cell that is split
+constexpr int kList = 512;    // tokens that are sorted (at most one a thread)
+constexpr int kUnit = 44;     // a weight of 1 is 2^44
 constexpr uint32_t kNone = 0xffffffffu;
 
 struct SampleArgs {
@@ -52,7 +55,7 @@ struct SampleArgs {
 };
 
 // ------------------------------------------------------------------------------ weights
-// 2^(j / 1024) = kCoarse[j / 32] * kFine[j % 32]; series of exp, in units of 2^-63 and 2^-62.
+// 2^(j / 1024) = coarse[j / 32] fine[j % 32]; series of exp, in units of 2^-63 and 2^-62.
 constexpr double exp_series(double y) {
     double term = 1.0, sum = 1.0;
     for (int n = 1; n < 24; ++n) {
@@ -73,63 +76,73 @@ struct Powers {
 };
 __device__ const Powers kPowers = Powers();
 
-// How a row's logits become weights: t = (x - top) / T log2(e), a pair of fp32.
-struct Scale {
-    float top, hi, lo;  // hi + lo = log2(e) / T
-    int drop;
-    const uint64_t *table;  // 2^(j / 1024) in units of 2^-46
+// 2^-(turns 2^-56) in units of 2^-(kUnit - drop), rounded: 2^-octaves 2^(j / 1024) (1 + q).
+__device__ __forceinline__ uint64_t power(uint64_t turns, int drop) {
+    constexpr uint64_t kOne = 1ull << 56;
+    const uint64_t left = kOne - (turns & (kOne - 1));  // up to the next octave
+    const int shift = 62 - kUnit + (int)(turns >> 56) + drop;
+    if (shift > 62) return 0;
+    uint64_t w = 1ull << 62;  // in units of 2^-62 of the octave below
+    if (left < kOne) {
+        const int j = (int)(left >> 46);
+        const float r = (float)(uint32_t)((left >> 22) & 0xffffffu) * 5.8207660913467407e-11f;  // 2^-34
+        const float q = r * __fmaf_rn(r, __fmaf_rn(r, 0.0555041087f, 0.240226507f), 0.693147181f);
+        w = __umul64hi(kPowers.coarse[j / 32], kPowers.fine[j % 32]);
+        w += __umul64hi(w, (uint64_t)__float2uint_rn(q * 2199023255552.f) << 23);  // q in units of 2^-41
+    }
+    return (w + (1ull << (shift - 1))) >> shift;
+}
 
-    // -1024 t rounded (0 .. 4000 * 1024, rising as x falls), the remainder of t and its low part.
-    __device__ __forceinline__ int steps(float x, float &rest, float &low) const {
-        // x - top and its rounding error, then the product with its own
-        const float d = __fsub_rn(x, top), b = __fsub_rn(d, x);
-        const float e = __fsub_rn(__fsub_rn(x, __fsub_rn(d, b)), __fadd_rn(top, b));
-        const float h = __fmul_rn(d, hi);
-        low = __fmaf_rn(e, hi, __fmaf_rn(d, lo, __fmaf_rn(d, hi, -h)));
-        const float c = fmaxf(h, -4000.f);
-        // the sum with 1.5 x 2^13 rounds to 2^-10 and leaves the whole number in the low bits
-        const float t = __fadd_rn(c, 12288.f);
-        rest = __fsub_rn(c, __fsub_rn(t, 12288.f));
-        return __float_as_int(12288.f) - __float_as_int(t);
+// A row's grid: steps g, a power of two from T / 62.75 on, so that 2047 of them span the 47 octaves in which
+// weights are not 0.
+struct Grid {
+    float base;        // taken off all logits: 0, or the largest where it is far from 0 (exact for all that count)
+    float low, high;   // what is left is cut to cells 0 .. kCells - 1
+    float magic;       // 1.5 * 2^23 steps: a sum with it is rounded to a grid point
+    float point;       // the grid point of the largest logit
+    float c, over;     // log2(e) / T and 1 / T
+    float unit;        // kUnit - drop
+    int zero;          // bits of point + magic
+
+    // The cell of a logit (0: the largest one's), what is left of it without the base, and its part of a cell.
+    __device__ __forceinline__ int cell(float x, float &y, float &part) const {
+        y = fminf(fmaxf(__fsub_rn(x, base), low), high);  // (NaN: low)
+        const float s = __fadd_rn(y, magic);
+        part = __fsub_rn(y, __fsub_rn(s, magic));
+        return (zero - __float_as_int(s)) & (kCells - 1);
     }
-    // 2^45 2^t, rounded to a multiple of 2^drop and over it.  2^t = 2^-whole 2^(j / 1024) (1 + q):
-    // |rest| <= 2^-11, so q's fp32 rounding is 2^-36 of the weight.
-    __device__ __forceinline__ uint64_t weight(int step, float rest, float low) const {
-        constexpr float k1 = (float)(0.693147180559945309 * (1ull << 42)), k2 = (float)(0.240226506959100712 * (1ull << 42)),
-                        k3 = (float)(0.0555041086648215800 * (1ull << 42));
-        const float q = __fmaf_rn(rest, __fmaf_rn(rest, __fmaf_rn(rest, k3, k2), k1), low * k1);
-        const int qi = __float2int_rn(q);  // units of 2^-42
-        const uint64_t w = table[-step & (kSteps - 1)];
-        const uint64_t full = w + (uint64_t)((int64_t)__mulhi((int)(w >> 16), qi) * 64);
-        const int shift = (step + kSteps - 1) / kSteps + drop;
-        return shift > kUnit + 1 ? 0 : ((full >> shift) + 1) >> 1;
+    __device__ __forceinline__ int cell(float x) const {
+        return (zero - __float_as_int(__fadd_rn(fminf(fmaxf(__fsub_rn(x, base), low), high), magic))) & (kCells - 1);
     }
-    __device__ __forceinline__ uint64_t weight(float x) const {
-        float rest, low;
-        const int step = steps(x, rest, low);
-        return weight(step, rest, low);
+    // What is to be added to the weight of a part's grid point: the hardware's exp2, to 2^-22, of the
+    // whole weight, in units, times 1 - exp(-part / T), |part / T| < 1 / 62.75.
+    __device__ __forceinline__ float rest(float y, float part) const {
+        float e;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmaf_rn(__fsub_rn(y, point), c, unit)));
+        const float z = part * over;
+        return e * (z * __fmaf_rn(z, __fmaf_rn(z, __fmaf_rn(z, -1.f / 24.f, 1.f / 6.f), -0.5f), 1.f));
     }
-    // 2^t in fp32, for the probabilities that are written
-    __device__ __forceinline__ float value(float x) const {
-        const float d = __fsub_rn(x, top), b = __fsub_rn(d, x);
-        const float e = __fsub_rn(__fsub_rn(x, __fsub_rn(d, b)), __fadd_rn(top, b));
-        const float h = __fmul_rn(d, hi);
-        const float low = __fmaf_rn(e, hi, __fmaf_rn(d, lo, __fmaf_rn(d, hi, -h)));
-        return h < -200.f ? 0.f : exp2f(h) * __fmaf_rn(low, 0.693147181f, 1.f);
-    }
-    __device__ __forceinline__ int bin(int step) const { return min(step / (kSteps / kBinsPerOctave), kBins - 1); }
+};
+
+// The sum of a lane's weights.  It is 0 if and only if all of them are: corrections of weights that
+// are 0 do not count.
+struct Sum {
+    uint64_t whole = 0;
+    float rest = 0.f;
+    __device__ __forceinline__ uint64_t total() const { return whole ? (uint64_t)max((long long)whole + __float2ll_rn(rest), 1ll) : 0; }
 };
 
 // ---------------------------------------------------------------------------- the order
-// Keys rise with logits; -0 and 0 are equal.
+// Keys rise with logits; -0 and 0 are equal, NaN is -inf.
 __device__ __forceinline__ uint32_t key_of(float x) {
-    const uint32_t b = __float_as_uint(x + 0.f);
+    const uint32_t b = __float_as_uint(fmaxf(x, -INFINITY) + 0.f);
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 __device__ __forceinline__ float logit_of(uint32_t key) { return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key); }
 
 // A token's place in the order as one number: falling logit, rising index.
 __device__ __forceinline__ uint64_t place_of(uint32_t key, int v) { return (uint64_t)~key << 32 | (uint32_t)v; }
+__device__ __forceinline__ float logit_at(uint64_t place) { return logit_of(~(uint32_t)(place >> 32)); }
 
 // The lowest key in [lo, hi] of which `holds` is true; it is false below some key, true above,
 // and true at hi.  All lanes of a warp, 32 keys at a time.
@@ -187,44 +200,60 @@ __device__ __forceinline__ uint64_t draw_goal(uint64_t sum, float u) {
     return u < 1.f ? fraction_of(sum, fmaxf(u, 0.f), cut) : sum - 1;
 }
 
-struct alignas(16) Part {
-    uint64_t mass, count;
+struct alignas(16) Part {  // a CTA's sums
+    uint64_t mass, count, cell_mass, all_mass;
 };
+// What the CTAs of a cluster tell each other; a place of its own for each step.
+enum { kTop, kCellSums, kCellBorder, kBins, kRuns, kExchanges };
 struct alignas(16) Border {
-    uint64_t mass_above, count_above;
-    uint32_t bin, count;
+    uint64_t mass_above, count_above, bin, count;
 };
 
 struct alignas(16) Shared {
-    uint64_t table[kSteps];
-    uint32_t hist[4][kBins];  // counts, and sums of the weights' lowest 15 bits, the next 15 and the rest
-    uint64_t own[kList];      // places gathered here, and of all CTAs
-    uint64_t all[kList];
-    Part part[2][kMaxCluster];
+    uint64_t table[kCells];
+    uint32_t cells[kCells];      // tokens in each
+    uint32_t hist[4][kSplit];    // of a cell that is split: counts, and sums of the weights' lowest 15 bits, the next 15 and the rest
+    uint64_t own[kList];         // places gathered here; then the sorted ones' weights
+    uint64_t all[kList];         // of all CTAs
+    Part part[kExchanges][kMaxCluster];
     Border border;
     uint64_t warp_mass[kWarps], warp_count[kWarps];
+    uint64_t run_mass[kWarps];   // of the runs' tokens before the cell of the border
+    uint64_t added[kMaxCluster]; // of the list's tokens that stay, by CTA
     uint64_t cut[2], cut_mass[2];
     uint32_t n_own;
-    uint32_t first;           // temperature 0
+    uint32_t first;              // temperature 0
+    Grid grid;
 };
+extern __shared__ __align__(16) char shared_bytes[];
+__device__ __forceinline__ Shared &shared() { return *reinterpret_cast<Shared *>(shared_bytes); }
 
 // ------------------------------------------------------------------- the cluster of a row
+// Another CTA's copy of a number in shared memory.  A CTA's own is never reached through the cluster's
+// window: those accesses are ordered by barriers of the cluster alone, and a cluster of one has none.
 __device__ __forceinline__ uint32_t remote(const void *p, int rank) {
     uint32_t a = (uint32_t)__cvta_generic_to_shared(p);
     asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(a) : "r"(rank));
     return a;
 }
-__device__ __forceinline__ void put(uint32_t to, uint64_t a, uint64_t b) {
-    asm volatile("st.shared::cluster.v2.u64 [%0], {%1, %2};" ::"r"(to), "l"(a), "l"(b) : "memory");
+__device__ __forceinline__ void put(uint64_t *p, uint64_t a, uint64_t b, int to, int rank) {
+    if (to == rank) {
+        p[0] = a;
+        p[1] = b;
+    } else {
+        asm volatile("st.shared::cluster.v2.u64 [%0], {%1, %2};" ::"r"(remote(p, to)), "l"(a), "l"(b) : "memory");
+    }
 }
-__device__ __forceinline__ uint32_t get32(uint32_t from) {
+__device__ __forceinline__ uint32_t get(const uint32_t *p, int from, int rank) {
+    if (from == rank) return *p;
     uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(from) : "memory");
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote(p, from)) : "memory");
     return v;
 }
-__device__ __forceinline__ uint64_t get64(uint32_t from) {
+__device__ __forceinline__ uint64_t get(const uint64_t *p, int from, int rank) {
+    if (from == rank) return *p;
     uint64_t v;
-    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(from) : "memory");
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(remote(p, from)) : "memory");
     return v;
 }
 
@@ -257,7 +286,6 @@ template <typename T>
 struct Row {
     const T *base;  // of padded entry 0, 16-byte aligned; entry v is padded entry v + pad
     int pad, end;   // padded entries pad .. end - 1 are the row's
-    bool only_inf;  // the largest logit is +inf: the others do not count
 
     __device__ __forceinline__ uint4 load(int at) const {
         if (at >= pad && at + kVec<T> <= end) return __ldg(reinterpret_cast<const uint4 *>(base + at));
@@ -275,13 +303,7 @@ struct Row {
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
-    __device__ __forceinline__ float clean(float x) const {
-        x = fmaxf(x, -INFINITY);  // NaN
-        return only_inf ? (x == INFINITY ? 0.f : -INFINITY) : x;
-    }
-    __device__ __forceinline__ float at(int p) const {
-        return p >= pad && p < end ? clean(entry(base + p)) : -INFINITY;
-    }
+    __device__ __forceinline__ float at(int p) const { return p >= pad && p < end ? entry(base + p) : -INFINITY; }
     // f(x, padded index) for the entries of a warp's run [begin, stop), both multiples of 8
     template <typename F>
     __device__ __forceinline__ void each(int begin, int stop, int lane, F f) const {
@@ -296,41 +318,658 @@ struct Row {
             float x[N];
             unpack(raw, x);
 #pragma unroll
-            for (int i = 0; i < N; ++i) f(clean(x[i]), p + i);
+            for (int i = 0; i < N; ++i) f(x[i], p + i);
         }
     }
 };
 
+// One logit's weight.
+__device__ __forceinline__ uint64_t weight_of(const Grid &grid, float x) {
+    float y, part;
+    const uint64_t w = shared().table[grid.cell(x, y, part)];
+    return w + (uint64_t)__float2ll_rn(grid.rest(y, part));
+}
+
+// ------------------------------------------------------------------------ steps of a CTA
+// The steps are functions of their own (not inlined): each has the registers to itself, what a row's CTAs agree on
+// lies in shared memory between them.
+
+// Where a CTA stands: its row's cluster, and a warp's run.
+struct Here {
+    int C, rank, begin, stop;
+};
+
+__device__ __forceinline__ void cluster_arrive(int C) {
+    __syncwarp();
+    if (C > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait(int C) {
+    if (C > 1)
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    else
+        __syncthreads();
+}
+__device__ __forceinline__ void meet(int C) {
+    cluster_arrive(C);
+    cluster_wait(C);
+}
+
+// The CTAs' sums: every CTA writes its own into all of them, and they meet.  `mine`: the same in the first warp's
+// lanes.
+__device__ __forceinline__ void exchange(const Here &h, int step, const Part &mine) {
+    Part &to = shared().part[step][h.rank];
+    if (threadIdx.x < h.C) {
+        put(&to.mass, mine.mass, mine.count, threadIdx.x, h.rank);
+        put(&to.cell_mass, mine.cell_mass, mine.all_mass, threadIdx.x, h.rank);
+    }
+    meet(h.C);
+}
+
+// Inclusive sums by thread; the warps' sums are left in warp_mass.
+__device__ __forceinline__ uint64_t block_scan(uint64_t mass) {
+    Shared &sh = shared();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    mass = warp_scan(mass, lane);
+    __syncthreads();
+    if (lane == 31) sh.warp_mass[warp] = mass;
+    __syncthreads();
+    const uint64_t m = warp_scan(lane < kWarps ? sh.warp_mass[lane] : 0, lane);
+    const uint64_t before = __shfl_sync(0xffffffffu, m, max(warp - 1, 0));
+    return warp > 0 ? mass + before : mass;
+}
+// The sum of a number that each warp has left in an array.
+__device__ __forceinline__ uint64_t over_warps(const uint64_t *of) {
+    const int lane = threadIdx.x & 31;
+    return warp_sum(lane < kWarps ? of[lane] : 0);
+}
+
+// One number a thread, rising in the first `n` threads (the others have ~0); n <= kList.
+__device__ __noinline__ uint64_t sort(uint64_t mine, int n) {
+    Shared &sh = shared();
+    const int tid = threadIdx.x;
+    const int size = n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : n <= 256 ? 256 : kList;
+#pragma unroll 1
+    for (int k = 2; k <= size; k *= 2) {
+#pragma unroll 1
+        for (int j = k / 2; j > 0; j /= 2) {
+            uint64_t other;
+            if (j >= 32) {
+                __syncthreads();
+                sh.all[tid] = mine;
+                __syncthreads();
+                other = sh.all[tid ^ j];
+            } else {
+                other = __shfl_xor_sync(0xffffffffu, mine, j);
+            }
+            const bool lower = ((tid & j) == 0) == ((tid & k) == 0);
+            mine = lower ? min(mine, other) : max(mine, other);
+        }
+    }
+    __syncthreads();
+    return mine;
+}
+
+// The key of a row's largest logit.
+template <typename T>
+__device__ __noinline__ uint32_t find_top(Row<T> row, Here h) {
+    Shared &sh = shared();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float m = -INFINITY;
+    row.each(h.begin, h.stop, lane, [&](float x, int) { m = fmaxf(m, x); });
+    const uint32_t k = __reduce_max_sync(0xffffffffu, key_of(m));
+    if (lane == 0) sh.warp_count[warp] = k;
+    __syncthreads();
+    cluster_wait(h.C);
+    exchange(h, kTop, Part{__reduce_max_sync(0xffffffffu, lane < kWarps ? (uint32_t)sh.warp_count[lane] : 0), 0, 0, 0});
+    uint32_t top = 0;
+    for (int c = 0; c < h.C; ++c) top = max(top, (uint32_t)sh.part[kTop][c].mass);
+    return top;
+}
+
+// Temperature 0: the first place of the largest logit.
+template <typename T>
+__device__ __noinline__ int find_first(Row<T> row, Here h, float top) {
+    Shared &sh = shared();
+    const int lane = threadIdx.x & 31;
+    uint32_t first = kNone;
+    row.each(h.begin, h.stop, lane, [&](float x, int p) {
+        if (x == top) first = min(first, (uint32_t)p);
+    });
+    first = __reduce_min_sync(0xffffffffu, first);
+    if (lane == 0) atomicMin(&sh.first, first);
+    __syncthreads();
+    exchange(h, kRuns, Part{sh.first, 0, 0, 0});
+    for (int c = 0; c < h.C; ++c) first = min(first, (uint32_t)sh.part[kRuns][c].mass);
+    return (int)first;
+}
+
+// log2(e) / T as a pair: the remainder of the division is exact.  T is cut to 2^-60 .. 2^80.
+__device__ __forceinline__ float2 scale_of(float temperature) {
+    const float t = fminf(fmaxf(temperature, 8.6736174e-19f), 1.2089258e24f);
+    constexpr float kHi = 1.44269502f, kLo = 1.92596299e-8f;
+    const float hi = __fdiv_rn(kHi, t);
+    return make_float2(hi, __fdiv_rn(__fadd_rn(__fmaf_rn(-hi, t, kHi), kLo), t));
+}
+
+// A row's grid and its table.
+__device__ __noinline__ void make_grid(float top, float temperature, int drop) {
+    Shared &sh = shared();
+    const float t = fminf(fmaxf(temperature, 8.6736174e-19f), 1.2089258e24f);
+    const float2 scale = scale_of(temperature);
+    const float step = __uint_as_float((__float_as_uint(t * (1.f / 62.75f)) + 0x7fffffu) & 0xff800000u);
+    Grid g;
+    g.base = fabsf(top) > step * 1048576.f ? top : 0.f;
+    g.high = __fsub_rn(top, g.base);
+    g.magic = step * 12582912.f;
+    const float s = __fadd_rn(g.high, g.magic);
+    g.zero = __float_as_int(s);
+    g.point = __fsub_rn(s, g.magic);
+    g.low = g.point - step * (kCells - 1);
+    g.c = scale.x;
+    g.over = __fdiv_rn(1.f, t);
+    g.unit = (float)(kUnit - drop);
+    if (threadIdx.x == 0) sh.grid = g;
+    const uint64_t turns = (uint64_t)(scale.x * step * 72057594037927936.f) + (uint64_t)(int64_t)(scale.y * step * 72057594037927936.f);
+    for (int k = threadIdx.x; k < kCells; k += kThreads) sh.table[k] = k < kCells - 1 ? power(k * turns, drop) : 0;
+    __syncthreads();
+}
+
+template <typename T>
+__device__ __noinline__ void count_cells(Row<T> row, Here h) {
+    Shared &sh = shared();
+    const Grid grid = sh.grid;
+    row.each(h.begin, h.stop, threadIdx.x & 31, [&](float x, int) {
+        const int k = grid.cell(x);
+        if (k < kCells - 1) atomicAdd(&sh.cells[k], 1u);
+    });
+    meet(h.C);
+}
+
+// The cell of a border, left in `border` with the tokens before it and in it: the first whose tokens (counting), or whose tokens'
+// weights at their grid points, reach `want` together with those before; want 0: top_p of all weights.  It is cut to
+// `limit`, whose own numbers are not known then (kNone), but for the last cell's.
+__device__ __noinline__ void find_cell(Here h, bool counting, uint64_t want, float top_p, int limit, int V) {
+    Shared &sh = shared();
+    constexpr int kEach = kCells / kThreads;  // cells of a thread, at most
+    const int tid = threadIdx.x, share = kCells / h.C, each = max(1, share / kThreads), at = h.rank * share + tid * each;
+    uint64_t mass[kEach], count[kEach], own_mass = 0, own_count = 0;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+        mass[e] = count[e] = 0;
+        if (e >= each || tid * each >= share) continue;
+        for (int c = 0; c < h.C; ++c) count[e] += get(&sh.cells[at + e], c, h.rank);
+        mass[e] = count[e] * sh.table[at + e];
+        own_mass += mass[e];
+        own_count += count[e];
+    }
+    if (tid == 0) sh.border = Border{0, kNone, (uint64_t)limit, kNone};
+    uint64_t before_mass = block_scan(own_mass) - own_mass;
+    const uint64_t sum_mass = over_warps(sh.warp_mass);
+    uint64_t before_count = block_scan(own_count) - own_count;
+    exchange(h, kCellSums, Part{sum_mass, over_warps(sh.warp_mass), 0, 0});
+    uint64_t all_mass = 0, all_count = 0;
+    for (int c = 0; c < h.C; ++c) {
+        const Part p = sh.part[kCellSums][c];
+        all_mass += p.mass;
+        all_count += p.count;
+        if (c < h.rank) {
+            before_mass += p.mass;
+            before_count += p.count;
+        }
+    }
+    const uint64_t goal = want ? want : top_p_goal(all_mass, top_p);
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+        if (e >= each || tid * each >= share) continue;
+        const uint64_t before = counting ? before_count : before_mass;
+        if (at + e < limit && before < goal && before + (counting ? count[e] : mass[e]) >= goal)
+            for (int c = 0; c < h.C; ++c) {
+                put(&sh.border.mass_above, 0, before_count, c, h.rank);
+                put(&sh.border.bin, at + e, count[e], c, h.rank);
+            }
+        before_mass += mass[e];
+        before_count += count[e];
+    }
+    meet(h.C);
+    if (tid == 0 && sh.border.bin == kCells - 1) {  // beyond all weights
+        sh.border.count_above = all_count;
+        sh.border.count = V - all_count;
+    }
+    __syncthreads();
+}
+
+// The sums before cell `b` (left by run in run_mass, by CTA in part[kCellBorder]) and its tokens, gathered in own; all_up_to: instead
+// all tokens up to the cell; all_wanted: the sum of all weights as well.  Tokens behind `last` in the order do not count.
+template <typename T>
+__device__ __noinline__ void sum_and_gather(Row<T> row, Here h, int b, bool all_up_to, bool all_wanted, uint64_t last) {
+    Shared &sh = shared();
+    const Grid grid = sh.grid;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    Sum before, all;
+    uint64_t inside = 0;
+    uint32_t n_inside = 0;
+    const int summed = all_up_to ? 0 : b;
+    row.each(h.begin, h.stop, lane, [&](float x, int p) {
+        float y, part;
+        const int k = grid.cell(x, y, part);
+        if (k == b || (all_up_to && k < b)) {
+            const uint64_t place = place_of(key_of(x), p);
+            if (place <= last && p >= row.pad && p < row.end) {
+                const uint32_t i = atomicAdd(&sh.n_own, 1u);
+                if (i < kList) sh.own[i] = place;
+                inside += weight_of(grid, x);
+                ++n_inside;
+            }
+        }
+        if (all_wanted || k < summed) {
+            const uint64_t w = sh.table[k];
+            const float rest = grid.rest(y, part);
+            all.whole += w;
+            all.rest += rest;
+            if (k < summed) {
+                before.whole += w;
+                before.rest += rest;
+            }
+        }
+    });
+    const uint64_t run = warp_sum(before.total()), in = warp_sum(inside), total = warp_sum(all.total());
+    n_inside = __reduce_add_sync(0xffffffffu, n_inside);
+    __syncthreads();
+    if (lane == 0) {
+        sh.run_mass[warp] = run;
+        sh.warp_mass[warp] = in;
+        sh.warp_count[warp] = total;
+        sh.all[warp] = n_inside;
+    }
+    __syncthreads();
+    exchange(h, kCellBorder, Part{over_warps(sh.run_mass), over_warps(sh.all), over_warps(sh.warp_mass), over_warps(sh.warp_count)});
+}
+
+// A cell of more than kList tokens, split on over their keys, and over the indices of equal keys, until a bin of the border has
+// no more: its tokens are gathered in own, what comes before them is left in border.
+template <typename T>
+__device__ __noinline__ void split_cell(Row<T> row, Here h, int b, bool counting, uint64_t want, uint64_t base_mass, uint64_t base_count,
+                                        uint32_t top_key, uint64_t last) {
+    Shared &sh = shared();
+    const Grid grid = sh.grid;
+    const int tid = threadIdx.x, lane = tid & 31;
+    auto up_to = [&](int most) {
+        return first_key(key_of(-INFINITY), top_key, lane, [&](uint32_t key) { return grid.cell(logit_of(key)) <= most; });
+    };
+    uint32_t lo = up_to(b), hi = b > 0 ? up_to(b - 1) - 1 : top_key;
+    int first = row.pad, final = row.end - 1;
+#pragma unroll 1
+    for (;;) {
+        const bool single = lo == hi;
+        const uint32_t width = single ? (uint32_t)(final - first) : hi - lo;
+        const int shift = max(0, 32 - __clz(width) - 9);
+        __syncthreads();
+        for (int i = tid; i < 4 * kSplit; i += kThreads) (&sh.hist[0][0])[i] = 0;
+        if (tid == 0) {
+            sh.n_own = 0;
+            sh.border = Border{base_mass, base_count, kSplit - 1, 0};
+        }
+        __syncthreads();
+        auto bin_of = [&](uint32_t key, int p) {  // -1: none
+            if (key < lo || key > hi || p < first || p > final) return -1;
+            return (int)(((single ? (uint32_t)(p - first) : hi - key) >> shift) & (kSplit - 1));
+        };
+        row.each(h.begin, h.stop, lane, [&](float x, int p) {
+            const uint32_t key = key_of(x);
+            const int at = bin_of(key, p);
+            if (at < 0 || place_of(key, p) > last) return;
+            const uint64_t w = weight_of(grid, x);
+            atomicAdd(&sh.hist[0][at], 1u);
+            atomicAdd(&sh.hist[1][at], (uint32_t)w & 0x7fffu);
+            atomicAdd(&sh.hist[2][at], (uint32_t)(w >> 15) & 0x7fffu);
+            atomicAdd(&sh.hist[3][at], (uint32_t)(w >> 30));
+        });
+        meet(h.C);
+        const int share = kSplit / h.C, mine = h.rank * share + tid;
+        uint64_t mass = 0, count = 0;
+        if (tid < share)
+            for (int c = 0; c < h.C; ++c) {
+                count += get(&sh.hist[0][mine], c, h.rank);
+                mass += get(&sh.hist[1][mine], c, h.rank) + ((uint64_t)get(&sh.hist[2][mine], c, h.rank) << 15) +
+                        ((uint64_t)get(&sh.hist[3][mine], c, h.rank) << 30);
+            }
+        uint64_t before_mass = block_scan(mass) - mass;
+        const uint64_t sum_mass = over_warps(sh.warp_mass);
+        uint64_t before_count = block_scan(count) - count;
+        exchange(h, kBins, Part{sum_mass, over_warps(sh.warp_mass), 0, 0});
+        before_mass += base_mass;
+        before_count += base_count;
+        for (int c = 0; c < h.rank; ++c) {
+            before_mass += sh.part[kBins][c].mass;
+            before_count += sh.part[kBins][c].count;
+        }
+        const uint64_t before = counting ? before_count : before_mass;
+        if (tid < share && before < want && before + (counting ? count : mass) >= want)
+            for (int c = 0; c < h.C; ++c) {
+                put(&sh.border.mass_above, before_mass, before_count, c, h.rank);
+                put(&sh.border.bin, mine, count, c, h.rank);
+            }
+        meet(h.C);
+        const int bin = (int)sh.border.bin;
+        base_mass = sh.border.mass_above;
+        base_count = sh.border.count_above;
+        if (sh.border.count <= kList) {
+            row.each(h.begin, h.stop, lane, [&](float x, int p) {
+                const uint32_t key = key_of(x);
+                if (bin_of(key, p) != bin) return;
+                const uint64_t place = place_of(key, p);
+                if (place > last) return;
+                const uint32_t i = atomicAdd(&sh.n_own, 1u);
+                if (i < kList) sh.own[i] = place;
+            });
+            meet(h.C);
+            return;
+        }
+        if (!single) {
+            hi -= (uint32_t)bin << shift;
+            lo = max(lo, hi - (uint32_t)((1ull << shift) - 1));
+        } else {
+            first += bin << shift;
+            final = min(final, first + (int)((1ull << shift) - 1));
+        }
+    }
+}
+
+// All CTAs' gathered places, sorted, in `all` of every CTA, and their weights in `own`; how many.
+__device__ __noinline__ int join_lists(Here h) {
+    Shared &sh = shared();
+    const Grid grid = sh.grid;
+    const int tid = threadIdx.x;
+    int n = 0;
+    uint64_t mine = ~0ull;
+    for (int c = 0; c < h.C; ++c) {
+        const int m = (int)min(get(&sh.n_own, c, h.rank), (uint32_t)kList);
+        if (tid >= n && tid < n + m) mine = get(&sh.own[tid - n], c, h.rank);
+        n += m;
+    }
+    n = min(n, kList);
+    cluster_arrive(h.C);  // has read the others' lists
+    mine = sort(mine, n);
+    const uint64_t w = tid < n ? weight_of(grid, logit_at(mine)) : 0;
+    cluster_wait(h.C);
+    __syncthreads();
+    if (tid == 0) sh.n_own = 0;
+    sh.all[tid] = mine;
+    sh.own[tid] = w;
+    __syncthreads();
+    return n;
+}
+
+// What is found of top-k and top-p.
+struct Kept {
+    uint64_t last;      // the last place that stays
+    uint64_t mass;      // of what stays; 0: not known
+    int n;              // tokens in the list
+    bool complete;      // the list has all that stays
+    bool runs;          // run_mass, part[kCellBorder] and the list give the sums of what stays
+};
+
+template <typename T>
+__device__ __noinline__ Kept find_borders(Row<T> row, Here h, bool by_count, bool by_mass, int top_k, float top_p, int V, uint32_t top_key) {
+    Shared &sh = shared();
+    const int tid = threadIdx.x;
+    Kept kept{~0ull, 0, 0, false, false};
+    count_cells(row, h);
+    int limit = by_count ? kCells - 1 : kCells - 2;  // the last cell that a border can be in
+#pragma unroll 1
+    for (int round = by_count ? 0 : 1; round < (by_mass ? 2 : 1); ++round) {
+        const bool counting = round == 0, all_wanted = !counting && kept.mass == 0;
+        uint64_t want = counting ? (uint64_t)top_k : all_wanted ? 0 : top_p_goal(kept.mass, top_p);
+        find_cell(h, counting, want, top_p, limit, V);
+        int b = (int)sh.border.bin, moved = 0;
+        const uint64_t cells_before = sh.border.count_above;
+        bool all_up_to = cells_before + sh.border.count <= kList, settled = counting;
+        uint64_t above, cell_mass, n_cell;
+#pragma unroll 1
+        for (;;) {
+            sum_and_gather(row, h, b, all_up_to, all_wanted, kept.last);
+            uint64_t all_mass = 0;
+            above = cell_mass = n_cell = 0;
+            for (int c = 0; c < h.C; ++c) {
+                const Part p = sh.part[kCellBorder][c];
+                above += p.mass;
+                n_cell += p.count;
+                cell_mass += p.cell_mass;
+                all_mass += p.all_mass;
+            }
+            if (all_wanted) want = top_p_goal(all_mass, top_p);
+            if (all_up_to && n_cell > kList) {
+                all_up_to = false;
+            } else {
+                // The cells' mean weights may have missed the cell.  (A sum's rounding must not send it to and fro: between
+                // two cells it is the end of the first.)
+                const int next = settled || (want > above && want <= above + cell_mass) ? 0 : want <= above ? -1 : 1;
+                settled |= moved != 0 && next == -moved;
+                if (next == 0 || (settled && next > 0) || b + next < 0 || b + next > limit) break;
+                moved = next;
+                b += next;
+            }
+            __syncthreads();
+            if (tid == 0) sh.n_own = 0;
+            meet(h.C);
+        }
+        if (!counting) want = min(max(want, above + 1), above + cell_mass);
+        uint64_t base_mass = above, base_count = all_up_to ? 0 : cells_before;
+        const bool split = n_cell > kList;
+        if (split) {
+            split_cell(row, h, b, counting, want, base_mass, base_count, top_key, kept.last);
+            base_mass = sh.border.mass_above;
+            base_count = sh.border.count_above;
+        }
+        const int n = join_lists(h);
+        const uint64_t mine = sh.all[tid], w = sh.own[tid], upto = base_mass + block_scan(w);
+        const bool real = tid < n;
+        if (counting && real && base_count + tid + 1 == want) {
+            sh.cut[0] = mine;
+            sh.cut_mass[0] = upto;
+        }
+        __syncthreads();
+        bool found = true;
+        if (counting) {
+            kept.last = sh.cut[0];
+            kept.mass = sh.cut_mass[0];
+            limit = b;
+            if (by_mass) {
+                want = top_p_goal(kept.mass, top_p);
+                found = want > base_mass;  // else the border of top-p is before this list
+            }
+        }
+        if (by_mass && found) {
+            const bool here = real && upto >= want && upto - w < want, any = __syncthreads_or(here);
+            if (here || (!any && tid == max(n - 1, 0))) {
+                sh.cut[1] = mine;
+                sh.cut_mass[1] = upto;
+            }
+            __syncthreads();
+            kept.last = sh.cut[1];
+            kept.mass = sh.cut_mass[1];
+            round = 1;
+        }
+        kept.n = n;
+        kept.complete = all_up_to && found;
+        kept.runs = !split && !all_up_to && found;
+    }
+    return kept;
+}
+
+// The lowest key whose weight stays by min-p.
+__device__ __noinline__ uint32_t find_min_key(float min_p, uint64_t most, uint32_t top_key) {
+    const Grid grid = shared().grid;
+    bool cut = false;
+    const uint64_t least = min_p < 1.f ? max((uint64_t)1, fraction_of(most, min_p, cut) + cut) : most;
+    return first_key(key_of(-INFINITY), top_key, threadIdx.x & 31, [&](uint32_t key) { return weight_of(grid, logit_of(key)) >= least; });
+}
+
+// The sums of what stays: by run in warp_mass, by CTA in added; all of it.
+template <typename T>
+__device__ __noinline__ uint64_t sum_runs(Row<T> row, Here h, Kept kept, int run) {
+    Shared &sh = shared();
+    const Grid grid = sh.grid;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint64_t own = 0;
+    if (kept.runs) {
+        // before the border's cell they are known; the list's tokens are added, run by run and CTA by CTA
+        uint64_t cta = 0;
+        for (int base = 0; base < kept.n; base += 32) {
+            const uint64_t place = sh.all[base + lane], w = place <= kept.last ? sh.own[base + lane] : 0;
+            const int of = (int)((uint32_t)place & 0x7fffffffu) / run;
+            if (of == h.rank * kWarps + warp) own += w;
+            if (of / kWarps == warp) cta += w;
+        }
+        own = sh.run_mass[warp] + warp_sum(own);
+        cta = warp_sum(cta);
+        if (lane == 0 && warp < h.C) sh.added[warp] = sh.part[kCellBorder][warp].mass + cta;
+        __syncthreads();
+        if (lane == 0) sh.warp_mass[warp] = own;
+        __syncthreads();
+    } else {
+        Sum s;
+        row.each(h.begin, h.stop, lane, [&](float x, int p) {
+            if (place_of(key_of(x), p) > kept.last) return;
+            float y, part;
+            s.whole += sh.table[grid.cell(x, y, part)];
+            s.rest += grid.rest(y, part);
+        });
+        own = warp_sum(s.total());
+        __syncthreads();
+        if (lane == 0) sh.warp_mass[warp] = own;
+        __syncthreads();
+        exchange(h, kRuns, Part{over_warps(sh.warp_mass), 0, 0, 0});
+        if (threadIdx.x < h.C) sh.added[threadIdx.x] = sh.part[kRuns][threadIdx.x].mass;
+        __syncthreads();
+    }
+    uint64_t sum = 0;
+    for (int c = 0; c < h.C; ++c) sum += sh.added[c];
+    return sum;
+}
+
+// A token and its probability.
+struct Drawn {
+    int p;  // padded index, -1: not in this thread
+    float probability;
+};
+
+// The draw from a list that has all that stays.
+__device__ __noinline__ Drawn draw_from_list(Kept kept, float u) {
+    Shared &sh = shared();
+    const Grid grid = sh.grid;
+    const int tid = threadIdx.x;
+    const uint64_t place = sh.all[tid];
+    const bool real = tid < kept.n && place <= kept.last;
+    const int n = __syncthreads_count(real);
+    const uint64_t by_index = sort(real ? place << 32 | place >> 32 : ~0ull, n);
+    const uint64_t w = tid < n ? weight_of(grid, logit_of(~(uint32_t)by_index)) : 0;
+    const uint64_t upto = block_scan(w), sum = over_warps(sh.warp_mass), goal = draw_goal(sum, u);
+    const bool here = w > 0 && upto > goal && upto - w <= goal;
+    return Drawn{here ? (int)(by_index >> 32) : -1, __fdiv_rn((float)w, (float)sum)};
+}
+
+// The draw from the runs: the CTA and run that hold its place, a thread's piece of the run, an entry.
+template <typename T>
+__device__ __noinline__ Drawn draw_from_runs(Row<T> row, Here h, Kept kept, uint64_t sum, float u, int run) {
+    Shared &sh = shared();
+    const Grid grid = sh.grid;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const uint64_t goal = draw_goal(sum, u);
+    uint64_t before = 0;
+    for (int c = 0; c < h.rank; ++c) before += sh.added[c];
+    Drawn drawn{-1, 0.f};
+    if (goal < before || goal - before >= sh.added[h.rank]) return drawn;
+    const uint64_t upto = before + warp_scan(lane < kWarps ? sh.warp_mass[lane] : 0, lane);
+    const int of = min(max(__ffs(__ballot_sync(0xffffffffu, upto > goal)) - 1, 0), kWarps - 1);
+    const uint64_t up = __shfl_sync(0xffffffffu, upto, max(of - 1, 0));
+    if (of > 0) before = up;
+    const int from = (h.rank * kWarps + of) * run, each = (run + kThreads - 1) / kThreads;
+    const int b = from + tid * each, e = min(min(b + each, from + run), row.end);
+    auto entry_weight = [&](int p) {
+        const float x = row.at(p);
+        return place_of(key_of(x), p) <= kept.last ? weight_of(grid, x) : 0;
+    };
+    uint64_t piece = 0;
+    for (int p = b; p < e; ++p) piece += entry_weight(p);
+    const uint64_t place = block_scan(piece);
+    // (single weights may add up to a little less than the run's sum)
+    const uint64_t left = min(goal - before, over_warps(sh.warp_mass) - 1);
+    if (place > left && place - piece <= left) {
+        uint64_t at = place - piece;
+        for (int p = b; p < e; ++p) {
+            const uint64_t w = entry_weight(p);
+            at += w;
+            if (at > left) {
+                drawn = Drawn{p, __fdiv_rn((float)w, (float)sum)};
+                break;
+            }
+        }
+    }
+    return drawn;
+}
+
+// ------------------------------------------------------------------------------ the kernel
 enum { kDraw = 0, kProbsF32 = 1, kProbsBf16 = 2 };
+
+// A row's probabilities, probability(x, padded index), written by runs.
+template <typename T, int OUT, typename F>
+__device__ __forceinline__ void write_row(const SampleArgs &a, const Row<T> &row, const Here &h, int64_t r, F probability) {
+    constexpr int N = kVec<T>, kSize = OUT == kProbsF32 ? 4 : 2;
+    char *out_row = static_cast<char *>(a.probs) + (r * a.p_stride - row.pad) * kSize;  // of padded entry 0
+    const bool vector = ((uintptr_t)out_row & (N * kSize - 1) & 15) == 0;
+    for (int p = h.begin + (threadIdx.x & 31) * N; p < h.stop; p += 32 * N) {
+        float x[N], y[N];
+        unpack(row.load(p), x);
+#pragma unroll
+        for (int i = 0; i < N; ++i) y[i] = probability(x[i], p + i);
+        const bool whole = vector && p >= row.pad && p + N <= row.end;
+        if constexpr (OUT == kProbsF32) {
+            float *to = reinterpret_cast<float *>(out_row) + p;
+            if (whole) {
+#pragma unroll
+                for (int i = 0; i < N; i += 4) *reinterpret_cast<float4 *>(to + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    if (p + i >= row.pad && p + i < row.end) to[i] = y[i];
+            }
+        } else {
+            uint32_t w[N / 2];
+#pragma unroll
+            for (int i = 0; i < N; i += 2) {
+                const __nv_bfloat162 two = __floats2bfloat162_rn(y[i], y[i + 1]);
+                w[i / 2] = *reinterpret_cast<const uint32_t *>(&two);
+            }
+            uint16_t *to = reinterpret_cast<uint16_t *>(out_row) + p;
+            if (whole) {
+                if constexpr (N == 8)
+                    *reinterpret_cast<uint4 *>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+                else
+                    *reinterpret_cast<uint2 *>(to) = make_uint2(w[0], w[1]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    if (p + i >= row.pad && p + i < row.end) to[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+            }
+        }
+    }
+}
 
 template <typename T, int OUT>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ SampleArgs a) {
-    __shared__ Shared sh;
-    const int C = a.cluster;
-    auto cluster_arrive = [&] {
-        __syncwarp();
-        if (C > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    };
-    auto cluster_wait = [&] {
-        if (C > 1)
-            asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-        else
-            __syncthreads();
-    };
-    auto meet = [&] {
-        cluster_arrive();
-        cluster_wait();
-    };
-    cluster_arrive();  // another CTA's shared memory may be written once it runs
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int r = blockIdx.x / C, rank = blockIdx.x % C;
-    for (int j = tid; j < kSteps; j += kThreads)
-        // units of 2^-61 from the product's upper half, then of 2^-46
-        sh.table[j] = (__umul64hi(kPowers.coarse[j / 32], kPowers.fine[j % 32]) + (1ull << 14)) >> 15;
-    auto clear_bins = [&] {
-        for (int i = tid; i < 4 * kBins; i += kThreads) (&sh.hist[0][0])[i] = 0;
-    };
-    clear_bins();
+    Shared &sh = shared();
+    const int tid = threadIdx.x;
+    const int64_t r = blockIdx.x / a.cluster;
+    Here h;
+    h.C = a.cluster;
+    h.rank = (int)(blockIdx.x % a.cluster);
+    cluster_arrive(h.C);  // another CTA's shared memory may be written once it runs
+    for (int i = tid; i < kCells; i += kThreads) sh.cells[i] = 0;
+    if (tid == 0) {
+        sh.n_own = 0;
+        sh.first = kNone;
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -343,467 +982,82 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         row.pad = (int)(((uintptr_t)x & 15) / sizeof(T));
         row.base = x - row.pad;
         row.end = row.pad + a.V;
-        row.only_inf = false;
     }
-    const int begin = (rank * kWarps + warp) * a.run, stop = min((row.end + 7) / 8 * 8, begin + a.run);
-    // a row's outputs: probability p of padded entry `at`
-    char *out_row = nullptr;
-    int out_size = 0;
-    bool out_vector = false;
-    if (OUT != kDraw) {
-        out_size = OUT == kProbsF32 ? 4 : 2;
-        out_row = static_cast<char *>(a.probs) + (r * a.p_stride - row.pad) * out_size;
-        out_vector = ((uintptr_t)out_row & (kVec<T> * out_size - 1) & 15) == 0;
-    }
-    auto write_row = [&](auto probability) {
-        constexpr int N = kVec<T>;
-        for (int p = begin + lane * N; p < stop; p += 32 * N) {
-            float x[N], y[N];
-            unpack(row.load(p), x);
-#pragma unroll
-            for (int i = 0; i < N; ++i) y[i] = probability(row.clean(x[i]), p + i);
-            if (OUT == kProbsF32) {
-                float *to = reinterpret_cast<float *>(out_row) + p;
-                if (out_vector && p >= row.pad && p + N <= row.end) {
-#pragma unroll
-                    for (int i = 0; i < N; i += 4) *reinterpret_cast<float4 *>(to + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < N; ++i)
-                        if (p + i >= row.pad && p + i < row.end) to[i] = y[i];
-                }
-            } else {
-                uint32_t w[N / 2];
-#pragma unroll
-                for (int i = 0; i < N; i += 2) {
-                    const __nv_bfloat162 two = __floats2bfloat162_rn(y[i], y[i + 1]);
-                    w[i / 2] = *reinterpret_cast<const uint32_t *>(&two);
-                }
-                uint16_t *to = reinterpret_cast<uint16_t *>(out_row) + p;
-                if (out_vector && p >= row.pad && p + N <= row.end) {
-                    if constexpr (N == 8)
-                        *reinterpret_cast<uint4 *>(to) = make_uint4(w[0], w[1], w[2], w[3]);
-                    else
-                        *reinterpret_cast<uint2 *>(to) = make_uint2(w[0], w[1]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < N; ++i)
-                        if (p + i >= row.pad && p + i < row.end) to[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
-                }
-            }
-        }
-    };
-    auto give = [&](int v, float p) {  // one thread of the cluster
-        if (OUT == kDraw) {
-            a.tokens[r] = v;
-            if (a.token_probs) a.token_probs[r] = p;
-        }
+    h.begin = (h.rank * kWarps + (tid >> 5)) * a.run;
+    h.stop = min((row.end + 7) / 8 * 8, h.begin + a.run);
+    auto give = [&](int p, float probability) {  // one thread of the cluster
+        a.tokens[r] = p - row.pad;
+        if (a.token_probs) a.token_probs[r] = probability;
     };
     auto refuse = [&](int flag) {  // every CTA of the cluster alike
-        if (rank == 0 && tid == 0) {
+        if (h.rank == 0 && tid == 0) {
             if (a.err_flag) atomicOr(a.err_flag, flag);
-            give(-1, 0.f);
+            if (OUT == kDraw) give(row.pad - 1, 0.f);
         }
-        if (OUT != kDraw) write_row([](float, int) { return 0.f; });
+        if constexpr (OUT != kDraw) write_row<T, OUT>(a, row, h, r, [](float, int) { return 0.f; });
     };
     if (!(temperature >= 0.f && temperature <= 3.402823466e38f) || top_p != top_p || min_p != min_p) {
-        cluster_wait();
+        cluster_wait(h.C);
         refuse(PA_FLAG_SAMPLING);
         return;
     }
-
-    // The CTAs' sums of two numbers: every CTA writes its own into all of them, and they meet.
-    int turn = 0;
-    auto exchange = [&](uint64_t mass, uint64_t count) {  // in the first warp; then part[turn ^ 1]
-        if (warp == 0 && lane < C) put(remote(&sh.part[turn][rank], lane), mass, count);
-        meet();
-        turn ^= 1;
-    };
-    auto sum_and_exchange = [&](uint64_t mass) {
-        mass = warp_sum(mass);
-        if (lane == 0) sh.warp_mass[warp] = mass;
-        __syncthreads();
-        exchange(warp_sum(warp == 0 && lane < kWarps ? sh.warp_mass[lane] : 0), 0);
-    };
-    auto block_scan = [&](uint64_t &mass, uint64_t &count) {  // inclusive, by thread
-        mass = warp_scan(mass, lane);
-        count = warp_scan(count, lane);
-        __syncthreads();
-        if (lane == 31) {
-            sh.warp_mass[warp] = mass;
-            sh.warp_count[warp] = count;
-        }
-        __syncthreads();
-        const uint64_t m = warp_scan(lane < kWarps ? sh.warp_mass[lane] : 0, lane), c = warp_scan(lane < kWarps ? sh.warp_count[lane] : 0, lane);
-        const uint64_t mb = __shfl_sync(0xffffffffu, m, max(warp - 1, 0)), cb = __shfl_sync(0xffffffffu, c, max(warp - 1, 0));
-        if (warp > 0) {
-            mass += mb;
-            count += cb;
-        }
-    };
-
-    // ---- the largest logit
-    uint32_t top_key = 0;
-    {
-        float m = -INFINITY;
-        row.each(begin, stop, lane, [&](float x, int) { m = fmaxf(m, x); });
-        const uint32_t k = __reduce_max_sync(0xffffffffu, key_of(m));
-        if (lane == 0) sh.warp_mass[warp] = k;
-        if (tid == 0) {
-            sh.n_own = 0;
-            sh.first = kNone;
-        }
-        __syncthreads();
-        cluster_wait();
-        exchange(__reduce_max_sync(0xffffffffu, lane < kWarps ? (uint32_t)sh.warp_mass[lane] : 0), 0);
-        for (int c = 0; c < C; ++c) top_key = max(top_key, (uint32_t)sh.part[turn ^ 1][c].mass);
-    }
-    float top = logit_of(top_key);
-    if (top == -INFINITY) {
+    const uint32_t top_key = find_top(row, h);
+    if (top_key == key_of(-INFINITY)) {
         refuse(PA_FLAG_PROBABILITY);
         return;
     }
-    if (top == INFINITY) {
-        row.only_inf = true;
-        top = 0.f;
-        top_key = key_of(0.f);
-    }
-    // What stays: places up to `last` in the order.
-    uint64_t last = place_of(top_key, 0);
-    auto stays = [&](float x, int p) { return place_of(key_of(x), p) <= last; };
-
     if (temperature == 0.f) {
-        uint32_t first = kNone;
-        row.each(begin, stop, lane, [&](float x, int p) {
-            if (x == top) first = min(first, (uint32_t)p);
-        });
-        first = __reduce_min_sync(0xffffffffu, first);
-        if (lane == 0) atomicMin(&sh.first, first);
-        __syncthreads();
-        exchange(sh.first, 0);
-        for (int c = 0; c < C; ++c) first = min(first, (uint32_t)sh.part[turn ^ 1][c].mass);
-        if (OUT == kDraw) {
-            if (rank == 0 && tid == 0) give((int)first - row.pad, 1.f);
-        } else {
-            write_row([&](float, int p) { return p == (int)first ? 1.f : 0.f; });
-        }
+        const int first = find_first(row, h, logit_of(top_key));
+        if constexpr (OUT != kDraw)
+            write_row<T, OUT>(a, row, h, r, [&](float, int p) { return p == first ? 1.f : 0.f; });
+        else if (h.rank == 0 && tid == 0)
+            give(first, 1.f);
         return;
     }
-
-    Scale scale;
-    scale.top = top;
-    scale.table = sh.table;
-    scale.drop = a.drop;
-    {
-        // log2(e) / T as a pair: the remainder of the division is exact
-        constexpr float kHi = 1.44269502f, kLo = 1.92596299e-8f;
-        const float h = fminf(__fdiv_rn(kHi, temperature), 8.5e37f);
-        scale.hi = h;
-        scale.lo = h < 8.5e37f ? __fdiv_rn(__fadd_rn(__fmaf_rn(-h, temperature, kHi), kLo), temperature) : 0.f;
-    }
-    const uint64_t one = 1ull << (kUnit - a.drop);
+    const float top = fminf(logit_of(top_key), 3.402823466e38f);  // (+inf counts as the largest number)
+    make_grid(top, temperature, a.drop);
+    const uint64_t most = weight_of(sh.grid, top);
     const bool by_count = top_k > 0 && top_k < a.V, by_mass = top_p < 1.f;
-    last = ~0ull;
-    uint64_t kept_mass = 0;   // of what stays, 0: not known
-    bool complete = false;    // all that stays is in `all`, sorted: n_all of it
-    int n_all = 0;
-    uint64_t min_weight = 0;  // min-p
-    if (min_p > 0.f) min_weight = max((uint64_t)1, min(one, (uint64_t)ceilf(__fmul_rn(fminf(min_p, 1.f), (float)one))));
-
-    // ---- the borders of top-k and top-p
-#pragma unroll 1
-    for (int round = by_count ? 0 : 1; round < (by_mass ? 2 : 1); ++round) {
-        const bool counting = round == 0;
-        // Undecided: keys lo .. hi; of a single key, indices first .. final.  level 0: everything.
-        uint32_t lo = 0, hi = kNone;
-        int first = 0, final = row.end, shift = 0;
-        uint64_t mass_above = 0, count_above = 0, want = top_k;
-#pragma unroll 1
-        for (int level = 0;; ++level) {
-            const bool single = level > 0 && lo == hi;
-            // the bin of an entry; -1 before all of them in the order, kBins behind
-            auto bin_of = [&](int step, uint32_t key, int p) {
-                if (level == 0) return scale.bin(step);
-                if (key > hi) return -1;
-                if (key < lo) return kBins;
-                if (!single) return (int)((hi - key) >> shift);
-                return p < first ? -1 : p > final ? kBins : (p - first) >> shift;
-            };
-            if (level > 0) {
-                const uint32_t width = single ? (uint32_t)(final - first) : hi - lo;
-                shift = max(0, 32 - __clz(width) - 10);
-                clear_bins();
-                __syncthreads();
-            }
-            row.each(begin, stop, lane, [&](float x, int p) {
-                if (!stays(x, p)) return;
-                float rest, low;
-                const int step = scale.steps(x, rest, low);
-                const int b = bin_of(step, key_of(x), p);
-                if (b < 0 || b >= kBins) return;
-                atomicAdd(&sh.hist[0][b], 1u);
-                if (by_mass) {
-                    const uint64_t w = scale.weight(step, rest, low);
-                    atomicAdd(&sh.hist[1][b], (uint32_t)w & 0x7fffu);
-                    atomicAdd(&sh.hist[2][b], (uint32_t)(w >> 15) & 0x7fffu);
-                    atomicAdd(&sh.hist[3][b], (uint32_t)(w >> 30));
-                }
-            });
-            meet();
-            // this CTA's share of the bins, kEach of them a thread
-            const int share = kBins / C, each = max(1, share / kThreads);
-            uint64_t mass[2] = {0, 0}, count[2] = {0, 0};
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                if (e >= each || tid * each >= share) break;
-                const int b = rank * share + tid * each + e;
-                for (int c = 0; c < C; ++c) {
-                    const uint32_t from = remote(&sh.hist[0][b], c);
-                    count[e] += get32(from);
-                    if (by_mass)
-                        mass[e] += get32(from + 4 * kBins) + ((uint64_t)get32(from + 8 * kBins) << 15) +
-                                   ((uint64_t)get32(from + 12 * kBins) << 30);
-                }
-            }
-            uint64_t upto_mass = mass[0] + mass[1], upto_count = count[0] + count[1];
-            block_scan(upto_mass, upto_count);
-            exchange(__shfl_sync(0xffffffffu, warp_sum(lane < kWarps ? sh.warp_mass[lane] : 0), 0),
-                     warp_sum(lane < kWarps ? sh.warp_count[lane] : 0));
-            uint64_t before_mass = mass_above, before_count = count_above, all_mass = 0;
-            for (int c = 0; c < C; ++c) {
-                const Part p = sh.part[turn ^ 1][c];
-                all_mass += p.mass;
-                if (c < rank) {
-                    before_mass += p.mass;
-                    before_count += p.count;
-                }
-            }
-            if (!counting && level == 0) {
-                // entries stay while the sum before them is below top_p times the whole
-                const uint64_t whole = kept_mass ? kept_mass : all_mass;
-                want = top_p_goal(whole, top_p);
-            }
-            before_mass += upto_mass - mass[0] - mass[1];
-            before_count += upto_count - count[0] - count[1];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                if (e >= each || tid * each >= share) break;
-                const uint64_t before = counting ? before_count : before_mass;
-                if (before < want && before + (counting ? count[e] : mass[e]) >= want)
-                    for (int c = 0; c < C; ++c) {
-                        const uint32_t to = remote(&sh.border, c);
-                        put(to, before_mass, before_count);
-                        asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(to + 16), "r"(rank * share + tid * each + e),
-                                     "r"((uint32_t)count[e]) : "memory");
-                    }
-                before_mass += mass[e];
-                before_count += count[e];
-            }
-            meet();
-            const Border border = sh.border;
-            const int b = (int)border.bin;
-            const bool whole_list = border.count_above + border.count <= kList;
-            if (whole_list || border.count <= kList) {
-                // ---- few enough: gather them, all CTAs' in every CTA, and sort them
-                row.each(begin, stop, lane, [&](float x, int p) {
-                    if (!stays(x, p)) return;
-                    float rest, low;
-                    const int step = level == 0 ? scale.steps(x, rest, low) : 0;
-                    const uint32_t key = key_of(x);
-                    const int at = bin_of(step, key, p);
-                    if (at == b || (whole_list && at < b)) {
-                        const uint32_t i = atomicAdd(&sh.n_own, 1u);
-                        if (i < kList) sh.own[i] = place_of(key, p);
-                    }
-                });
-                meet();
-                int n = 0;
-                uint64_t mine = ~0ull;
-                for (int c = 0; c < C; ++c) {
-                    const int m = (int)min(get32(remote(&sh.n_own, c)), (uint32_t)kList);
-                    if (tid >= n && tid < n + m) mine = get64(remote(&sh.own[tid - n], c));
-                    n += m;
-                }
-                cluster_arrive();  // has read the others' lists
-                int size = 32;
-                while (size < n) size *= 2;
-#pragma unroll 1
-                for (int k = 2; k <= size; k *= 2) {
-#pragma unroll 1
-                    for (int j = k / 2; j > 0; j /= 2) {
-                        uint64_t other;
-                        if (j >= 32) {
-                            __syncthreads();
-                            sh.all[tid] = mine;
-                            __syncthreads();
-                            other = sh.all[tid ^ j];
-                        } else {
-                            other = __shfl_xor_sync(0xffffffffu, mine, j);
-                        }
-                        const bool lower = ((tid & j) == 0) == ((tid & k) == 0);
-                        mine = lower ? min(mine, other) : max(mine, other);
-                    }
-                }
-                __syncthreads();
-                sh.all[tid] = mine;
-                const bool real = tid < n;
-                const uint64_t w = real ? scale.weight(logit_of(~(uint32_t)(mine >> 32))) : 0;
-                uint64_t upto = w, unused = 0;
-                block_scan(upto, unused);
-                const uint64_t base_mass = whole_list ? 0 : border.mass_above, base_count = whole_list ? 0 : border.count_above;
-                upto += base_mass;
-                if (counting && real && base_count + tid + 1 == want) {
-                    sh.cut[0] = mine;
-                    sh.cut_mass[0] = upto;
-                }
-                __syncthreads();
-                uint64_t goal = want;
-                bool found = true;
-                if (counting) {
-                    last = sh.cut[0];
-                    kept_mass = by_mass ? sh.cut_mass[0] : 0;
-                    if (by_mass) {
-                        goal = top_p_goal(kept_mass, top_p);
-                        found = goal > base_mass;  // else the border of top-p is above this bin
-                    }
-                }
-                if (by_mass && found) {
-                    if (real && upto >= goal && upto - w < goal) {
-                        sh.cut[1] = mine;
-                        sh.cut_mass[1] = upto;
-                    }
-                    __syncthreads();
-                    last = sh.cut[1];
-                    kept_mass = sh.cut_mass[1];
-                    round = 1;
-                }
-                complete = whole_list && found;
-                n_all = n;
-                cluster_wait();
-                if (tid == 0) sh.n_own = 0;
-                clear_bins();
-                __syncthreads();
-                break;
-            }
-            mass_above = border.mass_above;
-            count_above = border.count_above;
-            if (level == 0) {
-                // the keys of the bin
-                float rest, low;
-                auto in = [&](int most) {
-                    return first_key(key_of(-INFINITY), top_key, lane, [&](uint32_t key) { return scale.bin(scale.steps(logit_of(key), rest, low)) <= most; });
-                };
-                lo = in(b);
-                hi = b > 0 ? in(b - 1) - 1 : top_key;
-            } else if (!single) {
-                hi -= (uint32_t)b << shift;
-                lo = max(lo, hi - (uint32_t)((1ull << shift) - 1));
+    Kept kept{~0ull, 0, 0, false, false};
+    if (by_count || by_mass) kept = find_borders(row, h, by_count, by_mass, top_k, top_p, a.V, top_key);
+    if (min_p > 0.f) {
+        const uint64_t place = place_of(find_min_key(min_p, most, top_key), 0x7fffffff);
+        if (place < kept.last) {
+            kept.last = place;
+            kept.mass = 0;
+            kept.runs = false;
+        }
+    }
+    if constexpr (OUT == kDraw) {
+        Drawn drawn;
+        if (kept.complete) {
+            if (h.rank != 0) return;
+            drawn = draw_from_list(kept, a.u[r]);
+        } else {
+            drawn = draw_from_runs(row, h, kept, sum_runs(row, h, kept, a.run), a.u[r], a.run);
+        }
+        if (drawn.p >= 0) give(drawn.p, drawn.probability);
+    } else {
+        if (kept.mass == 0) {
+            if (kept.complete) {
+                block_scan(tid < kept.n && sh.all[tid] <= kept.last ? sh.own[tid] : 0);
+                kept.mass = over_warps(sh.warp_mass);
             } else {
-                first += b << shift;
-                final = min(final, first + (int)((1ull << shift) - 1));
+                kept.mass = sum_runs(row, h, kept, a.run);
             }
         }
-    }
-    // ---- min-p: the lowest key whose weight is enough
-    if (min_weight > 0) {
-        const uint32_t lowest = first_key(key_of(-INFINITY), top_key, lane, [&](uint32_t key) { return scale.weight(logit_of(key)) >= min_weight; });
-        const uint64_t place = place_of(lowest, 0x7fffffff);
-        if (place < last) {
-            last = place;
-            kept_mass = 0;
-        }
-    }
-
-    if (complete) {
-        // ---- all that stays is in the list
-        uint64_t mine = sh.all[tid];
-        bool real = tid < n_all && mine <= last;
-        uint64_t w = real ? scale.weight(logit_of(~(uint32_t)(mine >> 32))) : 0;
-        if (OUT == kDraw) {
-            if (rank != 0) return;
-            // by index
-            const int n = __syncthreads_count(real);
-            mine = real ? mine << 32 | mine >> 32 : ~0ull;
-            int size = 32;
-            while (size < n) size *= 2;
-#pragma unroll 1
-            for (int k = 2; k <= size; k *= 2) {
-#pragma unroll 1
-                for (int j = k / 2; j > 0; j /= 2) {
-                    uint64_t other;
-                    if (j >= 32) {
-                        __syncthreads();
-                        sh.all[tid] = mine;
-                        __syncthreads();
-                        other = sh.all[tid ^ j];
-                    } else {
-                        other = __shfl_xor_sync(0xffffffffu, mine, j);
-                    }
-                    const bool lower = ((tid & j) == 0) == ((tid & k) == 0);
-                    mine = lower ? min(mine, other) : max(mine, other);
-                }
-            }
-            w = tid < n ? scale.weight(logit_of(~(uint32_t)mine)) : 0;
-            uint64_t upto = w, unused = 0;
-            block_scan(upto, unused);
-            const uint64_t sum = warp_sum(lane < kWarps ? sh.warp_mass[lane] : 0);
-            const uint64_t target = draw_goal(sum, a.u[r]);
-            if (w > 0 && upto > target && upto - w <= target) give((int)(mine >> 32) - row.pad, __fdiv_rn((float)w, (float)sum));
-            return;
-        }
-        uint64_t upto = w, unused = 0;
-        block_scan(upto, unused);
-        kept_mass = warp_sum(lane < kWarps ? sh.warp_mass[lane] : 0);
-    } else if (OUT == kDraw || kept_mass == 0) {
-        // ---- the sums of the runs
-        uint64_t s = 0;
-        row.each(begin, stop, lane, [&](float x, int p) {
-            if (stays(x, p)) s += scale.weight(x);
+        // probabilities in fp32: 2^t with t = (x - top) / T log2(e) as a pair
+        const float over = __fdiv_rn((float)most, (float)kept.mass);
+        const float2 scale = scale_of(temperature);
+        write_row<T, OUT>(a, row, h, r, [&](float x, int p) {
+            if (place_of(key_of(x), p) > kept.last) return 0.f;
+            x = fminf(fmaxf(x, -INFINITY), top);
+            const float d = __fsub_rn(x, top), b = __fsub_rn(d, x);
+            const float e = __fsub_rn(__fsub_rn(x, __fsub_rn(d, b)), __fadd_rn(top, b));
+            const float t = __fmul_rn(d, scale.x);
+            const float low = __fmaf_rn(e, scale.x, __fmaf_rn(d, scale.y, __fmaf_rn(d, scale.x, -t)));
+            return d == 0.f ? over : t >= -200.f ? exp2f(t) * __fmaf_rn(low, 0.693147181f, 1.f) * over : 0.f;
         });
-        sum_and_exchange(s);
-        uint64_t before = 0, sum = 0;
-        for (int c = 0; c < C; ++c) {
-            const uint64_t m = sh.part[turn ^ 1][c].mass;
-            sum += m;
-            if (c < rank) before += m;
-        }
-        kept_mass = sum;
-        if (OUT == kDraw) {
-            const uint64_t target = draw_goal(sum, a.u[r]);
-            if (target < before || target >= before + sh.part[turn ^ 1][rank].mass) return;
-            // the run, and a thread's piece of it
-            const uint64_t upto = warp_scan(lane < kWarps ? sh.warp_mass[lane] : 0, lane) + before;
-            const int w = __ffs(__ballot_sync(0xffffffffu, upto > target)) - 1;
-            const uint64_t up = __shfl_sync(0xffffffffu, upto, max(w - 1, 0));
-            if (w > 0) before = up;
-            const int from = (rank * kWarps + w) * a.run, each = (a.run + kThreads - 1) / kThreads;
-            const int b = from + tid * each, e = min(min(b + each, from + a.run), row.end);
-            uint64_t piece = 0, unused = 0;
-            for (int p = b; p < e; ++p) {
-                const float x = row.at(p);
-                if (stays(x, p)) piece += scale.weight(x);
-            }
-            uint64_t place = piece;
-            block_scan(place, unused);
-            place += before;
-            if (place > target && place - piece <= target) {
-                place -= piece;
-                for (int p = b; p < e; ++p) {
-                    const float x = row.at(p);
-                    const uint64_t entry = stays(x, p) ? scale.weight(x) : 0;
-                    place += entry;
-                    if (place > target) {
-                        give(p - row.pad, __fdiv_rn((float)entry, (float)sum));
-                        break;
-                    }
-                }
-            }
-            return;
-        }
-    }
-    if (OUT != kDraw) {
-        const float over = __fdiv_rn((float)one, (float)kept_mass);
-        write_row([&](float x, int p) { return stays(x, p) ? scale.value(x) * over : 0.f; });
     }
 }
 
@@ -818,6 +1072,7 @@ cudaError_t launch_sample(const SampleArgs &a, int R, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)R * a.cluster);
     cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = sizeof(Shared);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
