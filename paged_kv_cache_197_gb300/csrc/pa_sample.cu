@@ -10,11 +10,11 @@
 // thread's piece of it and an entry; or the row is written.
 //
 // Weights and sums.  A logit is a grid point and a part of a cell, x = x_k + y, exactly;
-// its weight exp(x / T) is exp(x_k / T), one of 2047 entries of a table in whole numbers of 2^-44
-// made once a row to 2^-35, plus a correction of at most a 63rd of it, w (1 - exp(-y / T)), which
-// fp32 and the hardware's exp2 give to 2^-28 of w.  The whole numbers are summed exactly, the
+// its weight exp(x / T) is exp(x_k / T), one of 4095 entries of a table in whole numbers of 2^-44
+// made once a row to 2^-35, plus a correction of at most a 125th of it, w (1 - exp(-y / T)), which
+// fp32 and the hardware's exp2 give to 2^-29 of w.  The whole numbers are summed exactly, the
 // corrections of a lane in fp32.  So a border or draw comes out as it does in 64 bits unless
-// two numbers agree to about 2^-28 of a single weight and 2^-36 of the sum.  (fp32 weights and sums
+// two numbers agree to about 2^-29 of a single weight and 2^-36 of the sum.  (fp32 weights and sums
 // carry 2^-21: beside a vocabulary's tens of thousands of small weights, one row in a few hundred would
 // be cut or drawn elsewhere.  Weights as pairs of fp32 took 45 instructions each, three times as many;
 // GB300 has two fp64 lanes per SM and clock.)
@@ -22,6 +22,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "pa_internal.cuh"
 #include "pa_sample.h"
@@ -32,9 +33,12 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kCells = 2048;  // of the grid; the last one holds all logits whose weight is 0
+constexpr int kCells = 4096;  // of the grid; the last one holds all logits whose weight is 0
+constexpr int kGroups = 64;   // of 64 cells
 constexpr int kSplit = 512;   // bins of a cell that is split
-constexpr int kList = 512;    // tokens that are sorted (at most one a thread)
+constexpr int kList = 512;    // tokens that are listed (at most one a thread)
+constexpr int kFew = 64;      // top-k up to which its tokens are listed at once
+constexpr int kMaxima = 128;  // largest logits of equal parts of a row
 constexpr int kUnit = 44;     // a weight of 1 is 2^44
 constexpr uint32_t kNone = 0xffffffffu;
 
@@ -76,13 +80,15 @@ struct Powers {
 };
 __device__ const Powers kPowers = Powers();
 
-// 2^-(turns 2^-56) in units of 2^-(kUnit - drop), rounded: 2^-octaves 2^(j / 1024) (1 + q).
-__device__ __forceinline__ uint64_t power(uint64_t turns, int drop) {
+// 2^-(turns 2^-56) as a number of 62 bits, in units of 2^-62, and its octaves: 2^-octaves 2^(j / 1024) (1 + q) / 2.
+struct Power {
+    uint64_t w;
+    int octaves;
+};
+__device__ __forceinline__ Power power(uint64_t turns) {
     constexpr uint64_t kOne = 1ull << 56;
     const uint64_t left = kOne - (turns & (kOne - 1));  // up to the next octave
-    const int shift = 62 - kUnit + (int)(turns >> 56) + drop;
-    if (shift > 62) return 0;
-    uint64_t w = 1ull << 62;  // in units of 2^-62 of the octave below
+    uint64_t w = 1ull << 62;
     if (left < kOne) {
         const int j = (int)(left >> 46);
         const float r = (float)(uint32_t)((left >> 22) & 0xffffffu) * 5.8207660913467407e-11f;  // 2^-34
@@ -90,10 +96,10 @@ __device__ __forceinline__ uint64_t power(uint64_t turns, int drop) {
         w = __umul64hi(kPowers.coarse[j / 32], kPowers.fine[j % 32]);
         w += __umul64hi(w, (uint64_t)__float2uint_rn(q * 2199023255552.f) << 23);  // q in units of 2^-41
     }
-    return (w + (1ull << (shift - 1))) >> shift;
+    return Power{w, (int)(turns >> 56)};
 }
 
-// A row's grid: steps g, a power of two from T / 62.75 on, so that 2047 of them span the 47 octaves in which
+// A row's grid: steps g, a power of two from T / 125.5 on, so that 4095 of them span the 47 octaves in which
 // weights are not 0.
 struct Grid {
     float base;        // taken off all logits: 0, or the largest where it is far from 0 (exact for all that count)
@@ -115,7 +121,7 @@ struct Grid {
         return (zero - __float_as_int(__fadd_rn(fminf(fmaxf(__fsub_rn(x, base), low), high), magic))) & (kCells - 1);
     }
     // What is to be added to the weight of a part's grid point: the hardware's exp2, to 2^-22, of the
-    // whole weight, in units, times 1 - exp(-part / T), |part / T| < 1 / 62.75.
+    // whole weight, in units, times 1 - exp(-part / T), |part / T| < 1 / 125.
     __device__ __forceinline__ float rest(float y, float part) const {
         float e;
         asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmaf_rn(__fsub_rn(y, point), c, unit)));
@@ -204,7 +210,13 @@ struct alignas(16) Part {  // a CTA's sums
     uint64_t mass, count, cell_mass, all_mass;
 };
 // What the CTAs of a cluster tell each other; a place of its own for each step.
-enum { kTop, kCellSums, kCellBorder, kBins, kRuns, kExchanges };
+enum { kFewSums, kCellBorder, kBins, kRuns, kExchanges };
+struct alignas(16) Group {  // of cells: their tokens, and the weights of these at their grid points
+    uint64_t mass, count;
+};
+struct alignas(16) Entry {  // of the list
+    uint64_t place, weight;
+};
 struct alignas(16) Border {
     uint64_t mass_above, count_above, bin, count;
 };
@@ -213,8 +225,13 @@ struct alignas(16) Shared {
     uint64_t table[kCells];
     uint32_t cells[kCells];      // tokens in each
     uint32_t hist[4][kSplit];    // of a cell that is split: counts, and sums of the weights' lowest 15 bits, the next 15 and the rest
-    uint64_t own[kList];         // places gathered here; then the sorted ones' weights
-    uint64_t all[kList];         // of all CTAs
+    uint64_t own[kList];         // places gathered here
+    Entry list[kList];           // all CTAs'
+    uint64_t before_mass[kThreads];
+    uint32_t before_count[kThreads];
+    uint32_t maxima[kMaxima];    // keys
+    Group mine[kGroups], groups[kMaxCluster][kGroups];  // this CTA's, and all CTAs'
+    Power steps[2][kGroups];     // of the table: exp of 64 steps, and of one
     Part part[kExchanges][kMaxCluster];
     Border border;
     uint64_t warp_mass[kWarps], warp_count[kWarps];
@@ -223,6 +240,7 @@ struct alignas(16) Shared {
     uint64_t cut[2], cut_mass[2];
     uint32_t n_own;
     uint32_t first;              // temperature 0
+    uint32_t least;              // a key that top-k's tokens are not below
     Grid grid;
 };
 extern __shared__ __align__(16) char shared_bytes[];
@@ -243,6 +261,12 @@ __device__ __forceinline__ void put(uint64_t *p, uint64_t a, uint64_t b, int to,
     } else {
         asm volatile("st.shared::cluster.v2.u64 [%0], {%1, %2};" ::"r"(remote(p, to)), "l"(a), "l"(b) : "memory");
     }
+}
+__device__ __forceinline__ void put(uint32_t *p, uint32_t a, int to, int rank) {
+    if (to == rank)
+        *p = a;
+    else
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(remote(p, to)), "r"(a) : "memory");
 }
 __device__ __forceinline__ uint32_t get(const uint32_t *p, int from, int rank) {
     if (from == rank) return *p;
@@ -304,9 +328,9 @@ struct Row {
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
     __device__ __forceinline__ float at(int p) const { return p >= pad && p < end ? entry(base + p) : -INFINITY; }
-    // f(x, padded index) for the entries of a warp's run [begin, stop), both multiples of 8
+    // f(entries, padded index of the first) for the units of a warp's run [begin, stop), both multiples of 8
     template <typename F>
-    __device__ __forceinline__ void each(int begin, int stop, int lane, F f) const {
+    __device__ __forceinline__ void units(int begin, int stop, int lane, F f) const {
         constexpr int N = kVec<T>;
         int p = begin + lane * N;
         uint4 next = make_uint4(0, 0, 0, 0);
@@ -317,9 +341,16 @@ struct Row {
             if (p + 32 * N < stop) next = load(p + 32 * N);
             float x[N];
             unpack(raw, x);
-#pragma unroll
-            for (int i = 0; i < N; ++i) f(x[i], p + i);
+            f(x, p);
         }
+    }
+    // f(entry, padded index)
+    template <typename F>
+    __device__ __forceinline__ void each(int begin, int stop, int lane, F f) const {
+        units(begin, stop, lane, [&](const float (&x)[kVec<T>], int p) {
+#pragma unroll
+            for (int i = 0; i < kVec<T>; ++i) f(x[i], p + i);
+        });
     }
 };
 
@@ -328,6 +359,20 @@ __device__ __forceinline__ uint64_t weight_of(const Grid &grid, float x) {
     float y, part;
     const uint64_t w = shared().table[grid.cell(x, y, part)];
     return w + (uint64_t)__float2ll_rn(grid.rest(y, part));
+}
+
+// The same without a table, to 2^-35: the exponent as a pair of fp32, then in 64 bits.
+__device__ __forceinline__ uint64_t weight_of(float2 scale, float top, int drop, float x) {
+    x = fminf(fmaxf(x, -INFINITY), top);
+    const float d = __fsub_rn(x, top), b = __fsub_rn(d, x);
+    const float e = __fsub_rn(__fsub_rn(x, __fsub_rn(d, b)), __fadd_rn(top, b));
+    const float t = __fmul_rn(d, scale.x);
+    if (!(t > -62.f)) return 0;
+    const float low = __fmaf_rn(e, scale.x, __fmaf_rn(d, scale.y, __fmaf_rn(d, scale.x, -t)));
+    const long long turns = __float2ll_rn(-t * 72057594037927936.f) - __float2ll_rn(low * 72057594037927936.f);
+    const Power p = power((uint64_t)max(turns, 0ll));
+    const int shift = 62 - kUnit + p.octaves + drop;
+    return shift > 62 ? 0 : (p.w + (1ull << (shift - 1))) >> shift;
 }
 
 // ------------------------------------------------------------------------ steps of a CTA
@@ -383,47 +428,53 @@ __device__ __forceinline__ uint64_t over_warps(const uint64_t *of) {
     return warp_sum(lane < kWarps ? of[lane] : 0);
 }
 
-// One number a thread, rising in the first `n` threads (the others have ~0); n <= kList.
-__device__ __noinline__ uint64_t sort(uint64_t mine, int n) {
+// What comes before each of the list's n tokens (thread t: entry t) in their order, or by index among the places up to
+// `last`: weights and tokens.  All threads share the n^2 comparisons: 64 tokens take a few hundred clocks, a third of what
+// sorting them takes, 512 as long.
+template <bool BY_INDEX>
+__device__ __noinline__ Entry rank_list(int n, uint64_t last) {
     Shared &sh = shared();
     const int tid = threadIdx.x;
-    const int size = n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : n <= 256 ? 256 : kList;
-#pragma unroll 1
-    for (int k = 2; k <= size; k *= 2) {
-#pragma unroll 1
-        for (int j = k / 2; j > 0; j /= 2) {
-            uint64_t other;
-            if (j >= 32) {
-                __syncthreads();
-                sh.all[tid] = mine;
-                __syncthreads();
-                other = sh.all[tid ^ j];
-            } else {
-                other = __shfl_xor_sync(0xffffffffu, mine, j);
-            }
-            const bool lower = ((tid & j) == 0) == ((tid & k) == 0);
-            mine = lower ? min(mine, other) : max(mine, other);
-        }
+    const int size = n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : n <= 256 ? 256 : kList, parts = kThreads / size;
+    const uint64_t place = sh.list[tid & (size - 1)].place, mine = BY_INDEX ? (uint32_t)place : place;
+    uint64_t mass = 0;
+    uint32_t count = 0;
+#pragma unroll 4
+    for (int j = tid / size; j < n; j += parts) {
+        const Entry e = sh.list[j];
+        const bool before = (BY_INDEX ? (uint32_t)e.place : e.place) < mine && (!BY_INDEX || e.place <= last);
+        mass += before ? e.weight : 0;
+        count += before;
     }
+    sh.before_mass[tid] = mass;
+    sh.before_count[tid] = count;
     __syncthreads();
-    return mine;
+    mass = count = 0;
+    if (tid < n)
+        for (int i = tid; i < kThreads; i += size) {
+            mass += sh.before_mass[i];
+            count += sh.before_count[i];
+        }
+    __syncthreads();
+    return Entry{mass, count};  // (place: the weights)
 }
 
-// The key of a row's largest logit.
+// The key of a row's largest logit, and the largest keys of kMaxima equal parts of the row: of groups of 4 C lanes.
 template <typename T>
 __device__ __noinline__ uint32_t find_top(Row<T> row, Here h) {
     Shared &sh = shared();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     float m = -INFINITY;
     row.each(h.begin, h.stop, lane, [&](float x, int) { m = fmaxf(m, x); });
-    const uint32_t k = __reduce_max_sync(0xffffffffu, key_of(m));
-    if (lane == 0) sh.warp_count[warp] = k;
+    for (int o = 2 * h.C; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const int groups = 8 / h.C, share = kMaxima / h.C;  // of a warp, of a CTA
+    if (lane % (4 * h.C) == 0) sh.before_count[warp * groups + lane / (4 * h.C)] = key_of(m);
     __syncthreads();
     cluster_wait(h.C);
-    exchange(h, kTop, Part{__reduce_max_sync(0xffffffffu, lane < kWarps ? (uint32_t)sh.warp_count[lane] : 0), 0, 0, 0});
-    uint32_t top = 0;
-    for (int c = 0; c < h.C; ++c) top = max(top, (uint32_t)sh.part[kTop][c].mass);
-    return top;
+    if (tid < kMaxima) put(&sh.maxima[h.rank * share + tid % share], sh.before_count[tid % share], tid / share, h.rank);
+    meet(h.C);
+    const uint32_t a = max(max(sh.maxima[lane], sh.maxima[lane + 32]), max(sh.maxima[lane + 64], sh.maxima[lane + 96]));
+    return __reduce_max_sync(0xffffffffu, a);
 }
 
 // Temperature 0: the first place of the largest logit.
@@ -451,12 +502,35 @@ __device__ __forceinline__ float2 scale_of(float temperature) {
     return make_float2(hi, __fdiv_rn(__fadd_rn(__fmaf_rn(-hi, t, kHi), kLo), t));
 }
 
-// A row's grid and its table.
-__device__ __noinline__ void make_grid(float top, float temperature, int drop) {
-    Shared &sh = shared();
+__device__ __forceinline__ float step_of(float temperature) {
     const float t = fminf(fmaxf(temperature, 8.6736174e-19f), 1.2089258e24f);
+    return __uint_as_float((__float_as_uint(t * (1.f / 125.5f)) + 0x7fffffu) & 0xff800000u);
+}
+
+// A row's table, in units of 2^-(kUnit - drop): entry 64 i + j as a product of exp(-64 i g / T) and exp(-j g / T).
+__device__ __noinline__ void make_table(float temperature, int drop) {
+    Shared &sh = shared();
+    const int tid = threadIdx.x;
     const float2 scale = scale_of(temperature);
-    const float step = __uint_as_float((__float_as_uint(t * (1.f / 62.75f)) + 0x7fffffu) & 0xff800000u);
+    const float step = step_of(temperature);
+    if (tid < 2 * kGroups) {
+        const uint64_t turns = (uint64_t)(scale.x * step * 72057594037927936.f) + (uint64_t)(int64_t)(scale.y * step * 72057594037927936.f);
+        sh.steps[tid / kGroups][tid % kGroups] = power(turns * (tid < kGroups ? 64 * tid : tid - kGroups));
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int k = tid; k < kCells; k += kThreads) {
+        const Power a = sh.steps[0][k / 64], b = sh.steps[1][k % 64];
+        const uint64_t w = __umul64hi(a.w, b.w);  // units of 2^-60
+        const int shift = 60 - kUnit + a.octaves + b.octaves + drop;
+        sh.table[k] = shift > 61 || k == kCells - 1 ? 0 : (w + (1ull << (shift - 1))) >> shift;
+    }
+    __syncthreads();
+}
+
+// A row's grid.
+__device__ __forceinline__ Grid make_grid(float top, float temperature, int drop) {
+    const float t = fminf(fmaxf(temperature, 8.6736174e-19f), 1.2089258e24f), step = step_of(temperature);
     Grid g;
     g.base = fabsf(top) > step * 1048576.f ? top : 0.f;
     g.high = __fsub_rn(top, g.base);
@@ -465,75 +539,109 @@ __device__ __noinline__ void make_grid(float top, float temperature, int drop) {
     g.zero = __float_as_int(s);
     g.point = __fsub_rn(s, g.magic);
     g.low = g.point - step * (kCells - 1);
-    g.c = scale.x;
+    g.c = scale_of(temperature).x;
     g.over = __fdiv_rn(1.f, t);
     g.unit = (float)(kUnit - drop);
-    if (threadIdx.x == 0) sh.grid = g;
-    const uint64_t turns = (uint64_t)(scale.x * step * 72057594037927936.f) + (uint64_t)(int64_t)(scale.y * step * 72057594037927936.f);
-    for (int k = threadIdx.x; k < kCells; k += kThreads) sh.table[k] = k < kCells - 1 ? power(k * turns, drop) : 0;
-    __syncthreads();
+    return g;
 }
 
+// The tokens in the cells, in groups of 64 summed up for all CTAs.
 template <typename T>
 __device__ __noinline__ void count_cells(Row<T> row, Here h) {
     Shared &sh = shared();
+    const int tid = threadIdx.x, lane = tid & 31;
     const Grid grid = sh.grid;
-    row.each(h.begin, h.stop, threadIdx.x & 31, [&](float x, int) {
-        const int k = grid.cell(x);
-        if (k < kCells - 1) atomicAdd(&sh.cells[k], 1u);
+    row.units(h.begin, h.stop, lane, [&](const float (&x)[kVec<T>], int) {
+        int k[kVec<T>];
+#pragma unroll
+        for (int i = 0; i < kVec<T>; ++i) k[i] = grid.cell(x[i]);
+#pragma unroll
+        for (int i = 0; i < kVec<T>; ++i)
+            if (k[i] < kCells - 1) atomicAdd(&sh.cells[k[i]], 1u);
     });
+    __syncthreads();
+    constexpr int kEach = kCells / kThreads;
+    uint64_t mass = 0;
+    uint32_t count = 0;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+        const uint32_t n = sh.cells[tid * kEach + e];
+        count += n;
+        mass += n * sh.table[tid * kEach + e];
+    }
+#pragma unroll
+    for (int o = 64 / kEach / 2; o > 0; o >>= 1) {
+        mass += __shfl_xor_sync(0xffffffffu, mass, o);
+        count += __shfl_xor_sync(0xffffffffu, count, o);
+    }
+    if (tid % (64 / kEach) == 0) sh.mine[tid / (64 / kEach)] = Group{mass, count};
+    __syncthreads();
+    if (tid / kGroups < h.C) {
+        const Group g = sh.mine[tid % kGroups];
+        put(&sh.groups[h.rank][tid % kGroups].mass, g.mass, g.count, tid / kGroups, h.rank);
+    }
     meet(h.C);
 }
 
 // The cell of a border, left in `border` with the tokens before it and in it: the first whose tokens (counting), or whose tokens'
 // weights at their grid points, reach `want` together with those before; want 0: top_p of all weights.  It is cut to
-// `limit`, whose own numbers are not known then (kNone), but for the last cell's.
+// `limit`, whose own numbers are not known then (kNone), but for the last cell's.  The first warp narrows it down to a
+// group, and among the group's cells; two of them a lane.
 __device__ __noinline__ void find_cell(Here h, bool counting, uint64_t want, float top_p, int limit, int V) {
     Shared &sh = shared();
-    constexpr int kEach = kCells / kThreads;  // cells of a thread, at most
-    const int tid = threadIdx.x, share = kCells / h.C, each = max(1, share / kThreads), at = h.rank * share + tid * each;
-    uint64_t mass[kEach], count[kEach], own_mass = 0, own_count = 0;
-#pragma unroll
-    for (int e = 0; e < kEach; ++e) {
-        mass[e] = count[e] = 0;
-        if (e >= each || tid * each >= share) continue;
-        for (int c = 0; c < h.C; ++c) count[e] += get(&sh.cells[at + e], c, h.rank);
-        mass[e] = count[e] * sh.table[at + e];
-        own_mass += mass[e];
-        own_count += count[e];
-    }
-    if (tid == 0) sh.border = Border{0, kNone, (uint64_t)limit, kNone};
-    uint64_t before_mass = block_scan(own_mass) - own_mass;
-    const uint64_t sum_mass = over_warps(sh.warp_mass);
-    uint64_t before_count = block_scan(own_count) - own_count;
-    exchange(h, kCellSums, Part{sum_mass, over_warps(sh.warp_mass), 0, 0});
-    uint64_t all_mass = 0, all_count = 0;
-    for (int c = 0; c < h.C; ++c) {
-        const Part p = sh.part[kCellSums][c];
-        all_mass += p.mass;
-        all_count += p.count;
-        if (c < h.rank) {
-            before_mass += p.mass;
-            before_count += p.count;
+    const int lane = threadIdx.x & 31;
+    if (threadIdx.x < 32) {
+        uint64_t mass[2] = {0, 0}, count[2] = {0, 0};
+        for (int c = 0; c < h.C; ++c) {
+            const Group a = sh.groups[c][2 * lane], b = sh.groups[c][2 * lane + 1];
+            mass[0] += a.mass;
+            count[0] += a.count;
+            mass[1] += b.mass;
+            count[1] += b.count;
         }
-    }
-    const uint64_t goal = want ? want : top_p_goal(all_mass, top_p);
+        uint64_t upto_mass = warp_scan(mass[0] + mass[1], lane), upto_count = warp_scan(count[0] + count[1], lane);
+        const uint64_t all_mass = __shfl_sync(0xffffffffu, upto_mass, 31), all_count = __shfl_sync(0xffffffffu, upto_count, 31);
+        const uint64_t goal = want ? want : top_p_goal(all_mass, top_p);
+        // the lane and which of its two, and what comes before
+        uint64_t before_mass = 0, before_count = 0;
+        auto pick = [&](int &of, uint64_t &n) {  // false: none
+            const uint64_t upto = counting ? upto_count : upto_mass, second = counting ? count[1] : mass[1];
+            const unsigned yes = __ballot_sync(0xffffffffu, upto >= goal);
+            if (!yes) return false;
+            const int at = __ffs(yes) - 1;
+            const bool late = __shfl_sync(0xffffffffu, (int)(upto - second < goal), at);
+            const uint64_t m = upto_mass - mass[1] - (late ? 0 : mass[0]), c = upto_count - count[1] - (late ? 0 : count[0]);
+            before_mass = __shfl_sync(0xffffffffu, m, at);
+            before_count = __shfl_sync(0xffffffffu, c, at);
+            n = __shfl_sync(0xffffffffu, late ? count[1] : count[0], at);
+            of = 2 * at + late;
+            return true;
+        };
+        Border found{0, kNone, (uint64_t)limit, kNone};
+        int group = 0, of = 0;
+        uint64_t n = 0;
+        if (pick(group, n)) {
+            uint64_t both[kMaxCluster];  // two cells' tokens
 #pragma unroll
-    for (int e = 0; e < kEach; ++e) {
-        if (e >= each || tid * each >= share) continue;
-        const uint64_t before = counting ? before_count : before_mass;
-        if (at + e < limit && before < goal && before + (counting ? count[e] : mass[e]) >= goal)
-            for (int c = 0; c < h.C; ++c) {
-                put(&sh.border.mass_above, 0, before_count, c, h.rank);
-                put(&sh.border.bin, at + e, count[e], c, h.rank);
+            for (int c = 0; c < kMaxCluster; ++c)
+                both[c] = c < h.C ? get(reinterpret_cast<const uint64_t *>(&sh.cells[64 * group + 2 * lane]), c, h.rank) : 0;
+            count[0] = count[1] = 0;
+#pragma unroll
+            for (int c = 0; c < kMaxCluster; ++c) {
+                count[0] += (uint32_t)both[c];
+                count[1] += both[c] >> 32;
             }
-        before_mass += mass[e];
-        before_count += count[e];
-    }
-    meet(h.C);
-    if (tid == 0 && sh.border.bin == kCells - 1) {  // beyond all weights
-        sh.border.count_above = all_count;
-        sh.border.count = V - all_count;
+            mass[0] = count[0] * sh.table[64 * group + 2 * lane];
+            mass[1] = count[1] * sh.table[64 * group + 2 * lane + 1];
+            upto_mass = before_mass + warp_scan(mass[0] + mass[1], lane);
+            upto_count = before_count + warp_scan(count[0] + count[1], lane);
+            if (pick(of, n) && 64 * group + of < limit) found = Border{before_mass, before_count, (uint64_t)(64 * group + of), n};
+        }
+        if (found.bin == kCells - 1) {  // beyond all weights
+            found.count_above = all_count;
+            found.count = V - all_count;
+        }
+        if (lane == 0) sh.border = found;
     }
     __syncthreads();
 }
@@ -545,30 +653,58 @@ __device__ __noinline__ void sum_and_gather(Row<T> row, Here h, int b, bool all_
     Shared &sh = shared();
     const Grid grid = sh.grid;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int N = kVec<T>;
     Sum before, all;
     uint64_t inside = 0;
     uint32_t n_inside = 0;
-    const int summed = all_up_to ? 0 : b;
-    row.each(h.begin, h.stop, lane, [&](float x, int p) {
-        float y, part;
-        const int k = grid.cell(x, y, part);
-        if (k == b || (all_up_to && k < b)) {
-            const uint64_t place = place_of(key_of(x), p);
-            if (place <= last && p >= row.pad && p < row.end) {
-                const uint32_t i = atomicAdd(&sh.n_own, 1u);
-                if (i < kList) sh.own[i] = place;
-                inside += weight_of(grid, x);
+    const int summed = all_up_to ? 0 : b, listed = all_up_to ? 0 : b;  // cells listed .. b are gathered
+    row.units(h.begin, h.stop, lane, [&](const float (&x)[N], int p) {
+        float y[N], part[N];
+        int k[N];
+        bool list = false, sum = all_wanted;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            k[i] = grid.cell(x[i], y[i], part[i]);
+            list |= k[i] >= listed && k[i] <= b;
+            sum |= k[i] < summed;
+        }
+        if (list) {
+#pragma unroll 1
+            for (int i = 0; i < N; ++i) {
+                float one = x[0];
+                int cell = k[0];
+#pragma unroll
+                for (int j = 1; j < N; ++j) {
+                    one = i == j ? x[j] : one;
+                    cell = i == j ? k[j] : cell;
+                }
+                const uint64_t place = place_of(key_of(one), p + i);
+                if (cell < listed || cell > b || place > last || p + i < row.pad || p + i >= row.end) continue;
+                const uint32_t at = atomicAdd(&sh.n_own, 1u);
+                if (at < kList) sh.own[at] = place;
+                inside += weight_of(grid, one);
                 ++n_inside;
             }
         }
-        if (all_wanted || k < summed) {
-            const uint64_t w = sh.table[k];
-            const float rest = grid.rest(y, part);
-            all.whole += w;
-            all.rest += rest;
-            if (k < summed) {
-                before.whole += w;
-                before.rest += rest;
+        if (sum) {
+            uint64_t w[N];
+            float rest[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                w[i] = sh.table[k[i]];
+                rest[i] = grid.rest(y[i], part[i]);
+            }
+            if (all_wanted) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    all.whole += w[i];
+                    all.rest += rest[i];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                before.whole += k[i] < summed ? w[i] : 0;
+                before.rest += k[i] < summed ? rest[i] : 0.f;
             }
         }
     });
@@ -579,10 +715,10 @@ __device__ __noinline__ void sum_and_gather(Row<T> row, Here h, int b, bool all_
         sh.run_mass[warp] = run;
         sh.warp_mass[warp] = in;
         sh.warp_count[warp] = total;
-        sh.all[warp] = n_inside;
+        sh.before_mass[warp] = n_inside;
     }
     __syncthreads();
-    exchange(h, kCellBorder, Part{over_warps(sh.run_mass), over_warps(sh.all), over_warps(sh.warp_mass), over_warps(sh.warp_count)});
+    exchange(h, kCellBorder, Part{over_warps(sh.run_mass), over_warps(sh.before_mass), over_warps(sh.warp_mass), over_warps(sh.warp_count)});
 }
 
 // A cell of more than kList tokens, split on over their keys, and over the indices of equal keys, until a bin of the border has
@@ -675,28 +811,36 @@ __device__ __noinline__ void split_cell(Row<T> row, Here h, int b, bool counting
     }
 }
 
-// All CTAs' gathered places, sorted, in `all` of every CTA, and their weights in `own`; how many.
-__device__ __noinline__ int join_lists(Here h) {
+// All CTAs' gathered places in the list of every CTA, and their weights by `weight`; how many.
+template <typename F>
+__device__ __forceinline__ int join_lists(Here h, F weight) {
     Shared &sh = shared();
-    const Grid grid = sh.grid;
-    const int tid = threadIdx.x;
-    int n = 0;
-    uint64_t mine = ~0ull;
-    for (int c = 0; c < h.C; ++c) {
-        const int m = (int)min(get(&sh.n_own, c, h.rank), (uint32_t)kList);
-        if (tid >= n && tid < n + m) mine = get(&sh.own[tid - n], c, h.rank);
-        n += m;
+    const int tid = threadIdx.x, lane = tid & 31;
+    // how many each CTA has; a thread's place in the joined list is a CTA's and one in its own
+    const uint32_t has = lane < h.C ? min(get(&sh.n_own, lane, h.rank), (uint32_t)kList) : 0;
+    uint32_t upto = has;
+#pragma unroll
+    for (int o = 1; o < kMaxCluster; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
     }
+    int n = (int)__shfl_sync(0xffffffffu, upto, kMaxCluster - 1), from = 0, at = tid;
+#pragma unroll
+    for (int c = 0; c < kMaxCluster - 1; ++c) {
+        const int end = (int)__shfl_sync(0xffffffffu, upto, c);
+        if (tid >= end) {
+            from = c + 1;
+            at = tid - end;
+        }
+    }
+    uint64_t mine = ~0ull;
+    if (tid < n && at < kList) mine = get(&sh.own[at], from, h.rank);
     n = min(n, kList);
     cluster_arrive(h.C);  // has read the others' lists
-    mine = sort(mine, n);
-    const uint64_t w = tid < n ? weight_of(grid, logit_at(mine)) : 0;
+    sh.list[tid] = Entry{mine, tid < n ? weight(logit_at(mine)) : 0};
     cluster_wait(h.C);
     __syncthreads();
     if (tid == 0) sh.n_own = 0;
-    sh.all[tid] = mine;
-    sh.own[tid] = w;
-    __syncthreads();
     return n;
 }
 
@@ -709,9 +853,96 @@ struct Kept {
     bool runs;          // run_mass, part[kCellBorder] and the list give the sums of what stays
 };
 
+// The borders of top-k (the want-th token, want 0: none) and top-p in a list of n tokens that follow base_count tokens
+// with weights base_mass.  In a list of top-k's border, that of top-p may be before it: false.
+__device__ __noinline__ bool cut_list(Kept &kept, int n, bool counting, uint64_t want, bool by_mass, float top_p, uint64_t base_mass,
+                                      uint64_t base_count) {
+    Shared &sh = shared();
+    const int tid = threadIdx.x;
+    const Entry before = rank_list<false>(n, 0);
+    const Entry mine = sh.list[tid];
+    const uint64_t upto = base_mass + before.place + mine.weight;
+    const bool real = tid < n;
+    kept.n = n;
+    if (counting) {
+        if (real && base_count + before.weight + 1 == want) {
+            sh.cut[0] = mine.place;
+            sh.cut_mass[0] = upto;
+        }
+        __syncthreads();
+        kept.last = sh.cut[0];
+        kept.mass = sh.cut_mass[0];
+        if (!by_mass) return true;
+        want = top_p_goal(kept.mass, top_p);
+        if (want <= base_mass) return false;
+    }
+    const bool here = real && upto >= want && upto - mine.weight < want, any = __syncthreads_or(here);
+    if (here || (!any && real && before.weight + 1 == n)) {  // (else the last of them)
+        sh.cut[1] = mine.place;
+        sh.cut_mass[1] = upto;
+    }
+    __syncthreads();
+    kept.last = sh.cut[1];
+    kept.mass = sh.cut_mass[1];
+    return true;
+}
+
+// Top-k of few tokens: the k-th largest of the parts' largest logits is not above the k-th largest logit, and few tokens are not
+// below it.  They are listed, and both borders are in the list; false if they are too many (equal or masked logits).
+template <typename T>
+__device__ __noinline__ bool find_few(Kept &kept, Row<T> row, Here h, int top_k, bool by_mass, float top_p, float top, float temperature,
+                                      int drop) {
+    Shared &sh = shared();
+    const int tid = threadIdx.x, lane = tid & 31;
+    if (tid < kMaxima) {
+        const uint32_t mine = sh.maxima[tid];
+        int before = 0;
+#pragma unroll 8
+        for (int j = 0; j < kMaxima; ++j) {
+            const uint32_t key = sh.maxima[j];
+            before += key > mine || (key == mine && j < tid);
+        }
+        if (before == top_k - 1) sh.least = mine;
+    }
+    __syncthreads();
+    const float least = logit_of(sh.least);
+    constexpr int N = kVec<T>;
+    row.units(h.begin, h.stop, lane, [&](const float (&x)[N], int p) {
+        float m = x[0];
+#pragma unroll
+        for (int i = 1; i < N; ++i) m = fmaxf(m, x[i]);
+        if (!(m >= least)) return;
+#pragma unroll 1
+        for (int i = 0; i < N; ++i) {
+            float one = x[0];
+#pragma unroll
+            for (int j = 1; j < N; ++j) one = i == j ? x[j] : one;
+            if (!(one >= least) || p + i < row.pad || p + i >= row.end) continue;
+            const uint32_t at = atomicAdd(&sh.n_own, 1u);
+            if (at < kList) sh.own[at] = place_of(key_of(one), p + i);
+        }
+    });
+    __syncthreads();
+    exchange(h, kFewSums, Part{0, sh.n_own, 0, 0});
+    uint64_t n_all = 0;
+    for (int c = 0; c < h.C; ++c) n_all += sh.part[kFewSums][c].count;
+    if (n_all > kList || n_all < top_k) {  // (fewer: NaN among the parts)
+        __syncthreads();
+        if (tid == 0) sh.n_own = 0;
+        __syncthreads();
+        return false;
+    }
+    const float2 scale = scale_of(temperature);
+    const int n = join_lists(h, [&](float x) { return weight_of(scale, top, drop, x); });
+    cut_list(kept, n, true, top_k, by_mass, top_p, 0, 0);
+    kept.complete = true;
+    return true;
+}
+
 template <typename T>
 __device__ __noinline__ Kept find_borders(Row<T> row, Here h, bool by_count, bool by_mass, int top_k, float top_p, int V, uint32_t top_key) {
     Shared &sh = shared();
+    const Grid grid = sh.grid;
     const int tid = threadIdx.x;
     Kept kept{~0ull, 0, 0, false, false};
     count_cells(row, h);
@@ -721,7 +952,8 @@ __device__ __noinline__ Kept find_borders(Row<T> row, Here h, bool by_count, boo
         const bool counting = round == 0, all_wanted = !counting && kept.mass == 0;
         uint64_t want = counting ? (uint64_t)top_k : all_wanted ? 0 : top_p_goal(kept.mass, top_p);
         find_cell(h, counting, want, top_p, limit, V);
-        int b = (int)sh.border.bin, moved = 0;
+        int b = (int)sh.border.bin, moved = 0, jumps = sh.border.count == kNone ? 2 : 0;
+        uint64_t estimate = sh.border.mass_above;
         const uint64_t cells_before = sh.border.count_above;
         bool all_up_to = cells_before + sh.border.count <= kList, settled = counting;
         uint64_t above, cell_mass, n_cell;
@@ -741,13 +973,22 @@ __device__ __noinline__ Kept find_borders(Row<T> row, Here h, bool by_count, boo
             if (all_up_to && n_cell > kList) {
                 all_up_to = false;
             } else {
-                // The cells' mean weights may have missed the cell.  (A sum's rounding must not send it to and fro: between
-                // two cells it is the end of the first.)
+                // The weights at the grid points may have missed the cell, most often by what heavy tokens' weights are
+                // off: the same for its neighbours, so the next try takes that off.  Then step by step.  (A sum's
+                // rounding must not send it to and fro: between two cells it is the end of the first.)
                 const int next = settled || (want > above && want <= above + cell_mass) ? 0 : want <= above ? -1 : 1;
                 settled |= moved != 0 && next == -moved;
                 if (next == 0 || (settled && next > 0) || b + next < 0 || b + next > limit) break;
-                moved = next;
-                b += next;
+                int there = b;
+                if (jumps < 2 && !settled) {
+                    ++jumps;
+                    find_cell(h, false, (uint64_t)max((long long)(estimate + want - above), 1ll), top_p, limit, V);
+                    there = (int)sh.border.bin;
+                    estimate = sh.border.mass_above;
+                    if (sh.border.count == kNone) jumps = 2;
+                }
+                moved = there != b ? 0 : next;
+                b = there != b ? there : b + next;
             }
             __syncthreads();
             if (tid == 0) sh.n_own = 0;
@@ -761,47 +1002,19 @@ __device__ __noinline__ Kept find_borders(Row<T> row, Here h, bool by_count, boo
             base_mass = sh.border.mass_above;
             base_count = sh.border.count_above;
         }
-        const int n = join_lists(h);
-        const uint64_t mine = sh.all[tid], w = sh.own[tid], upto = base_mass + block_scan(w);
-        const bool real = tid < n;
-        if (counting && real && base_count + tid + 1 == want) {
-            sh.cut[0] = mine;
-            sh.cut_mass[0] = upto;
-        }
-        __syncthreads();
-        bool found = true;
-        if (counting) {
-            kept.last = sh.cut[0];
-            kept.mass = sh.cut_mass[0];
-            limit = b;
-            if (by_mass) {
-                want = top_p_goal(kept.mass, top_p);
-                found = want > base_mass;  // else the border of top-p is before this list
-            }
-        }
-        if (by_mass && found) {
-            const bool here = real && upto >= want && upto - w < want, any = __syncthreads_or(here);
-            if (here || (!any && tid == max(n - 1, 0))) {
-                sh.cut[1] = mine;
-                sh.cut_mass[1] = upto;
-            }
-            __syncthreads();
-            kept.last = sh.cut[1];
-            kept.mass = sh.cut_mass[1];
-            round = 1;
-        }
-        kept.n = n;
+        const int n = join_lists(h, [&](float x) { return weight_of(grid, x); });
+        const bool found = cut_list(kept, n, counting, want, by_mass, top_p, base_mass, base_count);
+        if (counting) limit = b;
+        if (by_mass && found) round = 1;
         kept.complete = all_up_to && found;
         kept.runs = !split && !all_up_to && found;
     }
     return kept;
 }
 
-// The lowest key whose weight stays by min-p.
-__device__ __noinline__ uint32_t find_min_key(float min_p, uint64_t most, uint32_t top_key) {
+// The lowest key whose weight is enough.
+__device__ __noinline__ uint32_t find_min_key(uint64_t least, uint32_t top_key) {
     const Grid grid = shared().grid;
-    bool cut = false;
-    const uint64_t least = min_p < 1.f ? max((uint64_t)1, fraction_of(most, min_p, cut) + cut) : most;
     return first_key(key_of(-INFINITY), top_key, threadIdx.x & 31, [&](uint32_t key) { return weight_of(grid, logit_of(key)) >= least; });
 }
 
@@ -816,8 +1029,9 @@ __device__ __noinline__ uint64_t sum_runs(Row<T> row, Here h, Kept kept, int run
         // before the border's cell they are known; the list's tokens are added, run by run and CTA by CTA
         uint64_t cta = 0;
         for (int base = 0; base < kept.n; base += 32) {
-            const uint64_t place = sh.all[base + lane], w = place <= kept.last ? sh.own[base + lane] : 0;
-            const int of = (int)((uint32_t)place & 0x7fffffffu) / run;
+            const Entry e = sh.list[base + lane];
+            const uint64_t w = e.place <= kept.last ? e.weight : 0;
+            const int of = (int)((uint32_t)e.place & 0x7fffffffu) / run;
             if (of == h.rank * kWarps + warp) own += w;
             if (of / kWarps == warp) cta += w;
         }
@@ -829,11 +1043,24 @@ __device__ __noinline__ uint64_t sum_runs(Row<T> row, Here h, Kept kept, int run
         __syncthreads();
     } else {
         Sum s;
-        row.each(h.begin, h.stop, lane, [&](float x, int p) {
-            if (place_of(key_of(x), p) > kept.last) return;
-            float y, part;
-            s.whole += sh.table[grid.cell(x, y, part)];
-            s.rest += grid.rest(y, part);
+        constexpr int N = kVec<T>;
+        const bool all = kept.last == ~0ull;
+        row.units(h.begin, h.stop, lane, [&](const float (&x)[N], int p) {
+            bool stays[N], any = false;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                stays[i] = all || place_of(key_of(x[i]), p + i) <= kept.last;
+                any |= stays[i];
+            }
+            if (!any) return;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                float y, part;
+                const uint64_t w = sh.table[grid.cell(x[i], y, part)];
+                const float rest = grid.rest(y, part);
+                s.whole += stays[i] ? w : 0;
+                s.rest += stays[i] ? rest : 0.f;
+            }
         });
         own = warp_sum(s.total());
         __syncthreads();
@@ -857,16 +1084,13 @@ struct Drawn {
 // The draw from a list that has all that stays.
 __device__ __noinline__ Drawn draw_from_list(Kept kept, float u) {
     Shared &sh = shared();
-    const Grid grid = sh.grid;
     const int tid = threadIdx.x;
-    const uint64_t place = sh.all[tid];
-    const bool real = tid < kept.n && place <= kept.last;
-    const int n = __syncthreads_count(real);
-    const uint64_t by_index = sort(real ? place << 32 | place >> 32 : ~0ull, n);
-    const uint64_t w = tid < n ? weight_of(grid, logit_of(~(uint32_t)by_index)) : 0;
-    const uint64_t upto = block_scan(w), sum = over_warps(sh.warp_mass), goal = draw_goal(sum, u);
-    const bool here = w > 0 && upto > goal && upto - w <= goal;
-    return Drawn{here ? (int)(by_index >> 32) : -1, __fdiv_rn((float)w, (float)sum)};
+    const uint64_t before = rank_list<true>(kept.n, kept.last).place;
+    const Entry mine = sh.list[tid];
+    const uint64_t w = tid < kept.n && mine.place <= kept.last ? mine.weight : 0;
+    block_scan(w);
+    const uint64_t sum = over_warps(sh.warp_mass), goal = draw_goal(sum, u);
+    return Drawn{w > 0 && before <= goal && goal - before < w ? (int)(uint32_t)mine.place : -1, __fdiv_rn((float)w, (float)sum)};
 }
 
 // The draw from the runs: the CTA and run that hold its place, a thread's piece of the run, an entry.
@@ -1015,17 +1239,40 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         return;
     }
     const float top = fminf(logit_of(top_key), 3.402823466e38f);  // (+inf counts as the largest number)
-    make_grid(top, temperature, a.drop);
-    const uint64_t most = weight_of(sh.grid, top);
     const bool by_count = top_k > 0 && top_k < a.V, by_mass = top_p < 1.f;
     Kept kept{~0ull, 0, 0, false, false};
-    if (by_count || by_mass) kept = find_borders(row, h, by_count, by_mass, top_k, top_p, a.V, top_key);
+    uint64_t most;  // the largest weight
+    if (by_count && top_k <= kFew && find_few(kept, row, h, top_k, by_mass, top_p, top, temperature, a.drop)) {
+        most = 1ull << (kUnit - a.drop);
+    } else {
+        if (tid == 0) sh.grid = make_grid(top, temperature, a.drop);
+        make_table(temperature, a.drop);
+        most = weight_of(sh.grid, top);
+        if (by_count || by_mass) kept = find_borders(row, h, by_count, by_mass, top_k, top_p, a.V, top_key);
+    }
     if (min_p > 0.f) {
-        const uint64_t place = place_of(find_min_key(min_p, most, top_key), 0x7fffffff);
-        if (place < kept.last) {
-            kept.last = place;
-            kept.mass = 0;
-            kept.runs = false;
+        bool cut = false;
+        const uint64_t least = min_p < 1.f ? max((uint64_t)1, fraction_of(most, min_p, cut) + cut) : most;
+        if (kept.complete) {
+            // tokens with enough weight come first in the order
+            const Entry mine = sh.list[tid];
+            const bool stays = tid < kept.n && mine.place <= kept.last && mine.weight >= least;
+            const int n = __syncthreads_count(stays);
+            const Entry before = rank_list<false>(kept.n, 0);
+            if (stays && before.weight + 1 == n) {
+                sh.cut[0] = mine.place;
+                sh.cut_mass[0] = before.place + mine.weight;
+            }
+            __syncthreads();
+            kept.last = sh.cut[0];
+            kept.mass = sh.cut_mass[0];
+        } else {
+            const uint64_t place = place_of(find_min_key(least, top_key), 0x7fffffff);
+            if (place < kept.last) {
+                kept.last = place;
+                kept.mass = 0;
+                kept.runs = false;
+            }
         }
     }
     if constexpr (OUT == kDraw) {
@@ -1038,14 +1285,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         }
         if (drawn.p >= 0) give(drawn.p, drawn.probability);
     } else {
-        if (kept.mass == 0) {
-            if (kept.complete) {
-                block_scan(tid < kept.n && sh.all[tid] <= kept.last ? sh.own[tid] : 0);
-                kept.mass = over_warps(sh.warp_mass);
-            } else {
-                kept.mass = sum_runs(row, h, kept, a.run);
-            }
-        }
+        if (kept.mass == 0) kept.mass = sum_runs(row, h, kept, a.run);
         // probabilities in fp32: 2^t with t = (x - top) / T log2(e) as a pair
         const float over = __fdiv_rn((float)most, (float)kept.mass);
         const float2 scale = scale_of(temperature);
@@ -1063,6 +1303,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 
 template <typename T, int OUT>
 cudaError_t launch_sample(const SampleArgs &a, int R, cudaStream_t stream) {
+    static std::atomic<bool> configured[64];  // per device: the shared-memory attribute is set
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!configured[dev].load(std::memory_order_acquire)) {
+        const cudaError_t e = cudaFuncSetAttribute(sample_kernel<T, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared));
+        if (e != cudaSuccess) return e;
+        configured[dev].store(true, std::memory_order_release);
+    }
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1079,7 +1327,13 @@ cudaError_t launch_sample(const SampleArgs &a, int R, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, sample_kernel<T, OUT>, a);
 }
 
-// The checks and the plan that both calls share; a.V = 0 where there is nothing to do.
+// The status of a launch.
+pa_status launched(const char *fn, cudaError_t err) {
+    const pa_status st = check_launch(fn);
+    return st != PA_OK || err == cudaSuccess ? st : fail(PA_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(err));
+}
+
+// The checks and the plan that both calls share.
 pa_status plan_sample(const char *fn, SampleArgs &a, const void *logits, int64_t logit_stride, int logit_dtype, const float *temperature,
                       const int32_t *top_k, const float *top_p, const float *min_p, int R, int V, int *err_flag) {
     if (R < 0) return fail(PA_ERR_INVALID_ARG, "%s: R = %d is negative", fn, R);
@@ -1128,9 +1382,9 @@ pa_status pa_sample_tokens(int32_t *tokens_out, float *probs_out, const void *lo
     a.tokens = tokens_out;
     a.token_probs = probs_out;
     a.u = uniforms;
-    logit_dtype == PA_PROB_F32 ? launch_sample<float, kDraw>(a, R, (cudaStream_t)stream)
-                               : launch_sample<uint16_t, kDraw>(a, R, (cudaStream_t)stream);
-    return check_launch(fn);
+    const cudaError_t err = logit_dtype == PA_PROB_F32 ? launch_sample<float, kDraw>(a, R, (cudaStream_t)stream)
+                                                       : launch_sample<uint16_t, kDraw>(a, R, (cudaStream_t)stream);
+    return launched(fn, err);
 }
 
 pa_status pa_sampling_probs(void *probs_out, int64_t prob_stride, int prob_dtype, const void *logits, int64_t logit_stride,
@@ -1154,11 +1408,11 @@ pa_status pa_sampling_probs(void *probs_out, int64_t prob_stride, int prob_dtype
     a.probs = probs_out;
     a.p_stride = prob_stride;
     const cudaStream_t s = (cudaStream_t)stream;
-    if (logit_dtype == PA_PROB_F32)
-        prob_dtype == PA_PROB_F32 ? launch_sample<float, kProbsF32>(a, R, s) : launch_sample<float, kProbsBf16>(a, R, s);
-    else
-        prob_dtype == PA_PROB_F32 ? launch_sample<uint16_t, kProbsF32>(a, R, s) : launch_sample<uint16_t, kProbsBf16>(a, R, s);
-    return check_launch(fn);
+    const cudaError_t err =
+        logit_dtype == PA_PROB_F32
+            ? (prob_dtype == PA_PROB_F32 ? launch_sample<float, kProbsF32>(a, R, s) : launch_sample<float, kProbsBf16>(a, R, s))
+            : (prob_dtype == PA_PROB_F32 ? launch_sample<uint16_t, kProbsF32>(a, R, s) : launch_sample<uint16_t, kProbsBf16>(a, R, s));
+    return launched(fn, err);
 }
 
 }  // extern "C"
