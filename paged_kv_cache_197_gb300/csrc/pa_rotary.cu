@@ -219,9 +219,11 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
             for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(gmask, s, o);
             return s * (1.f / D);
         };
-        float mean = squares();
-        if (!(mean <= 3.402823466e38f)) {  // beyond fp32: the row 2^-80 times as large (eps is nothing to it)
-            constexpr float k = 8.2718061255302767e-25f;
+        // Squares keep their bits while the mean with eps lies within 2^-100 .. 2^128 (what is lost below 2^-149 is nothing to it).
+        // Beyond, the row is taken 2^80 times smaller or larger, and eps, which stands beside its squares, 2^160 times.
+        float mean = squares(), eps = a.eps;
+        if (!(mean + eps >= 7.8886091e-31f && mean + eps <= 3.402823466e38f)) {
+            const float k = mean + eps < 1.f ? 1.2089258196146292e24f : 8.2718061255302767e-25f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 x[e] *= k;
@@ -229,8 +231,9 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
             }
             for (int e = 0; e < (LAYOUT == 2 ? 16 : 0); ++e) part[e] *= k;
             mean = squares();
+            eps = eps * k * k;
         }
-        const float over = rsqrtf(mean + a.eps);
+        const float over = rsqrtf(mean + eps);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             x[e] *= over * w[e];
