@@ -1359,7 +1359,7 @@ pa_status plan_sample(const char *fn, SampleArgs &a, const void *logits, int64_t
     a.cluster = V > 4000 ? kMaxCluster : 1;
     const int runs = a.cluster * kWarps;
     a.run = (int)align_up((size_t)((V + 7 + runs - 1) / runs), 8);  // (a row may start up to 7 entries into its first unit)
-    while (((int64_t)V << (kUnit - a.drop)) > ((int64_t)1 << 62)) ++a.drop;
+    while (V > 1 << (62 - kUnit + a.drop)) ++a.drop;  // V weights of 1 sum to 2^62 at most
     return PA_OK;
 }
 
