@@ -40,6 +40,9 @@ constexpr int kList = 512;    // tokens that are listed (at most one a thread)
 constexpr int kFew = 64;      // top-k up to which its tokens are listed at once
 constexpr int kMaxima = 128;  // largest logits of equal parts of a row
 constexpr int kUnit = 44;     // a weight of 1 is 2^44
+// Bits of a weight that are summed in 32 bits: a CTA has up to 131200 entries (2^20 in 128 runs, rounded up to 8), so 14 are the most.
+// The rest is at most 1.01 * 2^16 with 32896 entries a CTA (2^18 a row), and half of that for twice as many: below 2^32 as well.
+constexpr int kLimb = 14;
 constexpr uint32_t kNone = 0xffffffffu;
 
 struct SampleArgs {
@@ -224,7 +227,7 @@ struct alignas(16) Border {
 struct alignas(16) Shared {
     uint64_t table[kCells];
     uint32_t cells[kCells];      // tokens in each
-    uint32_t hist[4][kSplit];    // of a cell that is split: counts, and sums of the weights' lowest 15 bits, the next 15 and the rest
+    uint32_t hist[4][kSplit];    // of a cell that is split: counts, and sums of the weights' lowest kLimb bits, the next kLimb and the rest
     uint64_t own[kList];         // places gathered here
     Entry list[kList];           // all CTAs'
     uint64_t before_mass[kThreads];
@@ -756,9 +759,10 @@ __device__ __noinline__ void split_cell(Row<T> row, Here h, int b, bool counting
             if (at < 0 || place_of(key, p) > last) return;
             const uint64_t w = weight_of(grid, x);
             atomicAdd(&sh.hist[0][at], 1u);
-            atomicAdd(&sh.hist[1][at], (uint32_t)w & 0x7fffu);
-            atomicAdd(&sh.hist[2][at], (uint32_t)(w >> 15) & 0x7fffu);
-            atomicAdd(&sh.hist[3][at], (uint32_t)(w >> 30));
+            constexpr uint32_t kLow = (1u << kLimb) - 1;
+            atomicAdd(&sh.hist[1][at], (uint32_t)w & kLow);
+            atomicAdd(&sh.hist[2][at], (uint32_t)(w >> kLimb) & kLow);
+            atomicAdd(&sh.hist[3][at], (uint32_t)(w >> 2 * kLimb));
         });
         meet(h.C);
         const int share = kSplit / h.C, mine = h.rank * share + tid;
@@ -766,8 +770,8 @@ __device__ __noinline__ void split_cell(Row<T> row, Here h, int b, bool counting
         if (tid < share)
             for (int c = 0; c < h.C; ++c) {
                 count += get(&sh.hist[0][mine], c, h.rank);
-                mass += get(&sh.hist[1][mine], c, h.rank) + ((uint64_t)get(&sh.hist[2][mine], c, h.rank) << 15) +
-                        ((uint64_t)get(&sh.hist[3][mine], c, h.rank) << 30);
+                mass += get(&sh.hist[1][mine], c, h.rank) + ((uint64_t)get(&sh.hist[2][mine], c, h.rank) << kLimb) +
+                        ((uint64_t)get(&sh.hist[3][mine], c, h.rank) << 2 * kLimb);
             }
         uint64_t before_mass = block_scan(mass) - mass;
         const uint64_t sum_mass = over_warps(sh.warp_mass);
