@@ -1258,17 +1258,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         bool cut = false;
         const uint64_t least = min_p < 1.f ? max((uint64_t)1, fraction_of(most, min_p, cut) + cut) : most;
         if (kept.complete) {
-            // tokens with enough weight come first in the order
+            // Tokens with enough weight come first in the order, but for the roundings of two weights beside `least`: what stays ends
+            // with the last of them.
             const Entry mine = sh.list[tid];
             const bool stays = tid < kept.n && mine.place <= kept.last && mine.weight >= least;
-            const int n = __syncthreads_count(stays);
-            const Entry before = rank_list<false>(kept.n, 0);
-            if (stays && before.weight + 1 == n) {
-                sh.cut[0] = mine.place;
-                sh.cut_mass[0] = before.place + mine.weight;
-            }
+            __syncthreads();  // the cut has been read by all
+            if (tid == 0) sh.cut[0] = 0;
+            const Entry before = rank_list<false>(kept.n, 0);  // (its barriers part the line above from the next)
+            if (stays) atomicMax(reinterpret_cast<unsigned long long *>(&sh.cut[0]), (unsigned long long)mine.place);
             __syncthreads();
             kept.last = sh.cut[0];
+            if (stays && mine.place == kept.last) sh.cut_mass[0] = before.place + mine.weight;
+            __syncthreads();
             kept.mass = sh.cut_mass[0];
         } else {
             const uint64_t place = place_of(find_min_key(least, top_key), 0x7fffffff);
