@@ -366,11 +366,12 @@ __device__ __forceinline__ uint64_t weight_of(const Grid &grid, float x) {
 
 // The same without a table, to 2^-35: the exponent as a pair of fp32, then in 64 bits.
 __device__ __forceinline__ uint64_t weight_of(float2 scale, float top, int drop, float x) {
-    x = fminf(fmaxf(x, -INFINITY), top);
+    if (x == top) return 1ull << (kUnit - drop);
+    x = fmaxf(x, -INFINITY);
     const float d = __fsub_rn(x, top), b = __fsub_rn(d, x);
     const float e = __fsub_rn(__fsub_rn(x, __fsub_rn(d, b)), __fadd_rn(top, b));
     const float t = __fmul_rn(d, scale.x);
-    if (!(t > -62.f)) return 0;
+    if (!(t > -62.f)) return 0;  // (-inf beside an infinity)
     const float low = __fmaf_rn(e, scale.x, __fmaf_rn(d, scale.y, __fmaf_rn(d, scale.x, -t)));
     const long long turns = __float2ll_rn(-t * 72057594037927936.f) - __float2ll_rn(low * 72057594037927936.f);
     const Power p = power((uint64_t)max(turns, 0ll));
@@ -535,8 +536,13 @@ __device__ __noinline__ void make_table(float temperature, int drop) {
 __device__ __forceinline__ Grid make_grid(float top, float temperature, int drop) {
     const float t = fminf(fmaxf(temperature, 8.6736174e-19f), 1.2089258e24f), step = step_of(temperature);
     Grid g;
-    g.base = fabsf(top) > step * 1048576.f ? top : 0.f;
-    g.high = __fsub_rn(top, g.base);
+    if (top < INFINITY) {
+        g.base = fabsf(top) > step * 1048576.f ? top : 0.f;
+        g.high = __fsub_rn(top, g.base);
+    } else {  // beside an infinity all numbers have weight 0: they are cut to the last cell, infinities to the first
+        g.base = 3.402823466e38f;
+        g.high = step * (kCells - 1);
+    }
     g.magic = step * 12582912.f;
     const float s = __fadd_rn(g.high, g.magic);
     g.zero = __float_as_int(s);
@@ -1242,7 +1248,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             give(first, 1.f);
         return;
     }
-    const float top = fminf(logit_of(top_key), 3.402823466e38f);  // (+inf counts as the largest number)
+    const float top = logit_of(top_key);
     const bool by_count = top_k > 0 && top_k < a.V, by_mass = top_p < 1.f;
     Kept kept{~0ull, 0, 0, false, false};
     uint64_t most;  // the largest weight
@@ -1296,12 +1302,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         const float2 scale = scale_of(temperature);
         write_row<T, OUT>(a, row, h, r, [&](float x, int p) {
             if (place_of(key_of(x), p) > kept.last) return 0.f;
-            x = fminf(fmaxf(x, -INFINITY), top);
+            const bool largest = x == top;
+            x = fmaxf(x, -INFINITY);
             const float d = __fsub_rn(x, top), b = __fsub_rn(d, x);
             const float e = __fsub_rn(__fsub_rn(x, __fsub_rn(d, b)), __fadd_rn(top, b));
             const float t = __fmul_rn(d, scale.x);
             const float low = __fmaf_rn(e, scale.x, __fmaf_rn(d, scale.y, __fmaf_rn(d, scale.x, -t)));
-            return d == 0.f ? over : t >= -200.f ? exp2f(t) * __fmaf_rn(low, 0.693147181f, 1.f) * over : 0.f;
+            return largest ? over : t >= -200.f ? exp2f(t) * __fmaf_rn(low, 0.693147181f, 1.f) * over : 0.f;
         });
     }
 }
