@@ -388,11 +388,13 @@ struct Here {
     int C, rank, begin, stop;
 };
 
+// (Both halves of a cluster's barrier take whole warps: lanes that parted before one meet first.)
 __device__ __forceinline__ void cluster_arrive(int C) {
     __syncwarp();
     if (C > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait(int C) {
+    __syncwarp();
     if (C > 1)
         asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     else
