@@ -221,7 +221,7 @@ struct alignas(16) Entry {  // of the list
     uint64_t place, weight;
 };
 struct alignas(16) Border {
-    uint64_t mass_above, count_above, bin, count;
+    uint64_t mass_above, count_above, bin, count, mass, unused;
 };
 
 struct alignas(16) Shared {
@@ -594,11 +594,10 @@ __device__ __noinline__ void count_cells(Row<T> row, Here h) {
     meet(h.C);
 }
 
-// The cell of a border, left in `border` with the tokens before it and in it: the first whose tokens (counting), or whose tokens'
-// weights at their grid points, reach `want` together with those before; want 0: top_p of all weights.  It is cut to
-// `limit`, whose own numbers are not known then (kNone), but for the last cell's.  The first warp narrows it down to a
-// group, and among the group's cells; two of them a lane.
-__device__ __noinline__ void find_cell(Here h, bool counting, uint64_t want, float top_p, int limit, int V) {
+// The cell of a border, left in `border` with the tokens before it and in it and their weights at their grid points: the first
+// whose tokens (counting), or whose tokens' weights at their grid points, reach `want` together with those before; want 0: top_p of
+// all weights.  It is cut to low .. high.  The first warp narrows it down to a group, and among the group's cells; two of them a lane.
+__device__ __noinline__ void find_cell(Here h, bool counting, uint64_t want, float top_p, int low, int high, int V) {
     Shared &sh = shared();
     const int lane = threadIdx.x & 31;
     if (threadIdx.x < 32) {
@@ -613,46 +612,41 @@ __device__ __noinline__ void find_cell(Here h, bool counting, uint64_t want, flo
         uint64_t upto_mass = warp_scan(mass[0] + mass[1], lane), upto_count = warp_scan(count[0] + count[1], lane);
         const uint64_t all_mass = __shfl_sync(0xffffffffu, upto_mass, 31), all_count = __shfl_sync(0xffffffffu, upto_count, 31);
         const uint64_t goal = want ? want : top_p_goal(all_mass, top_p);
-        // the lane and which of its two, and what comes before
-        uint64_t before_mass = 0, before_count = 0;
-        auto pick = [&](int &of, uint64_t &n) {  // false: none
+        auto first = [&] {  // of the 64 that reaches the goal; 64: none
             const uint64_t upto = counting ? upto_count : upto_mass, second = counting ? count[1] : mass[1];
             const unsigned yes = __ballot_sync(0xffffffffu, upto >= goal);
-            if (!yes) return false;
-            const int at = __ffs(yes) - 1;
-            const bool late = __shfl_sync(0xffffffffu, (int)(upto - second < goal), at);
-            const uint64_t m = upto_mass - mass[1] - (late ? 0 : mass[0]), c = upto_count - count[1] - (late ? 0 : count[0]);
-            before_mass = __shfl_sync(0xffffffffu, m, at);
-            before_count = __shfl_sync(0xffffffffu, c, at);
-            n = __shfl_sync(0xffffffffu, late ? count[1] : count[0], at);
-            of = 2 * at + late;
-            return true;
+            const int at = max(__ffs(yes) - 1, 0), late = __shfl_sync(0xffffffffu, (int)(upto - second < goal), at);
+            return yes ? 2 * at + late : 64;
         };
-        Border found{0, kNone, (uint64_t)limit, kNone};
-        int group = 0, of = 0;
-        uint64_t n = 0;
-        if (pick(group, n)) {
-            uint64_t both[kMaxCluster];  // two cells' tokens
+        uint64_t before_mass = 0, before_count = 0, in_mass = 0, in_count = 0;
+        auto look = [&](int of) {  // at one of the 64: what comes before it, and what is in it
+            const bool late = of & 1;
+            const uint64_t m = upto_mass - mass[1] - (late ? 0 : mass[0]), c = upto_count - count[1] - (late ? 0 : count[0]);
+            before_mass = __shfl_sync(0xffffffffu, m, of / 2);
+            before_count = __shfl_sync(0xffffffffu, c, of / 2);
+            in_mass = __shfl_sync(0xffffffffu, late ? mass[1] : mass[0], of / 2);
+            in_count = __shfl_sync(0xffffffffu, late ? count[1] : count[0], of / 2);
+        };
+        const int group = min(max(first(), low / 64), high / 64);
+        look(group);
+        uint64_t both[kMaxCluster];  // two cells' tokens
 #pragma unroll
-            for (int c = 0; c < kMaxCluster; ++c)
-                both[c] = c < h.C ? get(reinterpret_cast<const uint64_t *>(&sh.cells[64 * group + 2 * lane]), c, h.rank) : 0;
-            count[0] = count[1] = 0;
+        for (int c = 0; c < kMaxCluster; ++c)
+            both[c] = c < h.C ? get(reinterpret_cast<const uint64_t *>(&sh.cells[64 * group + 2 * lane]), c, h.rank) : 0;
+        count[0] = count[1] = 0;
 #pragma unroll
-            for (int c = 0; c < kMaxCluster; ++c) {
-                count[0] += (uint32_t)both[c];
-                count[1] += both[c] >> 32;
-            }
-            mass[0] = count[0] * sh.table[64 * group + 2 * lane];
-            mass[1] = count[1] * sh.table[64 * group + 2 * lane + 1];
-            upto_mass = before_mass + warp_scan(mass[0] + mass[1], lane);
-            upto_count = before_count + warp_scan(count[0] + count[1], lane);
-            if (pick(of, n) && 64 * group + of < limit) found = Border{before_mass, before_count, (uint64_t)(64 * group + of), n};
+        for (int c = 0; c < kMaxCluster; ++c) {
+            count[0] += (uint32_t)both[c];
+            count[1] += both[c] >> 32;
         }
-        if (found.bin == kCells - 1) {  // beyond all weights
-            found.count_above = all_count;
-            found.count = V - all_count;
-        }
-        if (lane == 0) sh.border = found;
+        mass[0] = count[0] * sh.table[64 * group + 2 * lane];
+        mass[1] = count[1] * sh.table[64 * group + 2 * lane + 1];
+        upto_mass = before_mass + warp_scan(mass[0] + mass[1], lane);
+        upto_count = before_count + warp_scan(count[0] + count[1], lane);
+        const int cell = min(max(64 * group + first(), low), high);
+        look(cell & 63);
+        if (cell == kCells - 1) in_count = V - all_count;  // beyond all weights
+        if (lane == 0) sh.border = Border{before_mass, before_count, (uint64_t)cell, in_count, in_mass, 0};
     }
     __syncthreads();
 }
@@ -732,6 +726,12 @@ __device__ __noinline__ void sum_and_gather(Row<T> row, Here h, int b, bool all_
     exchange(h, kCellBorder, Part{over_warps(sh.run_mass), over_warps(sh.before_mass), over_warps(sh.warp_mass), over_warps(sh.warp_count)});
 }
 
+// The lowest key of the cells up to `b`.
+__device__ __noinline__ uint32_t lowest_key(int b, uint32_t top_key) {
+    const Grid grid = shared().grid;
+    return first_key(key_of(-INFINITY), top_key, threadIdx.x & 31, [&](uint32_t key) { return grid.cell(logit_of(key)) <= b; });
+}
+
 // A cell of more than kList tokens, split on over their keys, and over the indices of equal keys, until a bin of the border has
 // no more: its tokens are gathered in own, what comes before them is left in border.
 template <typename T>
@@ -740,10 +740,7 @@ __device__ __noinline__ void split_cell(Row<T> row, Here h, int b, bool counting
     Shared &sh = shared();
     const Grid grid = sh.grid;
     const int tid = threadIdx.x, lane = tid & 31;
-    auto up_to = [&](int most) {
-        return first_key(key_of(-INFINITY), top_key, lane, [&](uint32_t key) { return grid.cell(logit_of(key)) <= most; });
-    };
-    uint32_t lo = up_to(b), hi = b > 0 ? up_to(b - 1) - 1 : top_key;
+    uint32_t lo = lowest_key(b, top_key), hi = b > 0 ? lowest_key(b - 1, top_key) - 1 : top_key;
     int first = row.pad, final = row.end - 1;
 #pragma unroll 1
     for (;;) {
@@ -754,7 +751,7 @@ __device__ __noinline__ void split_cell(Row<T> row, Here h, int b, bool counting
         for (int i = tid; i < 4 * kSplit; i += kThreads) (&sh.hist[0][0])[i] = 0;
         if (tid == 0) {
             sh.n_own = 0;
-            sh.border = Border{base_mass, base_count, kSplit - 1, 0};
+            sh.border = Border{base_mass, base_count, kSplit - 1, 0, 0, 0};
         }
         __syncthreads();
         auto bin_of = [&](uint32_t key, int p) {  // -1: none
@@ -963,14 +960,22 @@ __device__ __noinline__ Kept find_borders(Row<T> row, Here h, bool by_count, boo
     for (int round = by_count ? 0 : 1; round < (by_mass ? 2 : 1); ++round) {
         const bool counting = round == 0, all_wanted = !counting && kept.mass == 0;
         uint64_t want = counting ? (uint64_t)top_k : all_wanted ? 0 : top_p_goal(kept.mass, top_p);
-        find_cell(h, counting, want, top_p, limit, V);
-        int b = (int)sh.border.bin, moved = 0, jumps = sh.border.count == kNone ? 2 : 0;
-        uint64_t estimate = sh.border.mass_above;
-        const uint64_t cells_before = sh.border.count_above;
-        bool all_up_to = cells_before + sh.border.count <= kList, settled = counting;
-        uint64_t above, cell_mass, n_cell;
+        // Counts give the cell; weights at the grid points may miss it, most often by what heavy tokens' weights are off, which is
+        // the same for its neighbours: the next two tries take that off.  What is known of the border is kept, and from the third
+        // try on what is open is halved, so that 12 more end it whatever the weights.  One to three passes for rows of real
+        // and of peaked logits.
+        int before = -1, behind = limit + 1, tries = 0;  // cells before and behind the border
+        uint64_t low = 1, high = ~0ull;                  // sums at the grid points that lie between these
+        bool settled = counting, all_up_to;
+        find_cell(h, counting, want, top_p, 0, limit, V);
+        int b;
+        uint64_t above, cell_mass, n_cell, cells_before;
 #pragma unroll 1
         for (;;) {
+            b = (int)sh.border.bin;
+            cells_before = sh.border.count_above;
+            const uint64_t grid_before = sh.border.mass_above, grid_up_to = grid_before + sh.border.mass;
+            all_up_to = cells_before + sh.border.count <= kList;
             sum_and_gather(row, h, b, all_up_to, all_wanted, kept.last);
             uint64_t all_mass = 0;
             above = cell_mass = n_cell = 0;
@@ -982,29 +987,26 @@ __device__ __noinline__ Kept find_borders(Row<T> row, Here h, bool by_count, boo
                 all_mass += p.all_mass;
             }
             if (all_wanted) want = top_p_goal(all_mass, top_p);
-            if (all_up_to && n_cell > kList) {
-                all_up_to = false;
+            if (settled || (want > above && want <= above + cell_mass)) break;
+            uint64_t goal;
+            if (want > above) {
+                before = b;
+                low = grid_up_to + 1;
+                goal = grid_up_to + (want - above - cell_mass);
             } else {
-                // The weights at the grid points may have missed the cell, most often by what heavy tokens' weights are
-                // off: the same for its neighbours, so the next try takes that off.  Then step by step.  (A sum's
-                // rounding must not send it to and fro: between two cells it is the end of the first.)
-                const int next = settled || (want > above && want <= above + cell_mass) ? 0 : want <= above ? -1 : 1;
-                settled |= moved != 0 && next == -moved;
-                if (next == 0 || (settled && next > 0) || b + next < 0 || b + next > limit) break;
-                int there = b;
-                if (jumps < 2 && !settled) {
-                    ++jumps;
-                    find_cell(h, false, (uint64_t)max((long long)(estimate + want - above), 1ll), top_p, limit, V);
-                    there = (int)sh.border.bin;
-                    estimate = sh.border.mass_above;
-                    if (sh.border.count == kNone) jumps = 2;
-                }
-                moved = there != b ? 0 : next;
-                b = there != b ? there : b + next;
+                behind = b;
+                high = grid_before;
+                goal = grid_before - min(grid_before, above - want);
             }
+            // Nothing between the two: the end of the first (a sum's rounding must not send the border to and fro).
+            settled = behind - before <= 1 || low > high;
+            if (settled && before == b) break;
             __syncthreads();
             if (tid == 0) sh.n_own = 0;
             meet(h.C);
+            const int middle = settled ? max(before, 0) : (before + behind) / 2;
+            const bool guess = !settled && tries++ < 2;
+            find_cell(h, false, min(max(goal, low), high), top_p, guess ? before + 1 : middle, guess ? behind - 1 : middle, V);
         }
         if (!counting) want = min(max(want, above + 1), above + cell_mass);
         uint64_t base_mass = above, base_count = all_up_to ? 0 : cells_before;
@@ -1015,8 +1017,14 @@ __device__ __noinline__ Kept find_borders(Row<T> row, Here h, bool by_count, boo
             base_count = sh.border.count_above;
         }
         const int n = join_lists(h, [&](float x) { return weight_of(grid, x); });
+        if (counting) limit = min(b, kCells - 2);
+        if (n == 0) {  // the goal is beyond all weights by a sum's rounding: all tokens up to the cell
+            kept.last = min(kept.last, place_of(lowest_key(b, top_key), 0x7fffffff));
+            kept.mass = 0;
+            kept.complete = kept.runs = false;
+            break;
+        }
         const bool found = cut_list(kept, n, counting, want, by_mass, top_p, base_mass, base_count);
-        if (counting) limit = b;
         if (by_mass && found) round = 1;
         kept.complete = all_up_to && found;
         kept.runs = !split && !all_up_to && found;
