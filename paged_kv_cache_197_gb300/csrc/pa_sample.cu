@@ -38,6 +38,9 @@ constexpr int kGroups = 64;   // of 64 cells
 constexpr int kSplit = 512;   // bins of a cell that is split
 constexpr int kList = 512;    // tokens that are listed (at most one a thread)
 constexpr int kFew = 64;      // top-k up to which its tokens are listed at once
+// Tokens up to a border's cell that are listed instead of summed: a list ends the call without the sums of runs, but ranking it takes
+// as many comparisons as its square.  20 mixed rows of 50021 take 90 us with 512, 56 with 128 or 32; one row of 4000 25, 19 and 19.
+constexpr int kWhole = 128;
 constexpr int kMaxima = 128;  // largest logits of equal parts of a row
 constexpr int kUnit = 44;     // a weight of 1 is 2^44
 // Bits of a weight that are summed in 32 bits: a CTA has up to 131200 entries (2^20 in 128 runs, rounded up to 8), so 14 are the most.
@@ -436,7 +439,7 @@ __device__ __forceinline__ uint64_t over_warps(const uint64_t *of) {
 
 // What comes before each of the list's n tokens (thread t: entry t) in their order, or by index among the places up to
 // `last`: weights and tokens.  All threads share the n^2 comparisons: 64 tokens take a few hundred clocks, a third of what
-// sorting them takes, 512 as long.
+// sorting them takes, 300 about 10000 with two CTAs per SM, where sorting takes about the same.
 template <bool BY_INDEX>
 __device__ __noinline__ Entry rank_list(int n, uint64_t last) {
     Shared &sh = shared();
@@ -658,58 +661,32 @@ __device__ __noinline__ void sum_and_gather(Row<T> row, Here h, int b, bool all_
     Shared &sh = shared();
     const Grid grid = sh.grid;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    constexpr int N = kVec<T>;
     Sum before, all;
     uint64_t inside = 0;
     uint32_t n_inside = 0;
-    const int summed = all_up_to ? 0 : b, listed = all_up_to ? 0 : b;  // cells listed .. b are gathered
-    row.units(h.begin, h.stop, lane, [&](const float (&x)[N], int p) {
-        float y[N], part[N];
-        int k[N];
-        bool list = false, sum = all_wanted;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            k[i] = grid.cell(x[i], y[i], part[i]);
-            list |= k[i] >= listed && k[i] <= b;
-            sum |= k[i] < summed;
-        }
-        if (list) {
-#pragma unroll 1
-            for (int i = 0; i < N; ++i) {
-                float one = x[0];
-                int cell = k[0];
-#pragma unroll
-                for (int j = 1; j < N; ++j) {
-                    one = i == j ? x[j] : one;
-                    cell = i == j ? k[j] : cell;
-                }
-                const uint64_t place = place_of(key_of(one), p + i);
-                if (cell < listed || cell > b || place > last || p + i < row.pad || p + i >= row.end) continue;
+    const int summed = all_up_to ? 0 : b;
+    // (Entry by entry, each with its own branches: a vector's entries summed at once and listed in a loop of their own need more
+    // registers than there are, 64 rows with top-p 127 instead of 102 us.)
+    row.each(h.begin, h.stop, lane, [&](float x, int p) {
+        float y, part;
+        const int k = grid.cell(x, y, part);
+        if (k == b || (all_up_to && k < b)) {
+            const uint64_t place = place_of(key_of(x), p);
+            if (place <= last && p >= row.pad && p < row.end) {
                 const uint32_t at = atomicAdd(&sh.n_own, 1u);
                 if (at < kList) sh.own[at] = place;
-                inside += weight_of(grid, one);
+                inside += weight_of(grid, x);
                 ++n_inside;
             }
         }
-        if (sum) {
-            uint64_t w[N];
-            float rest[N];
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                w[i] = sh.table[k[i]];
-                rest[i] = grid.rest(y[i], part[i]);
-            }
-            if (all_wanted) {
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    all.whole += w[i];
-                    all.rest += rest[i];
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                before.whole += k[i] < summed ? w[i] : 0;
-                before.rest += k[i] < summed ? rest[i] : 0.f;
+        if (all_wanted || k < summed) {
+            const uint64_t w = sh.table[k];
+            const float rest = grid.rest(y, part);
+            all.whole += w;
+            all.rest += rest;
+            if (k < summed) {
+                before.whole += w;
+                before.rest += rest;
             }
         }
     });
@@ -975,7 +952,7 @@ __device__ __noinline__ Kept find_borders(Row<T> row, Here h, bool by_count, boo
             b = (int)sh.border.bin;
             cells_before = sh.border.count_above;
             const uint64_t grid_before = sh.border.mass_above, grid_up_to = grid_before + sh.border.mass;
-            all_up_to = cells_before + sh.border.count <= kList;
+            all_up_to = cells_before + sh.border.count <= kWhole;
             sum_and_gather(row, h, b, all_up_to, all_wanted, kept.last);
             uint64_t all_mass = 0;
             above = cell_mass = n_cell = 0;
