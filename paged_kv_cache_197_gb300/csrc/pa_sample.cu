@@ -113,7 +113,7 @@ struct Grid {
     float magic;       // 1.5 * 2^23 steps: a sum with it is rounded to a grid point
     float point;       // the grid point of the largest logit
     float c, over;     // log2(e) / T and 1 / T
-    float unit;        // kUnit - drop
+    float unit;        // 2^(kUnit - drop)
     int zero;          // bits of point + magic
 
     // The cell of a logit (0: the largest one's), what is left of it without the base, and its part of a cell.
@@ -126,13 +126,15 @@ struct Grid {
     __device__ __forceinline__ int cell(float x) const {
         return (zero - __float_as_int(__fadd_rn(fminf(fmaxf(__fsub_rn(x, base), low), high), magic))) & (kCells - 1);
     }
-    // What is to be added to the weight of a part's grid point: the hardware's exp2, to 2^-22, of the
-    // whole weight, in units, times 1 - exp(-part / T), |part / T| < 1 / 125.
+    // What is to be added to the weight of a part's grid point: the hardware's exp2, to 2^-22, of the whole weight, times
+    // 1 - exp(-part / T), |part / T| < 1 / 125: 2^-28.5 of the weight, and 2^-30.5 more for each octave that it is below 1, which the
+    // rounding of the exponent costs (2^-25 for the smallest, in which a unit is more).  The unit multiplies the power: in the
+    // exponent it would round all of them to 2^-19, 2^-26.5 of the weight.
     __device__ __forceinline__ float rest(float y, float part) const {
         float e;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmaf_rn(__fsub_rn(y, point), c, unit)));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(__fsub_rn(y, point), c)));
         const float z = part * over;
-        return e * (z * __fmaf_rn(z, __fmaf_rn(z, __fmaf_rn(z, -1.f / 24.f, 1.f / 6.f), -0.5f), 1.f));
+        return e * unit * (z * __fmaf_rn(z, __fmaf_rn(z, __fmaf_rn(z, -1.f / 24.f, 1.f / 6.f), -0.5f), 1.f));
     }
 };
 
@@ -555,7 +557,7 @@ __device__ __forceinline__ Grid make_grid(float top, float temperature, int drop
     g.low = g.point - step * (kCells - 1);
     g.c = scale_of(temperature).x;
     g.over = __fdiv_rn(1.f, t);
-    g.unit = (float)(kUnit - drop);
+    g.unit = (float)(1ull << (kUnit - drop));
     return g;
 }
 
