@@ -513,10 +513,10 @@ def _need(t, name: str, dtype: torch.dtype, ndim: int, index: int) -> int:
 def _heads(t, name: str, index: int) -> int:
     """Token stride, in elements, of a [T][heads][D] bf16 tensor with dense heads on device `index`."""
     if t.dtype is torch.bfloat16 and t.get_device() == index and t.dim() == 3:
-        _, heads, D = t.shape
+        T, heads, D = t.shape
         by_token, by_head, by_element = t.stride()
         if (by_element == 1 or D <= 1) and (by_head == D or heads <= 1):
-            return by_token if t.shape[0] > 1 else heads * D
+            return by_token if T > 1 else heads * D
         raise ValueError(f"{name}: the heads of a token must be dense")
     if t.is_contiguous():
         _cuda(t, name, torch.bfloat16, 3)
@@ -590,17 +590,18 @@ def _rotary_call(fn: str, norms, query_out, query, key, positions, table, interl
     """pa_rotary_and_cache (norms None) and pa_norm_rotary_and_cache (query_weight, key_weight, eps)."""
     dev = _first_device(query, "query")
     q_stride, k_stride = _heads(query, "query", dev), _heads(key, "key", dev)
-    T, Hq, D = query.shape
-    T2, Hkv, D2 = key.shape
+    q_shape, k_shape = query.shape, key.shape  # (each look at .shape makes a new one)
+    T, Hq, D = q_shape
+    T2, Hkv, D2 = k_shape
     qo = _need(query_out, "query_out", torch.bfloat16, 3, dev)
     pos = _need(positions, "positions", torch.int64, 1, dev)
     tab = _need(table, "table", torch.int64, 1, dev)
-    if query_out.shape != query.shape or T2 != T or D2 != D or positions.shape[0] != T:
+    if query_out.shape != q_shape or T2 != T or D2 != D or positions.numel() != T:
         raise ValueError(f"{fn}: shape mismatch")
     ko = None
     if key_out is not None:
         ko = _need(key_out, "key_out", torch.bfloat16, 3, dev)
-        if key_out.shape != key.shape:
+        if key_out.shape != k_shape:
             raise ValueError(f"{fn}: shape mismatch")
     v_stride, kv_dtype, bs, N = 0, PA_KV_BF16, 16, 1
     vp = kc = vc = ks = vs = slots = None
@@ -613,11 +614,15 @@ def _rotary_call(fn: str, norms, query_out, query, key, positions, table, interl
         slots = _need(slot_mapping, "slot_mapping", torch.int64, 1, dev)
         shape = k_cache.shape
         N, heads, bs, D2 = shape
-        if value.shape != key.shape or v_cache.shape != shape or heads != Hkv or D2 != D or slot_mapping.shape[0] != T:
+        if value.shape != k_shape or v_cache.shape != shape or heads != Hkv or D2 != D or slot_mapping.numel() != T:
             raise ValueError(f"{fn}: shape mismatch")
-        ks, vs = _scales(k_scale, v_scale, N, Hkv, bs, kv_dtype, dev, fn)
-    more = ()
-    if norms is not None:
+        if kv_dtype != PA_KV_BF16:
+            ks, vs = _scales(k_scale, v_scale, N, Hkv, bs, kv_dtype, dev, fn)
+    lib, more = load_library(), ()
+    if norms is None:
+        function = lib.pa_rotary_and_cache
+    else:
+        function = lib.pa_norm_rotary_and_cache
         weights = []
         for w, name in ((norms[0], "query_weight"), (norms[1], "key_weight")):
             weights.append(None if w is None else _need(w, name, torch.float32, 1, dev))
@@ -625,8 +630,8 @@ def _rotary_call(fn: str, norms, query_out, query, key, positions, table, interl
                 raise ValueError(f"{fn}: {name} must have head_dim entries")
         more = (*weights, norms[2])
     flag = None if err_flag is None else _need(err_flag, "err_flag", torch.int32, err_flag.dim(), dev)
-    _call(getattr(load_library(), fn), dev, stream, qo, ko, query.data_ptr(), q_stride, key.data_ptr(), k_stride, vp, v_stride,
-          kc, vc, ks, vs, kv_dtype, slots, pos, tab, 2 * table.shape[0], 1 if interleaved else 0, attention_factor, *more, T, Hq,
+    _call(function, dev, stream, qo, ko, query.data_ptr(), q_stride, key.data_ptr(), k_stride, vp, v_stride,
+          kc, vc, ks, vs, kv_dtype, slots, pos, tab, 2 * table.numel(), 1 if interleaved else 0, attention_factor, *more, T, Hq,
           Hkv, D, bs, N, flag)
 
 
