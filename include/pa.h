@@ -168,7 +168,8 @@ pa_status pa_quantize_kv_fp8(const pa_bf16 *key, const pa_bf16 *value, uint8_t *
  *                       key_stride / value_stride elements apart (multiples of 8, at least
  *                       Hkv * D).  Row t receives the cache's row at slot_mapping[t]: its bits
  *                       (bf16 cache), or code * scale rounded to bf16 (int8, fp8).  Must not
- *                       overlap the cache.
+ *                       overlap the cache, nor each other (rows of both may lie in turn, as
+ *                       slices of one tensor with one stride do).
  *   slot_mapping        [T] int64, device, as in pa_reshape_and_cache, but several tokens may
  *                       name one slot.  A token with a negative slot, or one >= N * bs
  *                       (PA_FLAG_SLOT_OUT_OF_RANGE), leaves its rows as they were.

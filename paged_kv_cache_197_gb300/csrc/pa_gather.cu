@@ -136,6 +136,13 @@ extern "C" pa_status pa_gather_cache(pa_bf16 *key_out, int64_t key_stride, pa_bf
     for (const void *c : {k_cache, v_cache})
         if (overlap(key_out, kb, c, cache) || overlap(value_out, vb, c, cache))
             return fail(PA_ERR_INVALID_ARG, "%s: an output overlaps the cache", fn);
+    // rows of keys and values may lie in turn (slices of one tensor), but not on one another
+    if (overlap(key_out, kb, value_out, vb)) {
+        const int64_t apart = (int64_t)((uintptr_t)value_out - (uintptr_t)key_out) / 2 % key_stride;  // of a key's row to the next value's
+        const int64_t gap = apart < 0 ? apart + key_stride : apart;
+        if (key_stride != value_stride || gap < row || key_stride - gap < row)
+            return fail(PA_ERR_INVALID_ARG, "%s: key_out overlaps value_out", fn);
+    }
     GatherArgs a{};
     a.key = key_out;
     a.value = value_out;

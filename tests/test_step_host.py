@@ -62,6 +62,27 @@ def test_gather_host_checks(lib):
     assert call(T=0) == pa.PA_OK
 
 
+@pytest.mark.skipif(torch.cuda.is_available(), reason="addresses that nothing lies at: only where nothing can be launched")
+def test_gather_outputs_on_one_another(lib):
+    """Rows of keys and values on one another are refused, at any distance and with strides that differ; rows in turn, slices of one
+    tensor, are not."""
+    import paged_kv_cache_197_gb300 as pa
+
+    def refused(apart, k_stride=1024, v_stride=1024, T=3, row=256):
+        """Values `apart` entries behind the keys."""
+        status = lib.pa_gather_cache(BIG, k_stride, BIG + 2 * apart, v_stride, 4 * BIG, 4 * BIG + (1 << 30), None, None, 0, 5 * BIG, T,
+                                     row // 128, 128, 16, 4, None, None)
+        assert status != pa.PA_OK
+        return status == pa.PA_ERR_INVALID_ARG and b"key_out overlaps value_out" in lib.pa_last_error_string()
+
+    for apart in (0, 8, 248, 1024, 2048, -1024, -8, -248, 1024 - 248, 2048 - 8, -1024 + 8):
+        assert refused(apart), apart
+    assert refused(512, v_stride=512) and refused(0, T=1) and refused(-16, T=1)
+    for apart in (256, 768, -256, 1024 + 256, 4096, -4096, 8192):
+        assert not refused(apart), apart
+    assert not refused(256, T=1) and not refused(8192, v_stride=512)
+
+
 def test_sampling_host_checks(lib):
     import paged_kv_cache_197_gb300 as pa
 
