@@ -21,10 +21,14 @@
  *   temperature 0: the first token with x_v = m alone (the filters change nothing).
  * Probabilities are the weights left over their sum.
  *
- * Weights are computed to about 2^-36 relative and held as whole numbers of 2^-45 (2^-(62 -
- * ceil(log2 V)) for V > 131072), so that their sums are exact, the same in any order, and
- * borders and draws come out as they do in 64 bits but for ties closer than that.  (A weight
- * below half of that unit is never drawn; pa_sampling_probs still writes its probability.)
+ * Temperatures from 2^-60 to 2^80 are used as they are, lower ones above 0 and higher ones as
+ * these.
+ *
+ * Weights are computed to about 2^-28 relative (2^-25 for the smallest) and held as whole
+ * numbers of 2^-44 (2^-(62 - ceil(log2 V)) for V > 2^18); their sums are off by about 2^-32
+ * relative (2^-27 for a million equal logits), the same from call to call.  So borders and
+ * draws come out as they do in 64 bits unless what they compare is closer than that.  (A weight
+ * below half of the unit is never drawn; pa_sampling_probs still writes its probability.)
  *
  * Conventions (streams, device-side checks, err_flag) as in pa.h, but logits and
  * probabilities need only be aligned to their type: rows of any length and stride.

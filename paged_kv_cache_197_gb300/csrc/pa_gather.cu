@@ -3,7 +3,8 @@
 // A lane takes eight entries of a row, 16 bytes of a bf16 cache or 8 of an 8-bit one, and
 // writes 16 bytes; a warp's lanes are neighbours in the token's rows, so what it writes is one
 // run of 512 bytes and what it reads whole rows of 64 to 256.  kBatch pieces are in flight in a
-// thread.  Bound by HBM beyond a few thousand tokens.
+// thread.  Bound by HBM beyond a few thousand tokens: 131072 tokens of 8 heads take 138 us from an fp8 cache (815 MB, 5.9 TB/s,
+// 0.88 of the measured copy rate), 139 from int8, 159 from bf16 (1.07 GB, 6.7 TB/s, the copy rate itself); 8192 from bf16 13.1.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>

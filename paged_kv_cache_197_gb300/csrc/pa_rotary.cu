@@ -98,7 +98,9 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], float scale) {
 //
 // NORM: query and key rows are normalised first, y = x / sqrt(mean x^2 + eps) w, in fp32.  A row lies in
 // its lanes' registers anyway, so the norm costs its sum of squares (log2 of the lanes' number shuffles)
-// and two products an element, but no byte more.
+// and two products an element, but no byte more.  It is not free: 8192 tokens of 64 + 8 + 8 heads take 69.0 us (57.7 without
+// norms, timed the same way; 68.1 without weights), 4.9 TB/s; fp8 75.6, int8 76.6, interleaved pairs 70.8, rot_dim 20 of 6000
+// tokens 89.2 (60.9).  The four rows in flight have their sums one after the other, and 17 weights a lane stay in registers.
 template <int D, int KV, int LAYOUT, bool NORM>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryArgs a) {
     constexpr int LPR = D / 16;                      // lanes per row

@@ -11,13 +11,19 @@
 //
 // Weights and sums.  A logit is a grid point and a part of a cell, x = x_k + y, exactly;
 // its weight exp(x / T) is exp(x_k / T), one of 4095 entries of a table in whole numbers of 2^-44
-// made once a row to 2^-35, plus a correction of at most a 125th of it, w (1 - exp(-y / T)), which
-// fp32 and the hardware's exp2 give to 2^-29 of w.  The whole numbers are summed exactly, the
-// corrections of a lane in fp32.  So a border or draw comes out as it does in 64 bits unless
-// two numbers agree to about 2^-29 of a single weight and 2^-36 of the sum.  (fp32 weights and sums
+// made once a row to 2^-33, plus a correction of at most a 125th of it, w (1 - exp(-y / T)), which
+// fp32 and the hardware's exp2 give to 2^-28.5 of w (2^-25 of the smallest).  The whole numbers are summed
+// exactly, the corrections of a lane in fp32: 2^-32 of the sum for rows of real and of peaked logits,
+// 2^-27 for 2^20 equal ones, whose corrections are all rounded alike.  So a border or draw comes out as it
+// does in 64 bits unless two numbers agree to that.  (fp32 weights and sums
 // carry 2^-21: beside a vocabulary's tens of thousands of small weights, one row in a few hundred would
 // be cut or drawn elsewhere.  Weights as pairs of fp32 took 45 instructions each, three times as many;
 // GB300 has two fp64 lanes per SM and clock.)
+//
+// Bounds: not the bytes.  A row is a chain of dependent steps (the largest logit, the cells, the border's cell, the sums and the cell's
+// tokens, their list, the draw or the row), each of them a pass of instructions or a meeting of the cluster.
+// 64 rows of 131072 with top-p take 102 us where their bytes take 5; temperature alone 42; 384 rows of
+// probabilities 557 (60).
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -37,7 +43,10 @@ constexpr int kCells = 4096;  // of the grid; the last one holds all logits whos
 constexpr int kGroups = 64;   // of 64 cells
 constexpr int kSplit = 512;   // bins of a cell that is split
 constexpr int kList = 512;    // tokens that are listed (at most one a thread)
-constexpr int kFew = 64;      // top-k up to which its tokens are listed at once
+// top-k up to which its tokens are listed at once, from the largest logits of the row's parts: half as many as there are parts, so
+// that few tokens are not below the k-th of these.  top-k 64 of 64 rows of 131072 takes 47 us so and 66 by the grid; 100 would take
+// 60 and 69, 128 101 and 69.
+constexpr int kFew = 64;
 // Tokens up to a border's cell that are listed instead of summed: a list ends the call without the sums of runs, but ranking it takes
 // as many comparisons as its square.  20 mixed rows of 50021 take 90 us with 512, 56 with 128 or 32; one row of 4000 25, 19 and 19.
 constexpr int kWhole = 128;
@@ -255,8 +264,8 @@ extern __shared__ __align__(16) char shared_bytes[];
 __device__ __forceinline__ Shared &shared() { return *reinterpret_cast<Shared *>(shared_bytes); }
 
 // ------------------------------------------------------------------- the cluster of a row
-// Another CTA's copy of a number in shared memory.  A CTA's own is never reached through the cluster's
-// window: those accesses are ordered by barriers of the cluster alone, and a cluster of one has none.
+// Another CTA's copy of a number in shared memory.  A CTA's own is never reached through the cluster's window: accesses through it
+// are ordered by the cluster's barriers, and a cluster of one has block barriers alone.
 __device__ __forceinline__ uint32_t remote(const void *p, int rank) {
     uint32_t a = (uint32_t)__cvta_generic_to_shared(p);
     asm volatile("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(a) : "r"(rank));
@@ -1357,6 +1366,9 @@ pa_status plan_sample(const char *fn, SampleArgs &a, const void *logits, int64_t
     a.min_p = min_p;
     a.err_flag = err_flag;
     a.V = V;
+    // One CTA or eight a row.  A single row gains from eight beyond 6000 entries (top-p, one and eight CTAs: 4000 entries 17.5 and 19.2
+    // us, 6000 19.1 and 19.2, 8000 20.6 and 19.5, 16000 25.0 and 19.6); batches of 64 rows do not up to 16000 at least (33.9 and 52.8),
+    // as their clusters no longer run at once.  The rule is for single rows; it does not look at R.
     a.cluster = V > 4000 ? kMaxCluster : 1;
     const int runs = a.cluster * kWarps;
     a.run = (int)align_up((size_t)((V + 7 + runs - 1) / runs), 8);  // (a row may start up to 7 entries into its first unit)
