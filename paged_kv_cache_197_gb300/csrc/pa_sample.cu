@@ -1083,10 +1083,10 @@ __device__ __noinline__ uint64_t sum_runs(Row<T> row, Here h, Kept kept, int run
     return sum;
 }
 
-// A token and its probability.
+// A token, and the sum that it was drawn from.
 struct Drawn {
     int p;  // padded index, -1: not in this thread
-    float probability;
+    uint64_t sum;
 };
 
 // The draw from a list that has all that stays.
@@ -1098,7 +1098,7 @@ __device__ __noinline__ Drawn draw_from_list(Kept kept, float u) {
     const uint64_t w = tid < kept.n && mine.place <= kept.last ? mine.weight : 0;
     block_scan(w);
     const uint64_t sum = over_warps(sh.warp_mass), goal = draw_goal(sum, u);
-    return Drawn{w > 0 && before <= goal && goal - before < w ? (int)(uint32_t)mine.place : -1, __fdiv_rn((float)w, (float)sum)};
+    return Drawn{w > 0 && before <= goal && goal - before < w ? (int)(uint32_t)mine.place : -1, sum};
 }
 
 // The draw from the runs: the CTA and run that hold its place, a thread's piece of the run, an entry.
@@ -1110,7 +1110,7 @@ __device__ __noinline__ Drawn draw_from_runs(Row<T> row, Here h, Kept kept, uint
     const uint64_t goal = draw_goal(sum, u);
     uint64_t before = 0;
     for (int c = 0; c < h.rank; ++c) before += sh.added[c];
-    Drawn drawn{-1, 0.f};
+    Drawn drawn{-1, sum};
     if (goal < before || goal - before >= sh.added[h.rank]) return drawn;
     const uint64_t upto = before + warp_scan(lane < kWarps ? sh.warp_mass[lane] : 0, lane);
     const int of = min(max(__ffs(__ballot_sync(0xffffffffu, upto > goal)) - 1, 0), kWarps - 1);
@@ -1130,15 +1130,33 @@ __device__ __noinline__ Drawn draw_from_runs(Row<T> row, Here h, Kept kept, uint
     if (place > left && place - piece <= left) {
         uint64_t at = place - piece;
         for (int p = b; p < e; ++p) {
-            const uint64_t w = entry_weight(p);
-            at += w;
+            at += entry_weight(p);
             if (at > left) {
-                drawn = Drawn{p, __fdiv_rn((float)w, (float)sum)};
+                drawn.p = p;
                 break;
             }
         }
     }
     return drawn;
+}
+
+// The probability of a logit that stays, in fp32: that of the largest one times 2^t, t = (x - top) / T log2(e) as a pair.  (Whole numbers
+// of 2^-44 would be too coarse for rare tokens.)
+struct Probability {
+    float2 scale;
+    float top, largest;
+    __device__ __forceinline__ float operator()(float x) const {
+        if (x == top) return largest;
+        x = fmaxf(x, -INFINITY);
+        const float d = __fsub_rn(x, top), b = __fsub_rn(d, x);
+        const float e = __fsub_rn(__fsub_rn(x, __fsub_rn(d, b)), __fadd_rn(top, b));
+        const float t = __fmul_rn(d, scale.x);
+        const float low = __fmaf_rn(e, scale.x, __fmaf_rn(d, scale.y, __fmaf_rn(d, scale.x, -t)));
+        return t >= -200.f ? exp2f(t) * __fmaf_rn(low, 0.693147181f, 1.f) * largest : 0.f;
+    }
+};
+__device__ __forceinline__ Probability probability_of(float temperature, float top, uint64_t most, uint64_t sum) {
+    return Probability{scale_of(temperature), top, __fdiv_rn((float)most, (float)sum)};
 }
 
 // ------------------------------------------------------------------------------ the kernel
@@ -1292,22 +1310,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         } else {
             drawn = draw_from_runs(row, h, kept, sum_runs(row, h, kept, a.run), a.u[r], a.run);
         }
-        if (drawn.p >= 0) give(drawn.p, drawn.probability);
+        if (drawn.p >= 0) give(drawn.p, probability_of(temperature, top, most, drawn.sum)(row.at(drawn.p)));
     } else {
         if (kept.mass == 0) kept.mass = sum_runs(row, h, kept, a.run);
-        // probabilities in fp32: 2^t with t = (x - top) / T log2(e) as a pair
-        const float over = __fdiv_rn((float)most, (float)kept.mass);
-        const float2 scale = scale_of(temperature);
-        write_row<T, OUT>(a, row, h, r, [&](float x, int p) {
-            if (place_of(key_of(x), p) > kept.last) return 0.f;
-            const bool largest = x == top;
-            x = fmaxf(x, -INFINITY);
-            const float d = __fsub_rn(x, top), b = __fsub_rn(d, x);
-            const float e = __fsub_rn(__fsub_rn(x, __fsub_rn(d, b)), __fadd_rn(top, b));
-            const float t = __fmul_rn(d, scale.x);
-            const float low = __fmaf_rn(e, scale.x, __fmaf_rn(d, scale.y, __fmaf_rn(d, scale.x, -t)));
-            return largest ? over : t >= -200.f ? exp2f(t) * __fmaf_rn(low, 0.693147181f, 1.f) * over : 0.f;
-        });
+        const Probability probability = probability_of(temperature, top, most, kept.mass);
+        write_row<T, OUT>(a, row, h, r, [&](float x, int p) { return place_of(key_of(x), p) > kept.last ? 0.f : probability(x); });
     }
 }
 
