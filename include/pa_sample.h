@@ -25,10 +25,12 @@
  * these.
  *
  * Weights are computed to about 2^-28 relative (2^-25 for the smallest) and held as whole
- * numbers of 2^-44 (2^-(62 - ceil(log2 V)) for V > 2^18); their sums are off by about 2^-32
- * relative (2^-27 for a million equal logits), the same from call to call.  So borders and
- * draws come out as they do in 64 bits unless what they compare is closer than that.  (A weight
- * below half of the unit is never drawn; pa_sampling_probs still writes its probability.)
+ * numbers of 2^-44 (2^-(62 - ceil(log2 V)) for V > 2^18).  Their sums are the same from call to
+ * call, and off by at most about 2^-28 of the sum and half a unit a token (2^-27 of the largest
+ * weight for V = 2^18, 2^-23 for 2^20; a row of all equal logits under a large one comes near
+ * that, ordinary rows stay at 2^-32).  Borders and draws come out as they do in 64 bits unless
+ * what they compare is closer than that.  (A weight below half of the unit is never drawn;
+ * pa_sampling_probs still writes its probability.)
  *
  * Conventions (streams, device-side checks, err_flag) as in pa.h, but logits and
  * probabilities need only be aligned to their type: rows of any length and stride.

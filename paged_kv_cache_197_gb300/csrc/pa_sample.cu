@@ -13,9 +13,10 @@
 // its weight exp(x / T) is exp(x_k / T), one of 4095 entries of a table in whole numbers of 2^-44
 // made once a row to 2^-33, plus a correction of at most a 125th of it, w (1 - exp(-y / T)), which
 // fp32 and the hardware's exp2 give to 2^-28.5 of w (2^-25 of the smallest).  The whole numbers are summed
-// exactly, the corrections of a lane in fp32: 2^-32 of the sum for rows of real and of peaked logits,
-// 2^-27 for 2^20 equal ones, whose corrections are all rounded alike.  So a border or draw comes out as it
-// does in 64 bits unless two numbers agree to that.  (fp32 weights and sums
+// exactly, the corrections of a lane in fp32: 2^-32 of the sum for rows of real and of peaked logits, 2^-28 where a few
+// tokens have most of it, and where a vocabulary's small weights are all equal their roundings to the unit
+// add up (V half units).  So a border or draw comes out as it does in 64 bits unless two numbers agree to that:
+// in 336000 rows of all kinds of logits and filters 79 did not, all of them so.  (fp32 weights and sums
 // carry 2^-21: beside a vocabulary's tens of thousands of small weights, one row in a few hundred would
 // be cut or drawn elsewhere.  Weights as pairs of fp32 took 45 instructions each, three times as many;
 // GB300 has two fp64 lanes per SM and clock.)
